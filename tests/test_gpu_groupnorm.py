@@ -1,0 +1,238 @@
+"""GPU parity of group norm with an activation against the float64 oracle.
+
+Tolerances, element by element.  The kernels work in float32 (u = 2^-24) with
+centred sums.  A mean of n values is off by at most (n / 64 + 64) u mean|x| with
+the tree sums used, call that e; then x - mean is off by e + u|x|, rstd by a
+relative (n / 64 + 64) u plus what e does to the variance (e rstd, squared), so
+xh is off by rstd (e + u |x|) + (n / 64 + 64) u |xh|, and z = w xh + b by |w|
+times that and a few u |z|.  Activations have slopes below 1.13.  The result is
+rounded once.  The gradients' bounds use the same errors of xh in each factor.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import ops as O
+from xlstm_mlstm_matrix_amd import binding as B
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}
+U = 2.0 ** -24
+
+SHAPES = [  # N, S, G, D
+    (1, 1, 1, 1), (2, 3, 4, 16), (1, 5, 3, 64), (3, 7, 8, 128), (2, 4, 2, 512), (1, 3, 2, 576), (2, 2, 1, 2048),
+    (1, 3, 2, 2056), (1, 2, 1, 5000), (2, 33, 32, 10), (1, 50, 3, 7), (2, 5, 4, 300), (1, 65, 5, 24), (2, 100, 6, 80),
+    (1, 1000, 2, 40), (5, 17, 16, 8), (1, 2, 3, 250),
+]
+
+
+def make(io, shape, seed=0, mean=0.5):
+    r = np.random.default_rng(77 + seed)
+    t = lambda *s: torch.from_numpy(r.normal(0, 1, s).astype(np.float32))
+    N, S, G, D = shape
+    return (t(*shape) + mean).to(DT[io]), t(*shape).to(DT[io]), 1 + 0.3 * t(G, D), 0.3 * t(G, D)
+
+
+def xh_error(x, m, r, over):
+    """xh, and the bound of its error (see above)."""
+    ax = (3,) if over == "token" else (1, 3)
+    n = x.shape[3] * (1 if over == "token" else x.shape[1])
+    c = (n / 64 + 64) * U
+    e = c * np.abs(x).mean(ax, keepdims=True)
+    xh = (x - m) * r
+    return xh, r * (e + U * np.abs(x)) + (c + (e * r) ** 2) * np.abs(xh)
+
+
+def compare(x, ref, tol, what):
+    x = x.detach().double().cpu().numpy()
+    assert x.shape == ref.shape and np.all(np.isfinite(x)), what
+    bad = (np.abs(x - ref) / (tol + 1e-30)).max()
+    print(f"[groupnorm] {what}: {bad:.3f} of the bound", flush=True)
+    assert bad <= 1.0, (what, bad)
+
+
+def run(io, shape, over, act, head_major=False, seed=0, mean=0.5, affine=True):
+    what = f"{io} {shape} {over} {act}"
+    x, dy, w, b = make(io, shape, seed, mean)
+    if not affine:
+        w = b = None
+    print(f"[groupnorm] {what}", flush=True)
+    lay = (lambda t: t.cuda().transpose(1, 2).contiguous().transpose(1, 2)) if head_major else (lambda t: t.cuda())
+    c = lambda t: None if t is None else t.cuda()
+    y, m, r = B.groupnorm_fwd(lay(x), c(w), c(b), act=act, over=over)
+    dx, dw, db = B.groupnorm_bwd(lay(x), lay(dy), m, r, c(w), c(b), act=act, over=over)
+    torch.cuda.synchronize()
+    ry, rm, rr = O.groupnorm_forward(x, w, b, 1e-5, act, over)
+    ax = (3,) if over == "token" else (1, 3)
+    X, DY = x.double().numpy(), dy.double().numpy()
+    M, R = np.expand_dims(rm, ax), np.expand_dims(rr, ax)
+    W = np.ones(shape[2:]) if w is None else w.double().numpy()
+    Bb = np.zeros(shape[2:]) if b is None else b.double().numpy()
+    xh, ex = xh_error(X, M, R, over)
+    ez = np.abs(W) * ex + 4 * U * (np.abs(W * xh) + np.abs(Bb))
+    h = HALF[io]
+    compare(y, ry, h * 1.01 * np.abs(ry) + 1.2 * ez + 16 * U * (1 + np.abs(ry)), what + " y")
+    n = shape[3] * (1 if over == "token" else shape[1])
+    c64 = (n / 64 + 64) * U
+    compare(m, rm, c64 * np.abs(X).mean(ax), what + " mean")
+    ee = c64 * np.abs(X).mean(ax)
+    compare(r, rr, rr * (c64 + (ee * rr) ** 2 + 4 * U), what + " rstd")
+    # gradients, at the statistics the kernel saved
+    mm, rs = m.cpu(), r.cpu()
+    rdx, rdw, rdb = O.groupnorm_backward(x, dy, mm, rs, w, b, act, over)
+    xh = (X - np.expand_dims(mm.double().numpy(), ax)) * np.expand_dims(rs.double().numpy(), ax)
+    exh = 4 * U * (np.abs(xh) + np.abs(X) * R)
+    edz = np.abs(DY) * (16 * U + 1.0 * (np.abs(W) * exh + 4 * U * (np.abs(W * xh) + np.abs(Bb))))
+    u, eu = np.abs(DY * W) * 1.13, np.abs(W) * edz
+    mean_ = lambda t: t.mean(ax, keepdims=True)
+    tol = R * (eu + mean_(eu) + np.abs(xh) * mean_(eu * np.abs(xh) + u * exh) + exh * mean_(u * np.abs(xh))
+               + (c64 + 8 * U) * (u + mean_(u) + np.abs(xh) * mean_(u * np.abs(xh))))
+    compare(dx, rdx, h * 1.01 * np.abs(rdx) + tol, what + " dx")
+    k = (shape[0] * shape[1] / 16 + 64) * U
+    adz = np.abs(DY) * 1.13
+    compare(dw, rdw, (k * adz * np.abs(xh) + edz * np.abs(xh) + adz * exh).sum((0, 1)), what + " dw")
+    compare(db, rdb, (k * adz + edz).sum((0, 1)), what + " db")
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("over", ["token", "sequence"])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_parity(io, over, shape):
+    run(io, shape, over, {0: "none", 1: "silu", 2: "gelu"}[sum(shape) % 3], seed=sum(shape))
+
+
+@pytest.mark.parametrize("act", ["none", "silu", "gelu"])
+@pytest.mark.parametrize("over", ["token", "sequence"])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_head_major_and_activations(io, over, act):
+    run(io, (2, 37, 6, 64), over, act, head_major=True)
+    run(io, (2, 21, 3, 20), over, act, head_major=True, affine=False)
+
+
+@pytest.mark.parametrize("over", ["token", "sequence"])
+def test_large_mean(over):
+    """A mean of 200 standard deviations, and one far outlier in front."""
+    run("f32", (2, 40, 3, 32), over, "none", mean=200.0)
+    x, _, w, b = make("f32", (1, 64, 2, 16))
+    x[:, 0] = 1e4
+    y, m, r = B.groupnorm_fwd(x.cuda(), w.cuda(), b.cuda(), over=over)
+    ry, rm, rr = O.groupnorm_forward(x, w, b, over=over)
+    # the centred sum keeps its relative precision whatever the first value is
+    np.testing.assert_allclose(m.cpu().numpy(), rm, rtol=1e-5, atol=1e-6)
+    np.testing.assert_allclose(r.cpu().numpy(), rr, rtol=1e-4)
+
+
+@pytest.mark.parametrize("over", ["token", "sequence"])
+def test_constant_and_non_finite_groups(over):
+    """A constant group gives the bias; NaN and infinity stay in their own group."""
+    x, dy, w, b = make("f32", (2, 9, 4, 16))
+    x[:, :, 1] = 3.0
+    x[0, 4, 2, 5] = float("nan")
+    x[1, 2, 3, 0] = float("inf")
+    y, m, r = B.groupnorm_fwd(x.cuda(), w.cuda(), b.cuda(), over=over)
+    y = y.cpu()
+    torch.testing.assert_close(y[:, :, 1], b[1].expand(2, 9, 16), rtol=0, atol=0)
+    bad = torch.zeros(2, 9, 4, dtype=torch.bool)
+    if over == "token":
+        bad[0, 4, 2] = bad[1, 2, 3] = True
+    else:
+        bad[0, :, 2] = bad[1, :, 3] = True
+    assert torch.equal(~torch.isfinite(y).all(-1), bad)
+
+
+def test_strided_output_weight_grad_and_statistics_optional():
+    x, dy, w, b = (t.cuda() for t in make("bf16", (2, 30, 4, 64)))
+    y, m, r = B.groupnorm_fwd(x, w, b, act="silu")
+    out = torch.full((2, 4, 30, 64), float("nan"), device="cuda", dtype=torch.bfloat16)
+    y2 = B.groupnorm_fwd(x, w, b, act="silu", return_stats=False, y=out.transpose(1, 2))
+    assert torch.equal(y, y2) and torch.equal(out.transpose(1, 2), y)
+    dx, dw, db = B.groupnorm_bwd(x, dy, m, r, w, b, act="silu")
+    dx2, none, none2 = B.groupnorm_bwd(x, dy, m, r, w, b, act="silu", weight_grad=False)
+    assert none is None and none2 is None and torch.equal(dx, dx2)
+    # a gradient that repeats over positions
+    dy1 = dy[:, :1].expand(-1, 30, -1, -1)
+    a = B.groupnorm_bwd(x, dy1, m, r, w, b)
+    c = B.groupnorm_bwd(x, dy1.contiguous(), m, r, w, b)
+    assert all(torch.equal(p, q) for p, q in zip(a, c))
+
+
+@pytest.mark.parametrize("over", ["token", "sequence"])
+def test_graph_replays(over):
+    x, dy, w, b = (t.cuda() for t in make("bf16", (3, 100, 4, 40)))
+    B.groupnorm_fwd(x, w, b, over=over)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, m, r = B.groupnorm_fwd(x, w, b, over=over, act="gelu")
+        g = B.groupnorm_bwd(x, dy, m, r, w, b, over=over, act="gelu")
+    for i in range(3):
+        x.mul_(1.5)
+        graph.replay()
+        y2, m2, r2 = B.groupnorm_fwd(x, w, b, over=over, act="gelu")
+        g2 = B.groupnorm_bwd(x, dy, m2, r2, w, b, over=over, act="gelu")
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip((y, m, r) + g, (y2, m2, r2) + g2)), i
+
+
+def test_workspace_is_not_overrun():
+    for over in ("token", "sequence"):
+        x, dy, w, b = (t.cuda() for t in make("bf16", (3, 50, 4, 24)))
+        n = B.groupnorm_workspace_size(3, 50, 4, 24, over, B.BF16, True)
+        ws = torch.full((n + 64,), 0xFF, dtype=torch.uint8, device="cuda")
+        y, m, r = B.groupnorm_fwd(x, w, b, over=over)
+        a = B.groupnorm_bwd(x, dy, m, r, w, b, over=over, workspace=ws)
+        c = B.groupnorm_bwd(x, dy, m, r, w, b, over=over)
+        assert all(torch.equal(p, q) for p, q in zip(a, c))
+        assert bool((ws[n:] == 0xFF).all())
+
+
+def test_refusals_of_the_binding():
+    x, dy, w, b = (t.cuda() for t in make("f32", (2, 3, 4, 16)))
+    with pytest.raises(ValueError):
+        B.groupnorm_fwd(x, act="tanh")
+    with pytest.raises(ValueError):
+        B.groupnorm_fwd(x, w[:2], b)
+    with pytest.raises(TypeError):
+        B.groupnorm_fwd(x, w.bfloat16(), b)
+    with pytest.raises(B.MlstmError):
+        B.groupnorm_fwd(x, w, b, y=x)
+    with pytest.raises(B.MlstmError):
+        B.groupnorm_fwd(x, w, b, eps=0.0)
+    with pytest.raises(TypeError):
+        B.groupnorm_bwd(x, dy, None, None)
+
+
+def test_behind_linear_attention():
+    """The operators as a block uses them: prefill into token-major rows, head
+    norm with SiLU, its gradient straight into linear attention's backward, and
+    decode steps that continue with the same values."""
+    Bn, H, T, d = 2, 4, 70, 64
+    r = torch.Generator(device="cuda").manual_seed(9)
+    q, k, v = (torch.randn((Bn, H, T, d), generator=r, device="cuda") * s for s in (1.0, d ** -0.5, 1.0))
+    g = torch.tensor([-0.5, -0.1, -0.02, -0.004], device="cuda")
+    w = 1 + 0.1 * torch.randn((H, d), generator=r, device="cuda")
+    b = 0.1 * torch.randn((H, d), generator=r, device="cuda")
+    rows = torch.empty((Bn, T, H, d), device="cuda")
+    o, S = B.linattn_fwd(q, k, v, g, o=rows.permute(0, 2, 1, 3))
+    y, m, rs = B.groupnorm_fwd(rows, w, b, act="silu")
+    dy = torch.randn((Bn, T, H, d), generator=r, device="cuda")
+    dx, dw, db = B.groupnorm_bwd(rows, dy, m, rs, w, b, act="silu")
+    dq, dk, dv = B.linattn_bwd(q, k, v, g, dx.permute(0, 2, 1, 3))
+    # the oracle's chain
+    ro, _ = O.linattn_forward(q, k, v, g)
+    ry, rm, rr = O.groupnorm_forward(ro.transpose(0, 2, 1, 3), w, b, 1e-5, "silu")
+    rdx, rdw, rdb = O.groupnorm_backward(ro.transpose(0, 2, 1, 3), dy, rm, rr, w, b, "silu")
+    rg = O.linattn_backward(q, k, v, g, rdx.transpose(0, 2, 1, 3))
+    # float32 chain: each operator's own bounds are a few 1e-6 of its scale,
+    # and the norm of a row divides by its spread (not below 0.05 here)
+    for n, a, c in (("y", y, ry), ("dw", dw, rdw), ("db", db, rdb), ("dq", dq, rg[0]), ("dk", dk, rg[1]),
+                    ("dv", dv, rg[2])):
+        e = np.abs(a.double().cpu().numpy() - c).max() / np.abs(c).max()
+        assert e <= 1e-4, (n, e)
+    # decode: the last 10 tokens one by one
+    _, St = B.linattn_fwd(q[:, :, :60], k[:, :, :60], v[:, :, :60], g)
+    for t in range(60, T):
+        ot, _ = B.linattn_step(q[:, :, t], k[:, :, t], v[:, :, t], g, St)
+        yt = B.groupnorm_fwd(ot[:, None], w, b, act="silu", return_stats=False)
+        torch.testing.assert_close(yt[:, 0], y[:, t], rtol=0, atol=2e-4)

@@ -42,6 +42,20 @@ SIGNATURES = {
     "mlstm_layer_fwd": (_i, [_vp] * 20 + [_i] * 8 + [_vp, _sz, _vp]),
     "mlstm_slstm_fwd": (_i, [_vp] * 11 + [_i] * 5 + [_vp]),
 }
+# the same for include/mlstm_ops.h
+_f, _szp = ctypes.c_float, ctypes.POINTER(_sz)
+OPS_SIGNATURES = {
+    "mlstm_linattn_fwd_workspace_size": (_i, [_i] * 6 + [_szp]),
+    "mlstm_linattn_fwd": (_i, [_vp] * 9 + [_f] + [_i] * 6 + [_vp, _sz, _vp]),
+    "mlstm_linattn_step": (_i, [_vp] * 8 + [_f] + [_i] * 5 + [_vp]),
+    "mlstm_linattn_bwd_workspace_size": (_i, [_i] * 6 + [_szp]),
+    "mlstm_linattn_bwd": (_i, [_vp] * 13 + [_f] + [_i] * 6 + [_vp, _sz, _vp]),
+    "mlstm_groupnorm_workspace_size": (_i, [_i] * 7 + [_szp]),
+    "mlstm_groupnorm_fwd": (_i, [_vp] * 7 + [_i] * 6 + [_f, _i, _vp, _sz, _vp]),
+    "mlstm_groupnorm_bwd": (_i, [_vp] * 10 + [_i] * 7 + [_vp, _sz, _vp]),
+}
+ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2}
+NORM_OVER = {"token": 0, "sequence": 1}
 
 
 class MlstmError(RuntimeError):
@@ -63,7 +77,7 @@ def lib() -> ctypes.CDLL:
             raise RuntimeError(f"HIP library not built: {LIB_PATH} "
                                "(run python -m xlstm_mlstm_matrix_amd.build)")
         L = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in SIGNATURES.items():
+        for name, (res, args) in {**SIGNATURES, **OPS_SIGNATURES}.items():
             fn = getattr(L, name)
             fn.restype = res
             fn.argtypes = args
@@ -384,3 +398,268 @@ def step_noalloc(q, k, v, i_pre, f_pre, o_pre, C=None, n=None, m=None, *, h=None
         _ptr(C), _ptr(n), _ptr(m), _ptr(h), _ptr(C_out), _ptr(n_out), _ptr(m_out),
         B, H, dk, dv, _io(q), _stream(dev)))
     return h, C_out, n_out, m_out
+
+
+# ---- operators of include/mlstm_ops.h
+
+def _view(t, name, shape, dtype, device):
+    """Check a strided tensor whose last dimension is contiguous."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have a contiguous last dimension")
+
+
+def _dense(t, name, shape, dtype, device):
+    """Check a dense tensor (None passes)."""
+    if t is None:
+        return
+    _req(t, name, dtype, device)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _strides(*ts):
+    """mlstm_strides_t array of [., ., ., d] tensors (of [., ., d] ones: s2 = 0)."""
+    flat = []
+    for t in ts:
+        flat += (list(t.stride()[:-1]) + [0])[:3]
+    return (ctypes.c_longlong * len(flat))(*flat)
+
+
+def _hip_device(t, name):
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.device.type != "cuda":
+        raise ValueError("tensors must be on a HIP device")
+    return t.device
+
+
+def _workspace(workspace, nbytes, device):
+    """(pointer, bytes) of a call's workspace, a fresh one when none is given.
+    The tensor itself comes third: it has to live until the call is enqueued."""
+    import torch
+    if workspace is None:
+        if nbytes == 0:
+            return None, 0, None
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    elif workspace.device != device:
+        raise ValueError(f"workspace must be on {device}, got {workspace.device}")
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def linattn_workspace_size(B, H, T, d_qk, d_v, io: int, backward: bool = False) -> int:
+    """Bytes of workspace of linattn_fwd, or of linattn_bwd."""
+    n = ctypes.c_size_t(0)
+    f = lib().mlstm_linattn_bwd_workspace_size if backward else lib().mlstm_linattn_fwd_workspace_size
+    _check(f(B, H, T, d_qk, d_v, io, ctypes.byref(n)))
+    return n.value
+
+
+def linattn_fwd(q, k, v, log_decay, S0=None, *, lengths=None, scale: float = 1.0,
+                return_state: bool = True, o=None, S_T=None, workspace=None):
+    """Linear attention with a decay for each head, over whole sequences:
+    S_t = e^g S_{t-1} + k_t v_t^T, o_t = scale * q_t^T S_t, g = log_decay[h].
+
+    q, k [B,H,T,d_qk], v [B,H,T,d_v] (float32 or bfloat16, one dtype; any
+    strides that are multiples of 16 bytes, e.g. views of token-major rows,
+    the last dimension contiguous); log_decay [H] float32, <= 0; optional S0
+    [B,H,d_qk,d_v] float32; optional lengths [B] int32 of a padded batch: rows
+    behind a sequence's length are not read, come out as zeros, and do not
+    touch its state.  Returns o [B,H,T,d_v], or (o, S_T) with
+    ``return_state``.  Output buffers may be passed in (S_T may be S0; o may
+    be strided)."""
+    import torch
+    dev = _hip_device(q, "q")
+    io = _io(q)
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k, v must be [B, H, T, d]")
+    B, H, T, dk = q.shape
+    dv = v.shape[-1]
+    _view(q, "q", (B, H, T, dk), q.dtype, dev)
+    _view(k, "k", (B, H, T, dk), q.dtype, dev)
+    _view(v, "v", (B, H, T, dv), q.dtype, dev)
+    _dense(log_decay, "log_decay", (H,), torch.float32, dev)
+    _dense(S0, "S0", (B, H, dk, dv), torch.float32, dev)
+    _dense(lengths, "lengths", (B,), torch.int32, dev)
+    with torch.cuda.device(dev):
+        if o is None:
+            o = torch.empty((B, H, T, dv), dtype=q.dtype, device=dev)
+        if return_state and S_T is None:
+            S_T = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
+        _view(o, "o", (B, H, T, dv), q.dtype, dev)
+        _dense(S_T, "S_T", (B, H, dk, dv), torch.float32, dev)
+        wp, wn, _keep = _workspace(workspace, linattn_workspace_size(B, H, T, dk, dv, io), dev)
+        _check(lib().mlstm_linattn_fwd(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(S0), _ptr(lengths), _ptr(o), _ptr(S_T),
+            _strides(q, k, v, o), scale, B, H, T, dk, dv, io, wp, wn, _stream(dev)))
+    return (o, S_T) if return_state else o
+
+
+def linattn_step(q, k, v, log_decay, S=None, *, scale: float = 1.0, o=None, S_out=None,
+                 inplace: bool = True):
+    """One token of linear attention for B*H heads.
+
+    q, k [B,H,d_qk], v [B,H,d_v] (strided as in linattn_fwd), log_decay [H],
+    state S [B,H,d_qk,d_v] float32 or None for the zero state.  With
+    ``inplace`` (default), a state and no ``S_out``, the state tensor is
+    updated in place.  Returns (o, S_out)."""
+    import torch
+    dev = _hip_device(q, "q")
+    io = _io(q)
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k, v must be [B, H, d]")
+    B, H, dk = q.shape
+    dv = v.shape[-1]
+    _view(q, "q", (B, H, dk), q.dtype, dev)
+    _view(k, "k", (B, H, dk), q.dtype, dev)
+    _view(v, "v", (B, H, dv), q.dtype, dev)
+    _dense(log_decay, "log_decay", (H,), torch.float32, dev)
+    _dense(S, "S", (B, H, dk, dv), torch.float32, dev)
+    with torch.cuda.device(dev):
+        if o is None:
+            o = torch.empty((B, H, dv), dtype=q.dtype, device=dev)
+        if S_out is None:
+            S_out = S if inplace and S is not None else \
+                torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
+        _view(o, "o", (B, H, dv), q.dtype, dev)
+        _dense(S_out, "S_out", (B, H, dk, dv), torch.float32, dev)
+        _check(lib().mlstm_linattn_step(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(S), _ptr(o), _ptr(S_out),
+            _strides(q, k, v, o), scale, B, H, dk, dv, io, _stream(dev)))
+    return o, S_out
+
+
+def linattn_bwd(q, k, v, log_decay, do, S0=None, dS_T=None, *, lengths=None, scale: float = 1.0,
+                state_grad: bool = False, dq=None, dk=None, dv=None, workspace=None):
+    """Gradients of a loss L for the inputs of linattn_fwd, given dL/do [B,H,T,d_v]
+    and, where the final state was used, dL/dS_T.
+
+    Returns (dq, dk, dv) in the I/O dtype, each rounded once from float32 (zeros
+    behind a sequence's length), and with ``state_grad`` also dS0 float32 (of
+    the zero state when S0 is None).  log_decay is a constant and gets none.
+    Buffers for dq, dk and dv may be passed in, strided like the inputs."""
+    import torch
+    dev = _hip_device(q, "q")
+    io = _io(q)
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k, v must be [B, H, T, d]")
+    B, H, T, d_qk = q.shape
+    d_v = v.shape[-1]
+    nk, nv, ns = (B, H, T, d_qk), (B, H, T, d_v), (B, H, d_qk, d_v)
+    for name, t, shape in (("q", q, nk), ("k", k, nk), ("v", v, nv), ("do", do, nv)):
+        _view(t, name, shape, q.dtype, dev)
+    _dense(log_decay, "log_decay", (H,), torch.float32, dev)
+    _dense(S0, "S0", ns, torch.float32, dev)
+    _dense(dS_T, "dS_T", ns, torch.float32, dev)
+    _dense(lengths, "lengths", (B,), torch.int32, dev)
+    with torch.cuda.device(dev):
+        new = lambda t, shape: torch.empty(shape, dtype=q.dtype, device=dev) if t is None else t
+        dq, dk, dv = new(dq, nk), new(dk, nk), new(dv, nv)
+        for name, t, shape in (("dq", dq, nk), ("dk", dk, nk), ("dv", dv, nv)):
+            _view(t, name, shape, q.dtype, dev)
+        dS0 = torch.empty(ns, dtype=torch.float32, device=dev) if state_grad else None
+        wp, wn, _keep = _workspace(workspace, linattn_workspace_size(B, H, T, d_qk, d_v, io, True), dev)
+        _check(lib().mlstm_linattn_bwd(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(S0), _ptr(lengths), _ptr(do), _ptr(dS_T),
+            _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dS0), _strides(q, k, v, do, dq, dk, dv), scale,
+            B, H, T, d_qk, d_v, io, wp, wn, _stream(dev)))
+    return (dq, dk, dv, dS0) if state_grad else (dq, dk, dv)
+
+
+def _choice(table, key, name):
+    if key not in table:
+        raise ValueError(f"{name} must be one of {sorted(table)}, got {key!r}")
+    return table[key]
+
+
+def groupnorm_workspace_size(N, S, G, D, over: str, io: int, backward: bool = False) -> int:
+    """Bytes of workspace of groupnorm_fwd, or of groupnorm_bwd."""
+    n = ctypes.c_size_t(0)
+    _check(lib().mlstm_groupnorm_workspace_size(N, S, G, D, _choice(NORM_OVER, over, "over"), io,
+                                                int(backward), ctypes.byref(n)))
+    return n.value
+
+
+def groupnorm_fwd(x, weight=None, bias=None, *, eps: float = 1e-5, act: str = "none",
+                  over: str = "token", return_stats: bool = True, y=None, workspace=None):
+    """Group norm with an activation, channels last.
+
+    x [N,S,G,D] (float32 or bfloat16; N samples of S positions, G groups of D
+    channels; any strides, the last dimension contiguous: cell outputs
+    [B,H,T,d] go in as ``h.transpose(1, 2)``).  Statistics are taken over a
+    group's channels at each position (``over="token"``: the norm of each
+    head) or over all positions too (``over="sequence"``).  weight, bias
+    [G,D] float32 or None; act "none", "silu" or "gelu".  Returns y
+    [N,S,G,D] (dense unless a buffer is given), or (y, mean, rstd) with
+    ``return_stats``: float32 [N,S,G] over tokens, [N,G] over sequences."""
+    import torch
+    dev = _hip_device(x, "x")
+    io = _io(x)
+    if x.dim() != 4:
+        raise ValueError("x must be [N, S, G, D]")
+    N, S, G, D = x.shape
+    _view(x, "x", x.shape, x.dtype, dev)
+    _dense(weight, "weight", (G, D), torch.float32, dev)
+    _dense(bias, "bias", (G, D), torch.float32, dev)
+    ov, ac = _choice(NORM_OVER, over, "over"), _choice(ACTIVATIONS, act, "act")
+    with torch.cuda.device(dev):
+        if y is None:
+            y = torch.empty((N, S, G, D), dtype=x.dtype, device=dev)
+        _view(y, "y", x.shape, x.dtype, dev)
+        mean = rstd = None
+        if return_stats:
+            shape = (N, S, G) if over == "token" else (N, G)
+            mean = torch.empty(shape, dtype=torch.float32, device=dev)
+            rstd = torch.empty(shape, dtype=torch.float32, device=dev)
+        wp, wn, _keep = _workspace(workspace, groupnorm_workspace_size(N, S, G, D, over, io), dev)
+        _check(lib().mlstm_groupnorm_fwd(
+            _ptr(x), _ptr(weight), _ptr(bias), _ptr(y), _ptr(mean), _ptr(rstd), _strides(x, y),
+            N, S, G, D, ov, ac, eps, io, wp, wn, _stream(dev)))
+    return (y, mean, rstd) if return_stats else y
+
+
+def groupnorm_bwd(x, dy, mean, rstd, weight=None, bias=None, *, act: str = "none", over: str = "token",
+                  weight_grad: bool = True, dx=None, workspace=None):
+    """Gradients of groupnorm_fwd, given dy [N,S,G,D] (strided like x) and the
+    forward's mean and rstd.  Returns (dx, dweight, dbias), dx in the I/O
+    dtype, the other two [G,D] float32 (None without ``weight_grad``)."""
+    import torch
+    dev = _hip_device(x, "x")
+    io = _io(x)
+    if x.dim() != 4:
+        raise ValueError("x must be [N, S, G, D]")
+    N, S, G, D = x.shape
+    _view(x, "x", x.shape, x.dtype, dev)
+    _view(dy, "dy", x.shape, x.dtype, dev)
+    stat = (N, S, G) if over == "token" else (N, G)
+    ov, ac = _choice(NORM_OVER, over, "over"), _choice(ACTIVATIONS, act, "act")
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t is None:
+            raise TypeError(f"{name} must be a torch tensor")
+        _dense(t, name, stat, torch.float32, dev)
+    _dense(weight, "weight", (G, D), torch.float32, dev)
+    _dense(bias, "bias", (G, D), torch.float32, dev)
+    with torch.cuda.device(dev):
+        if dx is None:
+            dx = torch.empty((N, S, G, D), dtype=x.dtype, device=dev)
+        _view(dx, "dx", x.shape, x.dtype, dev)
+        dw = db = None
+        if weight_grad:
+            dw = torch.empty((G, D), dtype=torch.float32, device=dev)
+            db = torch.empty((G, D), dtype=torch.float32, device=dev)
+        wp, wn, _keep = _workspace(workspace, groupnorm_workspace_size(N, S, G, D, over, io, True), dev)
+        _check(lib().mlstm_groupnorm_bwd(
+            _ptr(x), _ptr(dy), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(bias), _ptr(dx), _ptr(dw), _ptr(db),
+            _strides(x, dy, dx), N, S, G, D, ov, ac, io, wp, wn, _stream(dev)))
+    return dx, dw, db

@@ -1,0 +1,676 @@
+// groupnorm.hip -- group norm with an activation, channels last, forward and
+// backward.
+//
+//   xh = (x - mean) rstd,  z = w xh + b,  y = act(z);
+//   dz = dy act'(z),  u = dz w,  dx = rstd (u - mean(u) - xh mean(u xh)),
+//   dw = sum dz xh,  db = sum dz        (sums over samples and positions).
+//
+// All of it is bound by memory: x read and y written once (forward), x and dy
+// read and dx written once (backward).
+//
+// Over tokens a group is D contiguous channels: gn_row_kernel holds it in the
+// registers of a few lanes.  Over sequences, and for rows too long for that,
+// the work is split over positions: gn_channel_kernel reduces a block of
+// positions to two numbers for each channel, gn_combine_kernel joins those
+// into the group's statistics (or the backward's two means), and
+// gn_apply_kernel writes the result.  Every sum has a fixed order.
+#include "ops.hpp"
+
+namespace mlstm {
+
+namespace {
+
+template <int ACT>
+__device__ __forceinline__ float act_f(float z) {
+    if constexpr (ACT == 1) return z / (1.0f + exp_e(-z));
+    if constexpr (ACT == 2) return 0.5f * z * (1.0f + erff(z * 0.70710678f));
+    return z;
+}
+template <int ACT>
+__device__ __forceinline__ float act_d(float z) {
+    if constexpr (ACT == 1) {
+        const float sg = sigmoid(z);
+        return sg * (1.0f + z * (1.0f - sg));
+    }
+    if constexpr (ACT == 2)
+        return 0.5f * (1.0f + erff(z * 0.70710678f)) + z * 0.39894228f * exp_e(-0.5f * z * z);
+    return 1.0f;
+}
+
+// V consecutive elements, V * sizeof(IO) = 16 bytes or one element.
+template <typename IO, int V>
+__device__ __forceinline__ void load_v(const IO *p, float *x) {
+    if constexpr (V == 1) {
+        x[0] = to_f(p[0]);
+    } else {
+        typedef IO vec __attribute__((ext_vector_type(V)));
+        const vec t = *(const vec *)p;
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = to_f(t[i]);
+    }
+}
+template <typename IO, int V>
+__device__ __forceinline__ void store_v(IO *p, const float *x) {
+    if constexpr (V == 1) {
+        p[0] = from_f<IO>(x[0]);
+    } else {
+        typedef IO vec __attribute__((ext_vector_type(V)));
+        vec t;
+#pragma unroll
+        for (int i = 0; i < V; ++i) t[i] = from_f<IO>(x[i]);
+        *(vec *)p = t;
+    }
+}
+
+// ---- over tokens, D <= 64 V K: lanes of a row
+//
+// A wavefront is cut into subgroups of `lpr` lanes, each holding one group's D
+// channels (K vectors a lane).  `gp` neighbouring subgroups take neighbouring
+// groups of one position (contiguous memory in token-major tensors), the rest
+// take further positions.  A workgroup stays with its groups, so weights are
+// loaded once and the weight gradients add up in registers.
+struct RowGeom {
+    int lpr, gp, gblk, rblk;  // lanes per row, groups side by side, blocks of groups, blocks of positions
+};
+
+template <typename IO, int V, int K, int ACT, bool BWD>
+__global__ __launch_bounds__(256) void gn_row_kernel(GnArgs a, RowGeom q) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int sub = lane / q.lpr, ln = lane % q.lpr;
+    const int rpi = 64 / (q.lpr * q.gp);  // positions of a wavefront at a time
+    const int gb = blockIdx.x % q.gblk, rb = blockIdx.x / q.gblk;
+    const int g = gb * q.gp + sub % q.gp, rsub = sub / q.gp;
+    const int D = a.D, nrow = a.N * a.S;
+    const IO *x = (const IO *)a.x + g * a.sx.s2;
+    const IO *dy = BWD ? (const IO *)a.dy + g * a.sdy.s2 : nullptr;
+    IO *y = (IO *)a.y + g * a.sy.s2;
+    bool ok[K];
+    int d[K];
+    float w[K][V], bb[K][V], aw[K][V], ab[K][V];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        d[k] = (k * q.lpr + ln) * V;
+        ok[k] = d[k] < D;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            w[k][i] = ok[k] && a.w ? a.w[(size_t)g * D + d[k] + i] : 1.0f;
+            bb[k][i] = ok[k] && a.b ? a.b[(size_t)g * D + d[k] + i] : 0.0f;
+            aw[k][i] = ab[k][i] = 0.0f;
+        }
+    }
+    const float inv = 1.0f / (float)D;
+    auto sum = [&](float v) {
+        for (int m = q.lpr >> 1; m > 0; m >>= 1) v += __shfl_xor(v, m, 64);
+        return v;
+    };
+    for (long long r0 = (long long)(rb * 4 + wave) * rpi; r0 < nrow; r0 += (long long)q.rblk * 4 * rpi) {
+        const int r = (int)r0 + rsub;
+        const bool rok = r0 + rsub < nrow;
+        const int n = rok ? r / a.S : 0, s = rok ? r % a.S : 0;
+        float v[K][V];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[k][i] = 0.0f;
+            if (rok && ok[k]) load_v<IO, V>(x + n * a.sx.s0 + s * a.sx.s1 + d[k], v[k]);
+        }
+        const size_t si = ((size_t)n * a.S + s) * a.G + g;
+        if constexpr (!BWD) {
+            float t = 0.0f;
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int i = 0; i < V; ++i) t += v[k][i];
+            const float mu = sum(t) * inv;
+            t = 0.0f;
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float c = v[k][i] - mu;
+                    t += ok[k] ? c * c : 0.0f;
+                }
+            const float rs = rsqrtf(sum(t) * inv + a.eps);
+            if (a.mean && rok && ln == 0) {
+                a.mean[si] = mu;
+                a.rstd[si] = rs;
+            }
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[k][i] = act_f<ACT>((v[k][i] - mu) * rs * w[k][i] + bb[k][i]);
+                if (rok && ok[k]) store_v<IO, V>(y + n * a.sy.s0 + s * a.sy.s1 + d[k], v[k]);
+            }
+        } else {
+            float u[K][V];
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) u[k][i] = 0.0f;
+                if (rok && ok[k]) load_v<IO, V>(dy + n * a.sdy.s0 + s * a.sdy.s1 + d[k], u[k]);
+            }
+            const float mu = rok ? a.mean[si] : 0.0f, rs = rok ? a.rstd[si] : 0.0f;
+            float c1 = 0.0f, c2 = 0.0f;
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    if (!(rok && ok[k])) continue;
+                    const float xh = (v[k][i] - mu) * rs;
+                    const float dz = u[k][i] * act_d<ACT>(xh * w[k][i] + bb[k][i]);
+                    ab[k][i] += dz;
+                    aw[k][i] += dz * xh;
+                    v[k][i] = xh;
+                    u[k][i] = dz * w[k][i];
+                    c1 += u[k][i];
+                    c2 += u[k][i] * xh;
+                }
+            c1 = sum(c1) * inv;
+            c2 = sum(c2) * inv;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) u[k][i] = rs * (u[k][i] - c1 - v[k][i] * c2);
+                if (rok && ok[k]) store_v<IO, V>(y + n * a.sy.s0 + s * a.sy.s1 + d[k], u[k]);
+            }
+        }
+    }
+    if constexpr (BWD) {
+        if (!a.dw && !a.db) return;
+        // the positions that the lanes of one channel took: over the
+        // wavefront's subgroups, then over the wavefronts
+        __shared__ float red[2][4][64];
+        const int step = q.lpr * q.gp;
+        float *ws = a.ws + (size_t)rb * 2 * a.G * D;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float pw = aw[k][i], pb = ab[k][i];
+                for (int m = step; m < 64; m <<= 1) {
+                    pw += __shfl_xor(pw, m, 64);
+                    pb += __shfl_xor(pb, m, 64);
+                }
+                __syncthreads();
+                red[0][wave][lane] = pw;
+                red[1][wave][lane] = pb;
+                __syncthreads();
+                if (wave < 2 && lane < step && ok[k]) {
+                    const float t = (red[wave][0][lane] + red[wave][1][lane]) +
+                                    (red[wave][2][lane] + red[wave][3][lane]);
+                    ws[(size_t)wave * a.G * D + (size_t)g * D + d[k] + i] = t;
+                }
+            }
+    }
+}
+
+__device__ __forceinline__ float gn_block_sum(float v, float *red) {
+    __syncthreads();
+    red[threadIdx.x] = v;
+    __syncthreads();
+    for (int m = 128; m > 0; m >>= 1) {
+        if ((int)threadIdx.x < m) red[threadIdx.x] += red[threadIdx.x + m];
+        __syncthreads();
+    }
+    return red[0];
+}
+
+// ---- over tokens, rows too long for the registers: a workgroup for each row,
+// which later passes over the row find in the caches.  The weight gradients
+// come from gn_channel_kernel.
+template <typename IO, int V, int ACT, bool BWD>
+__global__ __launch_bounds__(256) void gn_long_row_kernel(GnArgs a, long long rows) {
+    __shared__ float red[256];
+    const float inv = 1.0f / (float)a.D;
+    for (long long r = blockIdx.x; r < rows; r += gridDim.x) {
+        const int g = (int)(r % a.G), ns = (int)(r / a.G);
+        const int n = ns / a.S, p = ns % a.S;
+        const IO *x = (const IO *)a.x + n * a.sx.s0 + p * a.sx.s1 + g * a.sx.s2;
+        const IO *dy = BWD ? (const IO *)a.dy + n * a.sdy.s0 + p * a.sdy.s1 + g * a.sdy.s2 : nullptr;
+        IO *y = (IO *)a.y + n * a.sy.s0 + p * a.sy.s1 + g * a.sy.s2;
+        const float *w = a.w ? a.w + (size_t)g * a.D : nullptr, *b = a.b ? a.b + (size_t)g * a.D : nullptr;
+        float mu, rs, s0 = 0.0f, s1 = 0.0f;
+        float v[V], u[V];
+        if constexpr (!BWD) {
+            for (int d = threadIdx.x * V; d < a.D; d += 256 * V) {
+                load_v<IO, V>(x + d, v);
+#pragma unroll
+                for (int i = 0; i < V; ++i) s0 += v[i];
+            }
+            mu = gn_block_sum(s0, red) * inv;
+            for (int d = threadIdx.x * V; d < a.D; d += 256 * V) {
+                load_v<IO, V>(x + d, v);
+#pragma unroll
+                for (int i = 0; i < V; ++i) s1 += (v[i] - mu) * (v[i] - mu);
+            }
+            rs = rsqrtf(gn_block_sum(s1, red) * inv + a.eps);
+            if (a.mean && threadIdx.x == 0) {
+                a.mean[r] = mu;
+                a.rstd[r] = rs;
+            }
+        } else {
+            mu = a.mean[r];
+            rs = a.rstd[r];
+            for (int d = threadIdx.x * V; d < a.D; d += 256 * V) {
+                load_v<IO, V>(x + d, v);
+                load_v<IO, V>(dy + d, u);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float xh = (v[i] - mu) * rs, ww = w ? w[d + i] : 1.0f;
+                    const float t = u[i] * act_d<ACT>(xh * ww + (b ? b[d + i] : 0.0f)) * ww;
+                    s0 += t;
+                    s1 += t * xh;
+                }
+            }
+            s0 = gn_block_sum(s0, red) * inv;
+            s1 = gn_block_sum(s1, red) * inv;
+        }
+        for (int d = threadIdx.x * V; d < a.D; d += 256 * V) {
+            load_v<IO, V>(x + d, v);
+            if constexpr (BWD) load_v<IO, V>(dy + d, u);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float xh = (v[i] - mu) * rs, ww = w ? w[d + i] : 1.0f;
+                const float z = xh * ww + (b ? b[d + i] : 0.0f);
+                if constexpr (BWD)
+                    v[i] = rs * (u[i] * act_d<ACT>(z) * ww - s0 - xh * s1);
+                else
+                    v[i] = act_f<ACT>(z);
+            }
+            store_v<IO, V>(y + d, v);
+        }
+    }
+}
+
+// dw, db: sums of the partials [rblk][2][C] in ws over rblk; blockIdx.y is 0 for dw.
+__global__ __launch_bounds__(256) void gn_wsum_kernel(const float *ws, float *dw, float *db, int C, int rblk) {
+    __shared__ float red[16][17];
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int c = blockIdx.x * 16 + tx, which = blockIdx.y;
+    float *out = which ? db : dw;
+    if (!out) return;
+    float t = 0.0f;
+    if (c < C)
+#pragma unroll 4
+        for (int r = ty; r < rblk; r += 16) t += ws[((size_t)r * 2 + which) * C + c];
+    red[ty][tx] = t;
+    __syncthreads();
+    for (int m = 8; m > 0; m >>= 1) {
+        if (ty < m) red[ty][tx] += red[ty + m][tx];
+        __syncthreads();
+    }
+    if (ty == 0 && c < C) out[c] = red[0][tx];
+}
+
+// ---- split over positions
+//
+// The S positions of a sample are cut into pblk blocks of plen.  A workgroup is
+// tx channel vectors x 256 / tx positions.  Partials: ws [N][pblk][2][C].
+struct PosGeom {
+    int tx, cblk;    // channel vectors of a workgroup, blocks of them
+    int plen, pblk;  // positions of a block, blocks
+};
+
+// offset of channel c of sample n's first position
+__device__ __forceinline__ long long gn_at(const Strides &st, int D, int n, int c) {
+    const int g = c / D;
+    return n * st.s0 + g * st.s2 + (c - g * D);
+}
+
+// sum over the rows ty of a workgroup, for V channels of each tx
+template <int V>
+__device__ __forceinline__ void gn_reduce(float *red, float (*t)[V], int tx, int TX, int ty, int TY) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            __syncthreads();
+            red[threadIdx.x] = t[j][i];
+            __syncthreads();
+            for (int m = TY >> 1; m > 0; m >>= 1) {
+                if (ty < m) red[threadIdx.x] += red[threadIdx.x + m * TX];
+                __syncthreads();
+            }
+            t[j][i] = red[tx];
+        }
+}
+
+// BWD false: mean and centred sum of squares of each channel of the block;
+// true: sum dz and sum dz xh.
+template <typename IO, int V, int ACT, bool BWD>
+__global__ __launch_bounds__(256) void gn_channel_kernel(GnArgs a, PosGeom q) {
+    __shared__ float red[256];
+    const int C = a.G * a.D;
+    const int tx = threadIdx.x % q.tx, ty = threadIdx.x / q.tx, TY = 256 / q.tx;
+    const int cb = blockIdx.x % q.cblk;
+    const int pb = blockIdx.x / q.cblk % q.pblk, o = blockIdx.x / q.cblk / q.pblk;
+    const int c = (cb * q.tx + tx) * V;
+    const bool ok = c < C;
+    const int p0 = pb * q.plen, p1 = min(p0 + q.plen, a.S);
+    float t[2][V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) t[0][i] = t[1][i] = 0.0f;
+    float shift[V], mu[V], rs[V], w[V], bb[V];
+    if (ok) {
+        const IO *x = (const IO *)a.x + gn_at(a.sx, a.D, o, c);
+        if constexpr (!BWD) {
+            // sums of x - (the block's first x): its square adds at most what
+            // that value itself adds to the centred sum, times the row count
+            load_v<IO, V>(x + p0 * a.sx.s1, shift);
+            for (int p = p0 + ty; p < p1; p += TY) {
+                float v[V];
+                load_v<IO, V>(x + p * a.sx.s1, v);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float e = v[i] - shift[i];
+                    t[0][i] += e;
+                    t[1][i] += e * e;
+                }
+            }
+        } else {
+            const IO *dy = (const IO *)a.dy + gn_at(a.sdy, a.D, o, c);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const size_t si = (size_t)o * a.G + (c + i) / a.D;
+                mu[i] = a.seq ? a.mean[si] : 0.0f;
+                rs[i] = a.seq ? a.rstd[si] : 0.0f;
+                w[i] = a.w ? a.w[c + i] : 1.0f;
+                bb[i] = a.b ? a.b[c + i] : 0.0f;
+            }
+            for (int p = p0 + ty; p < p1; p += TY) {
+                float v[V], u[V];
+                load_v<IO, V>(x + p * a.sx.s1, v);
+                load_v<IO, V>(dy + p * a.sdy.s1, u);
+                if (!a.seq) {  // each position has its own statistics
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const size_t si = ((size_t)o * a.S + p) * a.G + (c + i) / a.D;
+                        mu[i] = a.mean[si];
+                        rs[i] = a.rstd[si];
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float xh = (v[i] - mu[i]) * rs[i];
+                    const float dz = u[i] * act_d<ACT>(xh * w[i] + bb[i]);
+                    t[0][i] += dz;
+                    t[1][i] += dz * xh;
+                }
+            }
+        }
+    }
+    gn_reduce<V>(red, t, tx, q.tx, ty, TY);
+    if (ty == 0 && ok) {
+        float *ws = a.ws + ((size_t)o * q.pblk + pb) * 2 * C + c;
+        const float cnt = (float)(p1 - p0);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if constexpr (BWD) {
+                ws[C + i] = t[0][i];   // [0] is dw's sum, [1] db's, as in the row kernel
+                ws[i] = t[1][i];
+            } else {
+                ws[i] = shift[i] + t[0][i] / cnt;
+                ws[C + i] = fmaxf(t[1][i] - t[0][i] * t[0][i] / cnt, 0.0f);
+            }
+        }
+    }
+}
+
+// One workgroup per (sample, group).  Forward: mean and rstd from the channels'
+// means and centred sums.  Backward: mean(u) and mean(u xh).  Written to
+// out0, out1 [N][G].
+template <bool BWD>
+__global__ __launch_bounds__(256) void gn_combine_kernel(GnArgs a, PosGeom q, float *out0, float *out1) {
+    __shared__ float red[256];
+    const int g = blockIdx.x % a.G, o = blockIdx.x / a.G;
+    const int C = a.G * a.D, n = q.pblk * a.D;
+    const float *ws = a.ws + (size_t)o * q.pblk * 2 * C + (size_t)g * a.D;
+    const float total = (float)a.D * (float)a.S;
+    float s0 = 0.0f, s1 = 0.0f;
+    for (int e = threadIdx.x; e < n; e += 256) {
+        const int pb = e / a.D, d = e % a.D;
+        const float *r = ws + (size_t)pb * 2 * C + d;
+        if constexpr (BWD) {
+            const float w = a.w ? a.w[g * a.D + d] : 1.0f;
+            s0 += w * r[C];
+            s1 += w * r[0];
+        } else {
+            s0 += r[0] * (float)(min(a.S, (pb + 1) * q.plen) - pb * q.plen);
+        }
+    }
+    float m0 = gn_block_sum(s0, red) / total;
+    if constexpr (BWD) {
+        const float m1 = gn_block_sum(s1, red) / total;
+        if (threadIdx.x == 0) {
+            out0[blockIdx.x] = m0;
+            out1[blockIdx.x] = m1;
+        }
+    } else {
+        for (int e = threadIdx.x; e < n; e += 256) {
+            const int pb = e / a.D, d = e % a.D;
+            const float *r = ws + (size_t)pb * 2 * C + d;
+            const float c = r[0] - m0;
+            s1 += r[C] + c * c * (float)(min(a.S, (pb + 1) * q.plen) - pb * q.plen);
+        }
+        const float var = gn_block_sum(s1, red) / total;
+        if (threadIdx.x == 0) {
+            out0[blockIdx.x] = m0;
+            out1[blockIdx.x] = rsqrtf(var + a.eps);
+        }
+    }
+}
+
+template <typename IO, int V, int ACT, bool BWD>
+__global__ __launch_bounds__(256) void gn_apply_kernel(GnArgs a, PosGeom q, const float *in0, const float *in1) {
+    const int C = a.G * a.D;
+    const int tx = threadIdx.x % q.tx, ty = threadIdx.x / q.tx, TY = 256 / q.tx;
+    const int cb = blockIdx.x % q.cblk;
+    const int pb = blockIdx.x / q.cblk % q.pblk, o = blockIdx.x / q.cblk / q.pblk;
+    const int c = (cb * q.tx + tx) * V;
+    if (c >= C) return;
+    const int p0 = pb * q.plen, p1 = min(p0 + q.plen, a.S);
+    float mu[V], rs[V], w[V], bb[V], c1[V], c2[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const size_t si = (size_t)o * a.G + (c + i) / a.D;
+        if constexpr (BWD) {
+            mu[i] = a.mean[si];
+            rs[i] = a.rstd[si];
+            c1[i] = in0[si];
+            c2[i] = in1[si];
+        } else {
+            mu[i] = in0[si];
+            rs[i] = in1[si];
+        }
+        w[i] = a.w ? a.w[c + i] : 1.0f;
+        bb[i] = a.b ? a.b[c + i] : 0.0f;
+    }
+    const IO *x = (const IO *)a.x + gn_at(a.sx, a.D, o, c);
+    const IO *dy = BWD ? (const IO *)a.dy + gn_at(a.sdy, a.D, o, c) : nullptr;
+    IO *y = (IO *)a.y + gn_at(a.sy, a.D, o, c);
+#pragma unroll 2
+    for (int p = p0 + ty; p < p1; p += TY) {
+        float v[V], u[V];
+        load_v<IO, V>(x + p * a.sx.s1, v);
+        if constexpr (BWD) load_v<IO, V>(dy + p * a.sdy.s1, u);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float xh = (v[i] - mu[i]) * rs[i], z = xh * w[i] + bb[i];
+            if constexpr (BWD)
+                v[i] = rs[i] * (u[i] * act_d<ACT>(z) * w[i] - c1[i] - xh * c2[i]);
+            else
+                v[i] = act_f<ACT>(z);
+        }
+        store_v<IO, V>(y + p * a.sy.s1, v);
+    }
+}
+
+// ---- plans
+
+int pow2_at_least(int x) {
+    int p = 1;
+    while (p < x) p <<= 1;
+    return p;
+}
+
+// lanes' vectors of a row held in registers: 1, 4 or 0 (the row is too long)
+int row_vectors(int D, int V) {
+    const int k = (D + 64 * V - 1) / (64 * V);
+    return k <= 1 ? 1 : k <= 4 ? 4 : 0;
+}
+
+// element count of a 16-byte vector if every row of channels starts aligned
+// and no vector crosses a group boundary that memory does not continue over
+bool vec_ok(const GnArgs &a, int V) {
+    const Strides *st[] = {&a.sx, &a.sy, &a.sdy};
+    const int n = a.dy ? 3 : 2;
+    for (int i = 0; i < n; ++i) {
+        const bool flat = st[i]->s2 == a.D || a.G == 1;
+        if (!(a.D % V == 0 || (a.seq && flat && ((long long)a.G * a.D) % V == 0))) return false;
+        if ((a.N > 1 && st[i]->s0 % V) || (a.S > 1 && st[i]->s1 % V)) return false;
+        if (a.D % V == 0 && a.G > 1 && st[i]->s2 % V) return false;
+    }
+    return true;
+}
+
+RowGeom row_geom(int N, int S, int G, int D, int V, int K, bool token_major, bool bwd) {
+    RowGeom q;
+    const int vecs = (D + V - 1) / V;
+    q.lpr = K > 1 ? 64 : pow2_at_least(vecs);
+    // neighbouring groups side by side where they are neighbours in memory
+    q.gp = 1;
+    while (token_major && q.gp * 2 * q.lpr <= 64 && G % (q.gp * 2) == 0) q.gp *= 2;
+    q.gblk = G / q.gp;
+    const long long rows = (long long)N * S;
+    const long long per = 4 * (64 / (q.lpr * q.gp));
+    long long want = (rows + per - 1) / per;
+    // the backward leaves one set of partials for each block of positions
+    const long long cap = bwd ? (2048 + q.gblk - 1) / q.gblk : (8192 + q.gblk - 1) / q.gblk;
+    if (want > cap) want = cap;
+    q.rblk = (int)want;
+    return q;
+}
+
+PosGeom pos_geom(int N, int S, int C, int V) {
+    PosGeom q;
+    const int cv = (C + V - 1) / V;
+    const int p = pow2_at_least(cv);
+    q.tx = p > 64 ? 64 : p;
+    q.cblk = (cv + q.tx - 1) / q.tx;
+    // about eight workgroups a compute unit, at least 16 positions a block
+    const long long per = (long long)N * q.cblk;
+    long long want = (2048 + per - 1) / per;
+    const long long most = (S + 15) / 16;
+    if (want > most) want = most;
+    q.plen = (int)((S + want - 1) / want);
+    q.pblk = (S + q.plen - 1) / q.plen;
+    return q;
+}
+
+template <typename IO, int V, int ACT>
+hipError_t launch_seq(const GnArgs &a, hipStream_t s) {
+    const int C = a.G * a.D;
+    const PosGeom q = pos_geom(a.N, a.S, C, V);
+    const dim3 grid((unsigned)(q.cblk * q.pblk * a.N)), groups((unsigned)(a.N * a.G));
+    float *m0 = a.ws + (size_t)a.N * q.pblk * 2 * C, *m1 = m0 + (size_t)a.N * a.G;
+    if (!a.dy) {
+        gn_channel_kernel<IO, V, ACT, false><<<grid, 256, 0, s>>>(a, q);
+        if (a.mean) {
+            m0 = a.mean;
+            m1 = a.rstd;
+        }
+        gn_combine_kernel<false><<<groups, 256, 0, s>>>(a, q, m0, m1);
+        gn_apply_kernel<IO, V, ACT, false><<<grid, 256, 0, s>>>(a, q, m0, m1);
+    } else {
+        gn_channel_kernel<IO, V, ACT, true><<<grid, 256, 0, s>>>(a, q);
+        gn_combine_kernel<true><<<groups, 256, 0, s>>>(a, q, m0, m1);
+        gn_apply_kernel<IO, V, ACT, true><<<grid, 256, 0, s>>>(a, q, m0, m1);
+        if (a.dw || a.db)
+            gn_wsum_kernel<<<dim3((C + 15) / 16, 2), 256, 0, s>>>(a.ws, a.dw, a.db, C, a.N * q.pblk);
+    }
+    return hipGetLastError();
+}
+
+template <typename IO, int V, int ACT>
+hipError_t launch_long_row(const GnArgs &a, hipStream_t s) {
+    const long long rows = (long long)a.N * a.S * a.G;
+    const dim3 grid((unsigned)(rows < 16384 ? rows : 16384));
+    if (!a.dy) {
+        gn_long_row_kernel<IO, V, ACT, false><<<grid, 256, 0, s>>>(a, rows);
+    } else {
+        gn_long_row_kernel<IO, V, ACT, true><<<grid, 256, 0, s>>>(a, rows);
+        if (a.dw || a.db) {
+            const int C = a.G * a.D;
+            const PosGeom q = pos_geom(a.N, a.S, C, V);
+            gn_channel_kernel<IO, V, ACT, true><<<dim3((unsigned)(q.cblk * q.pblk * a.N)), 256, 0, s>>>(a, q);
+            gn_wsum_kernel<<<dim3((C + 15) / 16, 2), 256, 0, s>>>(a.ws, a.dw, a.db, C, a.N * q.pblk);
+        }
+    }
+    return hipGetLastError();
+}
+
+template <typename IO, int V, int K, int ACT>
+hipError_t launch_row(const GnArgs &a, hipStream_t s) {
+    const RowGeom q = row_geom(a.N, a.S, a.G, a.D, V, K, a.sx.s2 < a.sx.s1, a.dy != nullptr);
+    const dim3 grid((unsigned)(q.gblk * q.rblk));
+    if (!a.dy) {
+        gn_row_kernel<IO, V, K, ACT, false><<<grid, 256, 0, s>>>(a, q);
+    } else {
+        gn_row_kernel<IO, V, K, ACT, true><<<grid, 256, 0, s>>>(a, q);
+        const int C = a.G * a.D;
+        if (a.dw || a.db) gn_wsum_kernel<<<dim3((C + 15) / 16, 2), 256, 0, s>>>(a.ws, a.dw, a.db, C, q.rblk);
+    }
+    return hipGetLastError();
+}
+
+template <typename IO, int ACT>
+hipError_t launch_io(const GnArgs &a, hipStream_t s) {
+    constexpr int VV = 16 / (int)sizeof(IO);
+    const bool vec = vec_ok(a, VV);
+    if (!a.seq) {
+        const int k = row_vectors(a.D, vec ? VV : 1);
+        if (vec && k == 1) return launch_row<IO, VV, 1, ACT>(a, s);
+        if (vec && k == 4) return launch_row<IO, VV, 4, ACT>(a, s);
+        if (!vec && k == 1) return launch_row<IO, 1, 1, ACT>(a, s);
+        if (!vec && k == 4) return launch_row<IO, 1, 4, ACT>(a, s);
+        return vec ? launch_long_row<IO, VV, ACT>(a, s) : launch_long_row<IO, 1, ACT>(a, s);
+    }
+    return vec ? launch_seq<IO, VV, ACT>(a, s) : launch_seq<IO, 1, ACT>(a, s);
+}
+
+template <typename IO>
+hipError_t launch_act(const GnArgs &a, hipStream_t s) {
+    if (a.act == 1) return launch_io<IO, 1>(a, s);
+    if (a.act == 2) return launch_io<IO, 2>(a, s);
+    return launch_io<IO, 0>(a, s);
+}
+
+}  // namespace
+
+// Enough for either vector width and either order of the strides, which the query does not know.
+size_t groupnorm_workspace_floats(int N, int S, int G, int D, int seq, int io_bf16, int bwd) {
+    size_t need = 0;
+    const int C = G * D;
+    for (int V : {io_bf16 ? 8 : 4, 1}) {
+        const int k = seq ? 0 : row_vectors(D, V);
+        size_t f = 0;
+        if (k) {
+            if (bwd)
+                for (bool tm : {false, true}) {
+                    const size_t r = (size_t)row_geom(N, S, G, D, V, k, tm, true).rblk;
+                    f = r * 2 * C > f ? r * 2 * C : f;
+                }
+        } else if (seq || bwd) {
+            const PosGeom q = pos_geom(N, S, C, V);
+            f = (size_t)N * q.pblk * 2 * C + (seq ? 2 * (size_t)N * G : 0);
+        }
+        need = f > need ? f : need;
+    }
+    return need;
+}
+
+hipError_t launch_groupnorm(const GnArgs &a, int io_bf16, hipStream_t s) {
+    return io_bf16 ? launch_act<bf16>(a, s) : launch_act<float>(a, s);
+}
+
+}  // namespace mlstm
