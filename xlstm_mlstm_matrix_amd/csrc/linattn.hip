@@ -1,87 +1,705 @@
-// linattn.hip -- linear attention with a decay for each head.
+// linattn.hip -- linear attention with a decay for each head, in chunks of
+// L = 32 tokens on the matrix cores (forward, and the three passes of the
+// backward).
+//
+// A pass (LinJob) carries a state X [dk x dv] through local tokens tau.  With
+// tokens i, j of a chunk and n of them:
+//   o_i = in_scale e^{g (i + 1 - shift)} X^T q_i
+//         + sum_{j <= i} e^{g (i - j)} p_scale (q_i . k_j) v_j,
+//   X  <- e^{g n} X + up_scale sum_j e^{g (n - 1 + shift - j)} k_j v_j^T.
+// Every exponent is a number of steps times g <= 0, never a difference of
+// large ones, so no decay overflows and -inf is an ordinary value.
+//
+// A workgroup owns a block of value columns of one (b, h) and segment and walks
+// its chunks in order; a wavefront owns NCT tiles of 16 columns with all dk rows
+// of X in registers (float32, accumulator layout).  Nothing is exchanged
+// between wavefronts but the Q, K and V tiles in LDS: each computes the
+// chunk's scores for itself (32 x 32 of them, a small part of its products),
+// which saves a second barrier and a trip through LDS.
+//
+// Everything is computed transposed, so that each product's result is, lane by
+// lane, the operand of the next one:
+//   scores^T = K Q^T, lane: token i = l16, rows j           (accumulators)
+//   o^T = X^T Q^T + V^T P^T, lane: token i = l16, value rows (P^T straight from the scores)
+//   X += K^T (w V), lane: column l16, rows dk                (X^T straight from X)
+// The MFMA's inner index may be permuted if both operands agree: slot e of
+// lane group g4 stands for d_qk index 32 kk + 8 g4 + e, and for token
+// 16 (e / 4) + 4 g4 + e % 4.
+//
+// Roundings (bfloat16 I/O).  P and the read-out's copy of X are rounded to
+// bfloat16 once, which adds to the output about what its own rounding does.
+// w_j v_j enters the state in three parts (8 + 8 + 8 bits of its 24), because
+// the state is handed out in float32 and carried over the whole sequence:
+// two parts would leave it 3e-6 off, three leave what float32 sums do.  X
+// itself, every decay and every sum are float32.  float32 I/O runs on the
+// float32 MFMA without further rounding.
 #include "ops.hpp"
 
 namespace mlstm {
 
 namespace {
 
-constexpr int kCols = 16;  // state columns of a workgroup
+typedef bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void lds_ptr;
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-// The recurrence token by token.  One workgroup owns 16 state columns of one
-// (job, b, h): X [dk][16] in LDS, thread (rg, c) updates rows rg, rg + 16, ...
+constexpr int L = 32;           // tokens of a chunk
+constexpr int kBuf = 0x00020000; // word 3 of a raw, range-checked buffer descriptor
+constexpr unsigned kOut = 0xfffffff0u;  // an offset past any range: reads zero, writes nothing
+constexpr size_t kLds = 160 * 1024;
+constexpr float kRenorm = 1.0f / 65536.0f;  // sigma's least value
+
+// How the states of a pass are cut into segments.
+struct SegPlan {
+    int nseg, seg_len;
+};
+
+struct KArgs {
+    LinJob job[3];
+    int tiles[3];       // column blocks of each job
+    int njob, tiles_all;
+    const float *g;
+    const int *lengths;
+    int B, H, T, nseg, seg_len;
+    // incoming states of the segments: state (job, bh, seg) at
+    // ws + ws_job[job] + (bh * nseg + seg) * tiles * block, in the register layout
+    float *ws;
+    size_t ws_job[3];
+};
+
 template <typename IO>
-__global__ __launch_bounds__(256) void linattn_rec_kernel(LinArgs a, int ntile) {
-    extern __shared__ float lds[];
-    const int tile = blockIdx.x % ntile;
-    const int bh = (blockIdx.x / ntile) % (a.B * a.H);
-    const LinJob &j = a.job[blockIdx.x / ntile / (a.B * a.H)];
-    const int c0 = tile * kCols;
-    if (c0 >= j.dv) return;
+struct Types;
+template <>
+struct Types<bf16> {
+    typedef bf16x8 Frag;
+    static constexpr int EPG = 8;  // elements of a 16-byte granule
+    static constexpr int PARTS = 3;
+};
+template <>
+struct Types<float> {
+    typedef f32x8 Frag;
+    static constexpr int EPG = 4;
+    static constexpr int PARTS = 1;
+};
+
+__device__ __forceinline__ f32x4 mfma(const bf16x8 &a, const bf16x8 &b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mfma(const f32x8 &a, const f32x8 &b, f32x4 c) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
+    return c;
+}
+
+// 8 floats as one operand (rounded to nearest even for bfloat16)
+__device__ __forceinline__ void pack(const float *x, bf16x8 &f) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const bf16x2 h = __builtin_convertvector((f32x2{x[2 * p], x[2 * p + 1]}), bf16x2);
+        f[2 * p] = h[0];
+        f[2 * p + 1] = h[1];
+    }
+}
+__device__ __forceinline__ void pack(const float *x, f32x8 &f) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = x[e];
+}
+
+// 8 floats as a sum of PARTS operands: each part is the rounded rest of the one before
+__device__ __forceinline__ void split(float *x, bf16x8 *f) {
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const bf16x2 h = __builtin_convertvector((f32x2{x[2 * p], x[2 * p + 1]}), bf16x2);
+            f[q][2 * p] = h[0];
+            f[q][2 * p + 1] = h[1];
+            if (q < 2) {
+                const unsigned b = __builtin_bit_cast(unsigned, h);
+                x[2 * p] -= __uint_as_float(b << 16);
+                x[2 * p + 1] -= __uint_as_float(b & 0xffff0000u);
+            }
+        }
+}
+__device__ __forceinline__ void split(float *x, f32x8 *f) { pack(x, f[0]); }
+
+// Granule swizzle of a tile with GPR granules a row: a row's granule p is
+// stored at p ^ swz(row).  Rows are read whole-granule, 16 rows at a time at one
+// granule (scores, read-out), and transposed, four rows 4 g + (0..3) at four
+// neighbouring granules (state update, V); both then spread over the banks.
+template <int GPR>
+__device__ __forceinline__ int swz(int r) {
+    if constexpr (GPR >= 16) return ((r & 3) << 2) | ((r >> 2) & 3);
+    const int x = (r >> 1) & 7;
+    return ((x & 1) << 2) | (x & 2) | ((x >> 2) & 1);
+}
+
+__device__ __forceinline__ s16x4 tr_read(const bf16 *p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
+}
+
+// Whole-granule reads of a row: d_qk index 32 kk + 8 g4 + (0..7) of rows
+// l16 and 16 + l16.  The swizzle touches the low four bits of the granule
+// number at most, so a few addresses and constant offsets serve all kk.
+template <int GPR>
+struct Rows {
+    static constexpr int M = GPR >= 16 ? 4 : 2;  // low parts of the granule number, in steps of 4
+    int off[M];
+    __device__ __forceinline__ void init(const bf16 *, int l16, int g4) {
+#pragma unroll
+        for (int m = 0; m < M; ++m) off[m] = l16 * GPR * 8 + (((4 * m + g4) ^ swz<GPR>(l16)) << 3);
+    }
+    __device__ __forceinline__ void init(const float *, int l16, int g4) {
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+            off[m] = l16 * GPR * 4 + (((8 * (m >> 1) + 2 * g4 + (m & 1)) ^ swz<GPR>(l16)) << 2);
+    }
+    __device__ __forceinline__ bf16x8 get(const bf16 *t, int half, int kk) const {
+        return *reinterpret_cast<const bf16x8 *>(t + off[kk % M] + half * 16 * GPR * 8 + kk / M * M * 32);
+    }
+    __device__ __forceinline__ f32x8 get(const float *t, int half, int kk) const {
+        f32x8 f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const f32x4 x = *reinterpret_cast<const f32x4 *>(t + off[2 * (kk & 1) + h] + half * 16 * GPR * 4 + (kk >> 1) * 64);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[4 * h + e] = x[e];
+        }
+        return f;
+    }
+};
+
+// Transposed reads of all d_qk columns for the state update: columns
+// 32 kk + 4 u + 8 a + (0..3) of quad a, tokens as in col_frag.
+template <int GPR>
+struct Cols {
+    static constexpr int M = GPR >= 16 ? 4 : 2;
+    int off[M], l16, g4;
+    __device__ __forceinline__ void init(const bf16 *, int l, int g) {
+        const int r0 = 4 * g + (l >> 2);
+#pragma unroll
+        for (int m = 0; m < M; ++m) off[m] = r0 * GPR * 8 + (((4 * m + (l & 3)) ^ swz<GPR>(r0)) << 3);
+    }
+    __device__ __forceinline__ void init(const float *, int l, int g) { l16 = l, g4 = g; }
+    __device__ __forceinline__ bf16x8 get(const bf16 *t, int kk, int u) const;
+    __device__ __forceinline__ f32x8 get(const float *t, int kk, int u) const;
+};
+
+// Column l16 of 16 columns, tokens 16 (e / 4) + 4 g4 + e % 4 of the chunk.  The
+// columns come in quads of 4 consecutive elements; quad a starts at element
+// c0 + step * a (multiples of 4).
+template <int GPR>
+__device__ __forceinline__ bf16x8 col_frag(const bf16 *t, int c0, int step, int l16, int g4) {
+    const int c = c0 + step * (l16 & 3);
+    const int r0 = 4 * g4 + (l16 >> 2), r1 = r0 + 16;
+    const int gr = c >> 3, h = c & 4;
+    typedef short s16x8 __attribute__((ext_vector_type(8)));
+    const s16x4 a = tr_read(t + r0 * GPR * 8 + ((gr ^ swz<GPR>(r0)) << 3) + h);
+    const s16x4 b = tr_read(t + r1 * GPR * 8 + ((gr ^ swz<GPR>(r1)) << 3) + h);
+    const s16x8 r = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    return __builtin_bit_cast(bf16x8, r);
+}
+template <int GPR>
+__device__ __forceinline__ f32x8 col_frag(const float *t, int c0, int step, int l16, int g4) {
+    const int c = c0 + step * (l16 >> 2) + (l16 & 3);
+    f32x8 f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int r = 16 * (e >> 2) + 4 * g4 + (e & 3);
+        f[e] = t[r * GPR * 4 + (((c >> 2) ^ swz<GPR>(r)) << 2) + (c & 3)];
+    }
+    return f;
+}
+
+template <int GPR>
+__device__ __forceinline__ bf16x8 Cols<GPR>::get(const bf16 *t, int kk, int u) const {
+    typedef short s16x8 __attribute__((ext_vector_type(8)));
+    const bf16 *p = t + off[kk % M] + kk / M * M * 32 + 4 * u;
+    const s16x4 a = tr_read(p), b = tr_read(p + 16 * GPR * 8);
+    const s16x8 r = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    return __builtin_bit_cast(bf16x8, r);
+}
+template <int GPR>
+__device__ __forceinline__ f32x8 Cols<GPR>::get(const float *t, int kk, int u) const {
+    return col_frag<GPR>(t, 32 * kk + 4 * u, 8, l16, g4);
+}
+
+template <typename IO, int DKP_, int NCT_, int NW_>
+struct Cfg {
+    static constexpr int DKP = DKP_, NCT = NCT_, NW = NW_, NTH = 64 * NW_;
+    static constexpr int BV = 16 * NCT * NW;               // value columns of a workgroup
+    static constexpr int NAT = DKP / 16, NKS = DKP / 32;   // 16-row tiles of X, inner steps over d_qk
+    static constexpr int EPG = Types<IO>::EPG;
+    static constexpr int QG = DKP / EPG, VG = BV / EPG;    // granules of a row
+    static constexpr size_t TILE = (size_t)L * (2 * DKP + BV) * sizeof(IO);
+    static constexpr int NBUF = 2 * TILE <= kLds ? 2 : 1;
+    static constexpr int PER_CU = 2 * NBUF * TILE <= kLds ? 2 : 1;  // workgroups of a compute unit
+    static constexpr int BLOCK = DKP * BV;                 // floats of a stored state block
+    static_assert(QG >= 8 && VG >= 8, "swizzle");
+    static_assert(TILE <= kLds, "LDS");
+};
+
+// SO (state only): the first pass over segments, each from the zero state.
+template <typename IO, int DKP, int NCT, int NW, bool SO>
+__global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU)) void linattn_kernel(KArgs a) {
+    using C = Cfg<IO, DKP, NCT, NW>;
+    using Frag = typename Types<IO>::Frag;
+    constexpr int NAT = C::NAT, NKS = C::NKS, QG = C::QG, VG = C::VG, BV = C::BV, NBUF = C::NBUF;
+    constexpr int PARTS = Types<IO>::PARTS;
+    constexpr int ES = (int)sizeof(IO);
+    __shared__ __attribute__((aligned(16))) IO tiles[NBUF][L * (2 * DKP + BV)];
+
+    const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g4 = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+    // consecutive workgroups go round the 8 XCDs: give each XCD a contiguous
+    // run, so that the column blocks of one (b, h) share its L2
+    const int nwg = gridDim.x, xq = nwg >> 3, xr = nwg & 7, xcd = blockIdx.x & 7;
+    const int logical = xcd * xq + min(xcd, xr) + (blockIdx.x >> 3);
+    const int gseg = SO ? a.nseg - 1 : a.nseg;
+    int tile = logical % a.tiles_all, ji = 0;
+    while (tile >= a.tiles[ji]) tile -= a.tiles[ji++];
+    const int seg = logical / a.tiles_all % gseg, bh = logical / a.tiles_all / gseg;
+    const LinJob &job = a.job[ji];
     const int b = bh / a.H, h = bh % a.H;
-    const int n = a.lengths ? max(0, min(a.lengths[b], a.T)) : a.T;
-    const int c = threadIdx.x & 15, rg = threadIdx.x >> 4, dk = j.dk;
-    const int col = c0 + c;
-    const bool ok = col < j.dv;
-    float *X = lds, *qs = X + dk * kCols, *ks = qs + dk, *red = ks + dk;
+    const int dk = job.dk, dv = job.dv, T = a.T;
+    const int n = a.lengths ? max(0, min(a.lengths[b], T)) : T;
+    const int tau0 = seg * a.seg_len, tau1 = min(tau0 + a.seg_len, n);
+    if (SO && tau0 + a.seg_len >= n) return;  // no later segment
+    const int col0 = tile * BV;
+    const int ldq = (int)job.sq.s2, ldk = (int)job.sk.s2, ldv = (int)job.sv.s2, ldo = (int)job.so.s2;
+    const IO *qg = (const IO *)job.q + b * job.sq.s0 + h * job.sq.s1;
+    const IO *kg = (const IO *)job.k + b * job.sk.s0 + h * job.sk.s1;
+    const IO *vg = (const IO *)job.v + b * job.sv.s0 + h * job.sv.s1 + col0;
+    IO *og = (IO *)job.o + b * job.so.s0 + h * job.so.s1 + col0;
+    const bool rev = job.reverse;
+
+    // ---- decays
     const float gl = decay_log2(a.g[h]);
-    const float gam = __builtin_amdgcn_exp2f(gl);
-    const size_t st = (size_t)bh * dk * j.dv;
-    for (int r = rg; r < dk; r += 16)
-        X[r * kCols + c] = (ok && j.X0) ? j.X0[st + r * j.rs + col * j.cs] : 0.0f;
-    const IO *q = (const IO *)j.q + b * j.sq.s0 + h * j.sq.s1;
-    const IO *k = (const IO *)j.k + b * j.sk.s0 + h * j.sk.s1;
-    const IO *v = (const IO *)j.v + b * j.sv.s0 + h * j.sv.s1;
-    IO *o = (IO *)j.o + b * j.so.s0 + h * j.so.s1;
-    for (int tau = 0; tau < n; ++tau) {
-        const long long t = j.reverse ? n - 1 - tau : tau;
-        __syncthreads();
-        for (int r = threadIdx.x; r < dk; r += 256) {
-            qs[r] = to_f(q[t * j.sq.s2 + r]);
-            ks[r] = to_f(k[t * j.sk.s2 + r]);
+    const auto gpow = [&](int steps) { return __builtin_amdgcn_exp2f(gl * (float)steps); };
+    // P's weights of a score tile on the diagonal, and one tile below it
+    float dg[4], db[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int d = l16 - 4 * g4 - r;
+        dg[r] = gpow(max(d, 0)) * job.p_scale;
+        db[r] = gpow(16 + d) * job.p_scale;
+    }
+    const float fade0 = gpow(l16 + 1 - job.shift) * job.in_scale;
+    const float fade1 = gpow(16 + l16 + 1 - job.shift) * job.in_scale;
+    // weights of this lane's tokens in the state update, in a chunk of nc tokens
+    float w[8];
+    auto weights = [&](int nc) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int j = 16 * (e >> 2) + 4 * g4 + (e & 3);
+            w[e] = j < nc ? gpow(nc - 1 + job.shift - j) * job.up_scale : 0.0f;
         }
-        __syncthreads();
-        const float vv = ok ? to_f(v[t * j.sv.s2 + col]) : 0.0f;
-        // carried part and this token's part apart: they have their own scales
-        const float fade = j.shift ? 1.0f : gam;
-        float inter = 0.0f, dot = 0.0f;
-        for (int r = rg; r < dk; r += 16) {
-            const float x = X[r * kCols + c];
-            inter += qs[r] * x;
-            dot += qs[r] * ks[r];
-            X[r * kCols + c] = gam * x + (j.shift ? gam : 1.0f) * j.up_scale * ks[r] * vv;
+    };
+
+    // ---- state.  Lane (l16, g4) of tile (at, bt) holds rows krow(at) + r
+    // of column vcol(bt)
+    const int vq = NCT == 2 ? 8 : 4;  // distance of a wavefront's column quads
+    const int vc0 = wave * 16 * NCT;
+    const int vcol = vc0 + vq * (l16 >> 2) + (l16 & 3);  // + 4 bt
+    auto krow = [&](int at) { return 32 * (at >> 1) + 8 * g4 + 4 * (at & 1); };
+    f32x4 X[NAT][NCT];
+    const size_t cell = (size_t)bh * dk * dv;
+    float *slot = a.ws ? a.ws + a.ws_job[ji] + ((size_t)(bh * a.nseg + seg) * a.tiles[ji] + tile) * C::BLOCK +
+                             (size_t)wave * NAT * NCT * 256 + lane * 4
+                       : nullptr;
+    const bool has = !SO && (a.nseg > 1 ? tau0 == 0 || tau0 < n : job.X0 != nullptr);
+#pragma unroll
+    for (int at = 0; at < NAT; ++at)
+#pragma unroll
+        for (int bt = 0; bt < NCT; ++bt) {
+            X[at][bt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            if (has) {
+                if (a.nseg > 1) {
+                    X[at][bt] = *(const f32x4 *)(slot + (at * NCT + bt) * 256);
+                } else {
+                    const int c = col0 + vcol + 4 * bt;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (krow(at) + r < dk && c < dv)
+                            X[at][bt][r] = job.X0[cell + (krow(at) + r) * job.rs + c * job.cs];
+                }
+            }
         }
-        red[threadIdx.x] = inter * fade * j.in_scale + dot * j.p_scale * vv;
+
+    // ---- tile copies: 64 granules of LDS per wavefront and instruction, the
+    // swizzle is in the source address.  Rows past the chunk's tokens and
+    // columns past the tensor's read as zero.
+    auto copy = [&](IO *dst, const IO *src, int ld, auto gpr_c, int ncol, int lo, int nc) {
+        constexpr int GPR = decltype(gpr_c)::value;
+        const auto rs = __builtin_amdgcn_make_buffer_rsrc((void *)(src + (size_t)lo * ld), 0,
+                                                          __builtin_amdgcn_readfirstlane(nc * ld * ES), kBuf);
+        static_assert(L * GPR % C::NTH == 0, "whole instructions");
+        constexpr int NI = L * GPR / C::NTH;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int gi = (i * NW + wave) * 64;  // first granule of this instruction
+            const int row = (gi + lane) / GPR, col = (((gi + lane) % GPR) ^ swz<GPR>(row)) * C::EPG;
+            const unsigned off = (unsigned)(((rev ? nc - 1 - row : row) * ld + col) * ES);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr *)(dst + gi * C::EPG), 16,
+                                                     row < nc && col < ncol ? off : kOut, 0, 0, 0);
+        }
+    };
+    // chunk c: tokens tau0 + c L ..., nc of them, the lowest in memory is lo
+    const int nch = tau1 > tau0 ? (tau1 - tau0 + L - 1) / L : 0;
+    auto chunk = [&](int c, int &nc, int &lo) {
+        const int s = tau0 + c * L;
+        nc = min(L, tau1 - s);
+        lo = rev ? n - s - nc : s;
+    };
+    auto load = [&](int c) {
+        int nc, lo;
+        chunk(c, nc, lo);
+        IO *t = tiles[c % NBUF];
+        if constexpr (!SO) copy(t, qg, ldq, std::integral_constant<int, QG>{}, dk, lo, nc);
+        copy(t + L * DKP, kg, ldk, std::integral_constant<int, QG>{}, dk, lo, nc);
+        copy(t + 2 * L * DKP, vg, ldv, std::integral_constant<int, VG>{}, dv - col0, lo, nc);
+    };
+
+    Rows<QG> rows;
+    Cols<QG> cols;
+    rows.init((const IO *)nullptr, l16, g4);
+    cols.init((const IO *)nullptr, l16, g4);
+    weights(L);
+    int held = 0;  // tokens since X was last brought to true scale
+    float sigma = 1.0f;
+    if (NBUF == 2 && nch > 0) load(0);
+    for (int c = 0; c < nch; ++c) {
+        if (NBUF == 1) {
+            __syncthreads();
+            load(c);
+        }
+        __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): this wavefront's copies have landed
         __syncthreads();
-        if (rg == 0 && ok) {
-            float x = 0.0f;
-            for (int i = 0; i < 16; ++i) x += red[c + 16 * i];
-            o[t * j.so.s2 + col] = from_f<IO>(x);
+        if (NBUF == 2 && c + 1 < nch) load(c + 1);
+        int nc, lo;
+        chunk(c, nc, lo);
+        const IO *Qs = tiles[c % NBUF], *Ks = Qs + L * DKP, *Vs = Ks + L * DKP;
+
+        Frag vf[NCT];
+#pragma unroll
+        for (int bt = 0; bt < NCT; ++bt) vf[bt] = col_frag<VG>(Vs, vc0 + 4 * bt, vq, l16, g4);
+
+        if constexpr (!SO) {
+            // read-out of the carried state and scores, one pass over d_qk
+            f32x4 O[2][NCT], S00 = {0, 0, 0, 0}, S10 = S00, S11 = S00;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int bt = 0; bt < NCT; ++bt) O[t][bt] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int kk = 0; kk < NKS; ++kk) {
+                const Frag q0 = rows.get(Qs, 0, kk), q1 = rows.get(Qs, 1, kk);
+                const Frag k0 = rows.get(Ks, 0, kk), k1 = rows.get(Ks, 1, kk);
+                S00 = mfma(k0, q0, S00);
+                S10 = mfma(k0, q1, S10);
+                S11 = mfma(k1, q1, S11);
+#pragma unroll
+                for (int bt = 0; bt < NCT; ++bt) {
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = X[2 * kk + (e >> 2)][bt][e & 3];
+                    Frag xf;
+                    pack(x, xf);
+                    O[0][bt] = mfma(xf, q0, O[0][bt]);
+                    O[1][bt] = mfma(xf, q1, O[1][bt]);
+                }
+            }
+            float p0[8], p1[8];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const bool seen = l16 >= 4 * g4 + r;  // token j <= i
+                p0[r] = seen ? S00[r] * dg[r] : 0.0f;
+                p0[4 + r] = 0.0f;
+                p1[r] = S10[r] * db[r];
+                p1[4 + r] = seen ? S11[r] * dg[r] : 0.0f;
+            }
+            Frag P0, P1;
+            pack(p0, P0);
+            pack(p1, P1);
+            const auto os = __builtin_amdgcn_make_buffer_rsrc((void *)(og + (size_t)lo * ldo), 0,
+                                                              __builtin_amdgcn_readfirstlane(nc * ldo * ES), kBuf);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                float y[4 * NCT];
+#pragma unroll
+                for (int bt = 0; bt < NCT; ++bt) {
+                    O[t][bt] = mfma(vf[bt], t ? P1 : P0, O[t][bt] * ((t ? fade1 : fade0) * sigma));
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) y[4 * bt + r] = O[t][bt][r];
+                }
+                // this lane: token 16 t + l16, columns vc0 + vq g4 + (0 .. 4 NCT - 1)
+                const int row = 16 * t + l16, col = vc0 + vq * g4;
+                const unsigned off = (unsigned)(((rev ? nc - 1 - row : row) * ldo + col) * ES);
+                const unsigned at = row < nc && col0 + col < dv ? off : kOut;
+                if constexpr (ES == 4) {
+#pragma unroll
+                    for (int i = 0; i < NCT; ++i)
+                        __builtin_amdgcn_raw_buffer_store_b128(
+                            __builtin_bit_cast(u32x4, f32x4{y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]}), os,
+                            at == kOut ? kOut : at + 16 * i, 0, 0);
+                } else if constexpr (NCT == 2) {
+                    bf16x8 o8;
+                    pack(y, o8);
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o8), os, at, 0, 0);
+                } else {
+                    const float z[8] = {y[0], y[1], y[2], y[3], 0, 0, 0, 0};
+                    bf16x8 o8;
+                    pack(z, o8);
+                    const u32x4 u = __builtin_bit_cast(u32x4, o8);
+                    __builtin_amdgcn_raw_buffer_store_b64(u32x2{u[0], u[1]}, os, at, 0, 0);
+                }
+            }
+        }
+
+        // state update: X is held divided by sigma = e^{g held}, so that a chunk's
+        // decay costs nothing and no rounded factor is applied again and again
+        held += nc;
+        sigma = gpow(held);
+        if (!(sigma >= kRenorm && sigma <= 1.0f / kRenorm)) {
+#pragma unroll
+            for (int at = 0; at < NAT; ++at)
+#pragma unroll
+                for (int bt = 0; bt < NCT; ++bt) X[at][bt] *= sigma;
+            held = 0;
+            sigma = 1.0f;
+        }
+        const float inv = gpow(-held);
+        if (nc < L) weights(nc);
+        Frag vw[NCT][PARTS];
+#pragma unroll
+        for (int bt = 0; bt < NCT; ++bt) {
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = (float)vf[bt][e] * (w[e] * inv);
+            split(x, vw[bt]);
+        }
+#pragma unroll
+        for (int at = 0; at < NAT; at += 2) {
+            Frag kf[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) kf[u] = cols.get(Ks, at >> 1, u);
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int bt = 0; bt < NCT; ++bt) X[at + u][bt] = mfma(kf[u], vw[bt][q], X[at + u][bt]);
         }
     }
-    if (ok)
-        for (long long t = n + rg; t < a.T; t += 16) o[t * j.so.s2 + col] = from_f<IO>(0.0f);
-    if (ok && j.Xn)
-        for (int r = rg; r < dk; r += 16) j.Xn[st + r * j.rs + col * j.cs] = X[r * kCols + c];
+
+    // ---- state out
+#pragma unroll
+    for (int at = 0; at < NAT; ++at)
+#pragma unroll
+        for (int bt = 0; bt < NCT; ++bt) X[at][bt] *= sigma;
+    if constexpr (SO) {
+        // the segment's own sum goes where the next one's incoming state will be
+        float *next = slot + (size_t)a.tiles[ji] * C::BLOCK;
+#pragma unroll
+        for (int at = 0; at < NAT; ++at)
+#pragma unroll
+            for (int bt = 0; bt < NCT; ++bt) *(f32x4 *)(next + (at * NCT + bt) * 256) = X[at][bt];
+    } else {
+        const int last = n > 0 ? (n - 1) / a.seg_len : 0;
+        if (job.Xn && seg == last) {
+#pragma unroll
+            for (int at = 0; at < NAT; ++at)
+#pragma unroll
+                for (int bt = 0; bt < NCT; ++bt) {
+                    const int c = col0 + vcol + 4 * bt;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (krow(at) + r < dk && c < dv)
+                            job.Xn[cell + (krow(at) + r) * job.rs + c * job.cs] = X[at][bt][r];
+                }
+        }
+        // rows behind the sequence's length
+        const int z1 = min(tau0 + a.seg_len, T);
+        constexpr int QPR = BV / 4;  // quads of a row
+        for (int e = tid; e < (z1 - max(n, tau0)) * QPR; e += C::NTH) {
+            const long long t = max(n, tau0) + e / QPR;
+            const int c = e % QPR * 4;
+            if (col0 + c < dv) {
+                if constexpr (ES == 4)
+                    *(f32x4 *)(og + t * ldo + c) = f32x4{0, 0, 0, 0};
+                else
+                    *(u32x2 *)(og + t * ldo + c) = u32x2{0, 0};
+            }
+        }
+    }
+}
+
+// Segments' own sums -> their incoming states: in_0 = X0, in_{s+1} = e^{g
+// seg_len} in_s + own_s, in place, elementwise; one thread for 4 rows of a column.
+template <int DKP, int NCT, int NW>
+__global__ __launch_bounds__(256) void linattn_scan_kernel(KArgs a) {
+    constexpr int BV = 16 * NCT * NW, BLOCK = DKP * BV, NAT = DKP / 16;
+    const int e = blockIdx.x * 256 + threadIdx.x;  // quad of the state's blocks
+    const int bh = blockIdx.y, ji = blockIdx.z;
+    const LinJob &job = a.job[ji];
+    if (e >= a.tiles[ji] * (BLOCK / 4)) return;
+    const int b = bh / a.H, h = bh % a.H;
+    const int n = a.lengths ? max(0, min(a.lengths[b], a.T)) : a.T;
+    const int tile = e / (BLOCK / 4), x = e % (BLOCK / 4);
+    const int lane = x & 63, l16 = lane & 15, g4 = lane >> 4;
+    const int bt = (x >> 6) % NCT, at = (x >> 6) / NCT % NAT, wave = x / (64 * NCT * NAT);
+    const int row = 32 * (at >> 1) + 8 * g4 + 4 * (at & 1);
+    const int col = tile * BV + wave * 16 * NCT + (NCT == 2 ? 8 : 4) * (l16 >> 2) + (l16 & 3) + 4 * bt;
+    const float f = __builtin_amdgcn_exp2f(decay_log2(a.g[h]) * (float)a.seg_len);
+    f32x4 run = {0, 0, 0, 0};
+    if (job.X0)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (row + r < job.dk && col < job.dv)
+                run[r] = job.X0[(size_t)bh * job.dk * job.dv + (row + r) * job.rs + col * job.cs];
+    const size_t step = (size_t)a.tiles[ji] * BLOCK;
+    float *s = a.ws + a.ws_job[ji] + (size_t)bh * a.nseg * step + (size_t)e * 4;
+    *(f32x4 *)s = run;
+    for (int i = 1; i < a.nseg && (long long)i * a.seg_len < n; ++i) {
+        s += step;
+        run = run * f + *(const f32x4 *)s;
+        *(f32x4 *)s = run;
+    }
+}
+
+// ---- plans
+
+// Kernel shape of a job: rows padded to 64, 128, 256 or 512; 64 columns a
+// workgroup (16 a wavefront) for up to 64 columns and where 512 rows leave no
+// registers for more, else 128 (32 a wavefront).
+int dkp_of(int dk) { return dk <= 64 ? 64 : dk <= 128 ? 128 : dk <= 256 ? 256 : 512; }
+int bv_of(int dkp, int dv) { return dv <= 64 || dkp == 512 ? 64 : 128; }
+
+struct Shape {
+    int dkp, bv, tiles;
+};
+Shape shape_of(int dk, int dv) {
+    Shape s;
+    s.dkp = dkp_of(dk);
+    s.bv = bv_of(s.dkp, dv);
+    s.tiles = (dv + s.bv - 1) / s.bv;
+    return s;
+}
+
+// Enough segments for two workgroups on every compute unit, each at least four
+// chunks long; one where the column blocks alone give them.
+SegPlan seg_plan(long long wgs, int T) {
+    const int nch = (T + L - 1) / L;
+    long long want = wgs >= 256 ? 1 : (512 + wgs - 1) / wgs;
+    if (want > nch / 4) want = nch / 4;
+    if (want < 1) want = 1;
+    SegPlan p;
+    const int cps = (int)((nch + want - 1) / want);
+    p.seg_len = cps * L;
+    p.nseg = (T + p.seg_len - 1) / p.seg_len;
+    return p;
+}
+
+// jobs' rows and columns of a call
+int job_dims(int dk, int dv, int backward, int (*d)[2]) {
+    d[0][0] = backward ? dv : dk;
+    d[0][1] = backward ? dk : dv;
+    d[1][0] = dk, d[1][1] = dv;
+    d[2][0] = dv, d[2][1] = dk;
+    return backward ? 3 : 1;
+}
+
+SegPlan call_plan(int B, int H, int T, int dk, int dv, int backward) {
+    int d[3][2];
+    const int n = job_dims(dk, dv, backward, d);
+    long long wgs = 0;
+    for (int i = 0; i < n; ++i) wgs += shape_of(d[i][0], d[i][1]).tiles;
+    return seg_plan(wgs * B * H, T);
+}
+
+template <typename IO, int DKP, int NCT, int NW>
+hipError_t launch_shape(const KArgs &a, hipStream_t s) {
+    const int cells = a.B * a.H;
+    if (a.nseg > 1) {
+        linattn_kernel<IO, DKP, NCT, NW, true><<<dim3((unsigned)(cells * (a.nseg - 1) * a.tiles_all)), 64 * NW, 0, s>>>(a);
+        int most = 0;
+        for (int i = 0; i < a.njob; ++i) most = a.tiles[i] > most ? a.tiles[i] : most;
+        const int quads = most * DKP * 4 * NCT * NW;
+        linattn_scan_kernel<DKP, NCT, NW><<<dim3((unsigned)((quads + 255) / 256), (unsigned)cells, (unsigned)a.njob), 256, 0, s>>>(a);
+    }
+    linattn_kernel<IO, DKP, NCT, NW, false><<<dim3((unsigned)(cells * a.nseg * a.tiles_all)), 64 * NW, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <typename IO>
+hipError_t launch_io(const LinArgs &in, hipStream_t s) {
+    KArgs a{};
+    a.g = in.g;
+    a.lengths = in.lengths;
+    a.B = in.B, a.H = in.H, a.T = in.T;
+    const SegPlan p = call_plan(in.B, in.H, in.T, in.njob > 1 ? in.job[1].dk : in.job[0].dk,
+                                in.njob > 1 ? in.job[1].dv : in.job[0].dv, in.njob > 1);
+    a.nseg = p.nseg, a.seg_len = p.seg_len;
+    size_t ws = 0, at[3];
+    for (int i = 0; i < in.njob; ++i) {
+        const Shape f = shape_of(in.job[i].dk, in.job[i].dv);
+        at[i] = ws;
+        ws += (size_t)in.B * in.H * p.nseg * f.tiles * f.dkp * f.bv;
+    }
+    // jobs of one kernel shape go in one launch
+    bool done[3] = {false, false, false};
+    for (int i = 0; i < in.njob; ++i) {
+        if (done[i]) continue;
+        const Shape f = shape_of(in.job[i].dk, in.job[i].dv);
+        a.njob = a.tiles_all = 0;
+        for (int k = i; k < in.njob; ++k) {
+            const Shape fk = shape_of(in.job[k].dk, in.job[k].dv);
+            if (done[k] || fk.dkp != f.dkp || fk.bv != f.bv) continue;
+            done[k] = true;
+            a.job[a.njob] = in.job[k];
+            a.tiles[a.njob] = fk.tiles;
+            a.ws_job[a.njob] = at[k];
+            a.tiles_all += fk.tiles;
+            ++a.njob;
+        }
+        a.ws = p.nseg > 1 ? in.ws : nullptr;
+        hipError_t e;
+        if (f.dkp == 64)
+            e = f.bv == 64 ? launch_shape<IO, 64, 1, 4>(a, s) : launch_shape<IO, 64, 2, 4>(a, s);
+        else if (f.dkp == 128)
+            e = f.bv == 64 ? launch_shape<IO, 128, 1, 4>(a, s) : launch_shape<IO, 128, 2, 4>(a, s);
+        else if (f.dkp == 256)
+            e = f.bv == 64 ? launch_shape<IO, 256, 1, 4>(a, s) : launch_shape<IO, 256, 2, 4>(a, s);
+        else
+            e = launch_shape<IO, 512, 1, 4>(a, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace
 
-size_t linattn_workspace_floats(int, int, int, int, int, int, int) { return 0; }
+size_t linattn_workspace_floats(int B, int H, int T, int dk, int dv, int, int backward) {
+    const SegPlan p = call_plan(B, H, T, dk, dv, backward);
+    if (p.nseg == 1) return 0;
+    int d[3][2];
+    const int n = job_dims(dk, dv, backward, d);
+    size_t f = 0;
+    for (int i = 0; i < n; ++i) {
+        const Shape s = shape_of(d[i][0], d[i][1]);
+        f += (size_t)B * H * p.nseg * s.tiles * s.dkp * s.bv;
+    }
+    return f;
+}
 
 hipError_t launch_linattn(const LinArgs &a, int io_bf16, hipStream_t s) {
-    int dv = 0, dk = 0;
-    for (int i = 0; i < a.njob; ++i) {
-        dv = a.job[i].dv > dv ? a.job[i].dv : dv;
-        dk = a.job[i].dk > dk ? a.job[i].dk : dk;
-    }
-    const int ntile = (dv + kCols - 1) / kCols;
-    const size_t lds = ((size_t)dk * kCols + 2 * dk + 256) * 4;
-    const dim3 grid((unsigned)(a.njob * a.B * a.H * ntile));
-    if (io_bf16)
-        linattn_rec_kernel<bf16><<<grid, 256, lds, s>>>(a, ntile);
-    else
-        linattn_rec_kernel<float><<<grid, 256, lds, s>>>(a, ntile);
-    return hipGetLastError();
+    return io_bf16 ? launch_io<bf16>(a, s) : launch_io<float>(a, s);
 }
 
 }  // namespace mlstm
