@@ -143,6 +143,14 @@ __device__ __forceinline__ s16x4 tr_read(const bf16 *p) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
 }
 
+// Wait until at most N of this wavefront's memory operations are outstanding
+// (they complete in order).
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+    static_assert(N < 16, "four bits here");
+    __builtin_amdgcn_s_waitcnt(0x0f70 | N);
+}
+
 // Whole-granule reads of a row: d_qk index 32 kk + 8 g4 + (0..7) of rows
 // l16 and 16 + l16.  The swizzle touches the low four bits of the granule
 // number at most, so a few addresses and constant offsets serve all kk.
@@ -252,7 +260,11 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU)) void lina
     constexpr int NAT = C::NAT, NKS = C::NKS, QG = C::QG, VG = C::VG, BV = C::BV, NBUF = C::NBUF;
     constexpr int PARTS = Types<IO>::PARTS;
     constexpr int ES = (int)sizeof(IO);
-    __shared__ __attribute__((aligned(16))) IO tiles[NBUF][L * (2 * DKP + BV)];
+    // Q, K and V tiles of a chunk, double buffered where two fit.  Two arrays and
+    // a loop over pairs of chunks, not one array indexed by parity: the compiler
+    // waits for a copy in flight before any LDS read that may alias it.
+    __shared__ __attribute__((aligned(16))) IO tile0[L * (2 * DKP + BV)];
+    __shared__ __attribute__((aligned(16))) IO tile1[NBUF == 2 ? L * (2 * DKP + BV) : 16];
 
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g4 = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -310,27 +322,38 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU)) void lina
     auto krow = [&](int at) { return 32 * (at >> 1) + 8 * g4 + 4 * (at & 1); };
     f32x4 X[NAT][NCT];
     const size_t cell = (size_t)bh * dk * dv;
+    // byte offset of row krow(at), column vcol + 4 bt in one (b, h)'s state as the caller has it
+    const int rs = (int)job.rs * 4, cs = (int)job.cs * 4;
+    auto state_at = [&](int at, int bt) {
+        return krow(at) < dk && col0 + vcol + 4 * bt < dv ? (unsigned)(krow(at) * rs + (col0 + vcol + 4 * bt) * cs)
+                                                          : kOut;
+    };
     float *slot = a.ws ? a.ws + a.ws_job[ji] + ((size_t)(bh * a.nseg + seg) * a.tiles[ji] + tile) * C::BLOCK +
                              (size_t)wave * NAT * NCT * 256 + lane * 4
                        : nullptr;
-    const bool has = !SO && (a.nseg > 1 ? tau0 == 0 || tau0 < n : job.X0 != nullptr);
+    if (!SO && a.nseg > 1 && (tau0 == 0 || tau0 < n)) {
 #pragma unroll
-    for (int at = 0; at < NAT; ++at)
+        for (int at = 0; at < NAT; ++at)
 #pragma unroll
-        for (int bt = 0; bt < NCT; ++bt) {
-            X[at][bt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            if (has) {
-                if (a.nseg > 1) {
-                    X[at][bt] = *(const f32x4 *)(slot + (at * NCT + bt) * 256);
-                } else {
-                    const int c = col0 + vcol + 4 * bt;
+            for (int bt = 0; bt < NCT; ++bt) X[at][bt] = *(const f32x4 *)(slot + (at * NCT + bt) * 256);
+    } else if (!SO && a.nseg == 1 && job.X0) {
+        const auto xs = __builtin_amdgcn_make_buffer_rsrc((void *)(job.X0 + cell), 0, dk * dv * 4, kBuf);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (krow(at) + r < dk && c < dv)
-                            X[at][bt][r] = job.X0[cell + (krow(at) + r) * job.rs + c * job.cs];
-                }
+        for (int at = 0; at < NAT; ++at)
+#pragma unroll
+            for (int bt = 0; bt < NCT; ++bt) {
+                const unsigned off = state_at(at, bt);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    X[at][bt][r] = __uint_as_float(
+                        __builtin_amdgcn_raw_buffer_load_b32(xs, off == kOut ? kOut : off + r * rs, 0, 0));
             }
-        }
+    } else {
+#pragma unroll
+        for (int at = 0; at < NAT; ++at)
+#pragma unroll
+            for (int bt = 0; bt < NCT; ++bt) X[at][bt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
 
     // ---- tile copies: 64 granules of LDS per wavefront and instruction, the
     // swizzle is in the source address.  Rows past the chunk's tokens and
@@ -357,10 +380,9 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU)) void lina
         nc = min(L, tau1 - s);
         lo = rev ? n - s - nc : s;
     };
-    auto load = [&](int c) {
+    auto load = [&](IO *t, int c) {
         int nc, lo;
         chunk(c, nc, lo);
-        IO *t = tiles[c % NBUF];
         if constexpr (!SO) copy(t, qg, ldq, std::integral_constant<int, QG>{}, dk, lo, nc);
         copy(t + L * DKP, kg, ldk, std::integral_constant<int, QG>{}, dk, lo, nc);
         copy(t + 2 * L * DKP, vg, ldv, std::integral_constant<int, VG>{}, dv - col0, lo, nc);
@@ -373,18 +395,24 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU)) void lina
     weights(L);
     int held = 0;  // tokens since X was last brought to true scale
     float sigma = 1.0f;
-    if (NBUF == 2 && nch > 0) load(0);
-    for (int c = 0; c < nch; ++c) {
+    // memory operations of a chunk issued after its copies of the next one: the stores of o
+    constexpr int NST = SO ? 0 : 2 * (ES == 4 ? NCT : 1);
+    auto body = [&](IO *cur, IO *next, int c) {
         if (NBUF == 1) {
             __syncthreads();
-            load(c);
+            load(cur, c);
+            wait_vm<0>();
+        } else if (c == 0) {
+            wait_vm<0>();
+        } else {
+            wait_vm<NST>();  // this wavefront's copies have landed
         }
-        __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): this wavefront's copies have landed
         __syncthreads();
-        if (NBUF == 2 && c + 1 < nch) load(c + 1);
+        if (NBUF == 2 && c + 1 < nch) load(next, c + 1);
+        __builtin_amdgcn_sched_barrier(0);
         int nc, lo;
         chunk(c, nc, lo);
-        const IO *Qs = tiles[c % NBUF], *Ks = Qs + L * DKP, *Vs = Ks + L * DKP;
+        const IO *Qs = cur, *Ks = Qs + L * DKP, *Vs = Ks + L * DKP;
 
         Frag vf[NCT];
 #pragma unroll
@@ -496,6 +524,11 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU)) void lina
 #pragma unroll
                     for (int bt = 0; bt < NCT; ++bt) X[at + u][bt] = mfma(kf[u], vw[bt][q], X[at + u][bt]);
         }
+    };
+    if (NBUF == 2 && nch > 0) load(tile0, 0);
+    for (int c = 0; c < nch; c += 2) {
+        body(tile0, tile1, c);
+        if (c + 1 < nch) body(NBUF == 2 ? tile1 : tile0, tile0, c + 1);
     }
 
     // ---- state out
@@ -513,15 +546,16 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU)) void lina
     } else {
         const int last = n > 0 ? (n - 1) / a.seg_len : 0;
         if (job.Xn && seg == last) {
+            const auto xs = __builtin_amdgcn_make_buffer_rsrc((void *)(job.Xn + cell), 0, dk * dv * 4, kBuf);
 #pragma unroll
             for (int at = 0; at < NAT; ++at)
 #pragma unroll
                 for (int bt = 0; bt < NCT; ++bt) {
-                    const int c = col0 + vcol + 4 * bt;
+                    const unsigned off = state_at(at, bt);
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        if (krow(at) + r < dk && c < dv)
-                            job.Xn[cell + (krow(at) + r) * job.rs + c * job.cs] = X[at][bt][r];
+                        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(X[at][bt][r]), xs,
+                                                              off == kOut ? kOut : off + r * rs, 0, 0);
                 }
         }
         // rows behind the sequence's length
