@@ -50,7 +50,7 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr int L = 32;           // tokens of a chunk
 constexpr int kBuf = 0x00020000; // word 3 of a raw, range-checked buffer descriptor
-constexpr unsigned kOut = 0xfffffff0u;  // an offset past any range: reads zero, writes nothing
+constexpr unsigned kOut = 0xf0000000u;  // an offset past any range: reads zero, writes nothing
 constexpr size_t kLds = 160 * 1024;
 constexpr float kRenorm = 1.0f / 65536.0f;  // sigma's least value
 
@@ -110,23 +110,23 @@ __device__ __forceinline__ void pack(const float *x, f32x8 &f) {
     for (int e = 0; e < 8; ++e) f[e] = x[e];
 }
 
-// 8 floats as a sum of PARTS operands: each part is the rounded rest of the one before
-__device__ __forceinline__ void split(float *x, bf16x8 *f) {
+// Two floats as a sum of PARTS roundings, elements 2 p and 2 p + 1 of PARTS
+// operands: each part is the rounded rest of the one before
+__device__ __forceinline__ void split2(float x0, float x1, bf16x8 *f, int p) {
 #pragma unroll
-    for (int q = 0; q < 3; ++q)
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            const bf16x2 h = __builtin_convertvector((f32x2{x[2 * p], x[2 * p + 1]}), bf16x2);
-            f[q][2 * p] = h[0];
-            f[q][2 * p + 1] = h[1];
-            if (q < 2) {
-                const unsigned b = __builtin_bit_cast(unsigned, h);
-                x[2 * p] -= __uint_as_float(b << 16);
-                x[2 * p + 1] -= __uint_as_float(b & 0xffff0000u);
-            }
-        }
+    for (int q = 0; q < 3; ++q) {
+        const bf16x2 h = __builtin_convertvector((f32x2{x0, x1}), bf16x2);
+        f[q][2 * p] = h[0];
+        f[q][2 * p + 1] = h[1];
+        const unsigned b = __builtin_bit_cast(unsigned, h);
+        x0 -= __uint_as_float(b << 16);
+        x1 -= __uint_as_float(b & 0xffff0000u);
+    }
 }
-__device__ __forceinline__ void split(float *x, f32x8 *f) { pack(x, f[0]); }
+__device__ __forceinline__ void split2(float x0, float x1, f32x8 *f, int p) {
+    f[0][2 * p] = x0;
+    f[0][2 * p + 1] = x1;
+}
 
 // Granule swizzle of a tile with GPR granules a row: a row's granule p is
 // stored at p ^ swz(row).  Rows are read whole-granule, 16 rows at a time at one
@@ -302,17 +302,12 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU)) void lina
         dg[r] = gpow(max(d, 0)) * job.p_scale;
         db[r] = gpow(16 + d) * job.p_scale;
     }
-    const float fade0 = gpow(l16 + 1 - job.shift) * job.in_scale;
-    const float fade1 = gpow(16 + l16 + 1 - job.shift) * job.in_scale;
-    // weights of this lane's tokens in the state update, in a chunk of nc tokens
+    // weights of this lane's tokens in the state update.  A chunk of nc < L
+    // tokens fills its last rows, behind rows of zeros, so they are always these.
     float w[8];
-    auto weights = [&](int nc) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int j = 16 * (e >> 2) + 4 * g4 + (e & 3);
-            w[e] = j < nc ? gpow(nc - 1 + job.shift - j) * job.up_scale : 0.0f;
-        }
-    };
+    for (int e = 0; e < 8; ++e)
+        w[e] = gpow(L - 1 + job.shift - (16 * (e >> 2) + 4 * g4 + (e & 3))) * job.up_scale;
 
     // ---- state.  Lane (l16, g4) of tile (at, bt) holds rows krow(at) + r
     // of column vcol(bt)
@@ -355,48 +350,74 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU)) void lina
             for (int bt = 0; bt < NCT; ++bt) X[at][bt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 
-    // ---- tile copies: 64 granules of LDS per wavefront and instruction, the
-    // swizzle is in the source address.  Rows past the chunk's tokens and
-    // columns past the tensor's read as zero.
-    auto copy = [&](IO *dst, const IO *src, int ld, auto gpr_c, int ncol, int lo, int nc) {
-        constexpr int GPR = decltype(gpr_c)::value;
-        const auto rs = __builtin_amdgcn_make_buffer_rsrc((void *)(src + (size_t)lo * ld), 0,
-                                                          __builtin_amdgcn_readfirstlane(nc * ld * ES), kBuf);
-        static_assert(L * GPR % C::NTH == 0, "whole instructions");
-        constexpr int NI = L * GPR / C::NTH;
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int gi = (i * NW + wave) * 64;  // first granule of this instruction
-            const int row = (gi + lane) / GPR, col = (((gi + lane) % GPR) ^ swz<GPR>(row)) * C::EPG;
-            const unsigned off = (unsigned)(((rev ? nc - 1 - row : row) * ld + col) * ES);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr *)(dst + gi * C::EPG), 16,
-                                                     row < nc && col < ncol ? off : kOut, 0, 0, 0);
-        }
-    };
-    // chunk c: tokens tau0 + c L ..., nc of them, the lowest in memory is lo
+    // ---- chunks.  Chunk c has tokens tau0 + c L ..., nc of them, the lowest in
+    // memory is lo; row r of its tiles is local token r - (L - nc).
     const int nch = tau1 > tau0 ? (tau1 - tau0 + L - 1) / L : 0;
     auto chunk = [&](int c, int &nc, int &lo) {
         const int s = tau0 + c * L;
         nc = min(L, tau1 - s);
         lo = rev ? n - s - nc : s;
     };
+    // Byte offset of (row, element col) from token lo: rows run up or down in
+    // memory.  Rows in front of a short chunk come out below zero or past
+    // nc rows: either way out of the descriptor's range, so they read as zero
+    // and are not written.
+    auto row_off = [&](int row, int ld, int col) { return (unsigned)(((rev ? L - 1 - row : row) * ld + col) * ES); };
+    auto short_by = [&](int nc, int ld) { return rev ? 0u : (unsigned)((L - nc) * ld * ES); };
+    // Tile copies: 64 granules of LDS per wavefront and instruction, the swizzle
+    // is in the source address; columns past the tensor's read as zero.  The
+    // swizzle repeats every 16 rows, so a few per-lane offsets serve all instructions.
+    constexpr int QPER = 16 * QG / C::NTH > 1 ? 16 * QG / C::NTH : 1;
+    constexpr int VPER = 16 * VG / C::NTH > 1 ? 16 * VG / C::NTH : 1;
+    auto copy_offsets = [&](unsigned *off, int ld, int ncol, auto gpr_c) {
+        constexpr int GPR = decltype(gpr_c)::value;
+        static_assert(L * GPR % C::NTH == 0, "whole instructions");
+#pragma unroll
+        for (int i = 0; i < (16 * GPR / C::NTH > 1 ? 16 * GPR / C::NTH : 1); ++i) {
+            const int gi = i * C::NTH + tid, row = gi / GPR, col = ((gi % GPR) ^ swz<GPR>(row)) * C::EPG;
+            off[i] = col < ncol ? row_off(row & (L - 1), ld, col) : kOut;
+        }
+    };
+    auto copy = [&](IO *dst, const IO *src, int ld, const unsigned *off, auto gpr_c, int lo, int nc) {
+        constexpr int GPR = decltype(gpr_c)::value, NI = L * GPR / C::NTH, RPI = C::NTH / GPR;
+        constexpr int PER = 16 * GPR / C::NTH > 1 ? 16 * GPR / C::NTH : 1;
+        const auto rs = __builtin_amdgcn_make_buffer_rsrc((void *)(src + (size_t)lo * ld), 0,
+                                                          __builtin_amdgcn_readfirstlane(nc * ld * ES), kBuf);
+        const unsigned sb = short_by(nc, ld), step = (unsigned)((rev ? -RPI : RPI) * ld * ES);
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr *)(dst + (i * NW + wave) * 64 * C::EPG), 16,
+                                                     off[i % PER] + (i / PER * PER * step - sb), 0, 0, 0);
+    };
+    using QGc = std::integral_constant<int, QG>;
+    using VGc = std::integral_constant<int, VG>;
+    unsigned qoff[QPER], koff[QPER], voff[VPER];
+    if constexpr (!SO) copy_offsets(qoff, ldq, dk, QGc{});
+    copy_offsets(koff, ldk, dk, QGc{});
+    copy_offsets(voff, ldv, dv - col0, VGc{});
     auto load = [&](IO *t, int c) {
         int nc, lo;
         chunk(c, nc, lo);
-        if constexpr (!SO) copy(t, qg, ldq, std::integral_constant<int, QG>{}, dk, lo, nc);
-        copy(t + L * DKP, kg, ldk, std::integral_constant<int, QG>{}, dk, lo, nc);
-        copy(t + 2 * L * DKP, vg, ldv, std::integral_constant<int, VG>{}, dv - col0, lo, nc);
+        if constexpr (!SO) copy(t, qg, ldq, qoff, QGc{}, lo, nc);
+        copy(t + L * DKP, kg, ldk, koff, QGc{}, lo, nc);
+        copy(t + 2 * L * DKP, vg, ldv, voff, VGc{}, lo, nc);
     };
 
     Rows<QG> rows;
     Cols<QG> cols;
     rows.init((const IO *)nullptr, l16, g4);
     cols.init((const IO *)nullptr, l16, g4);
-    weights(L);
-    int held = 0;  // tokens since X was last brought to true scale
+    // this lane's outputs: tokens l16 and 16 + l16, columns vc0 + vq g4 + (0 .. 4 NCT - 1)
+    const int ocol = vc0 + vq * g4;
+    const bool ook = col0 + ocol < dv;
+    int held = 0;  // X is held divided by sigma = e^{g held}
     float sigma = 1.0f;
     // memory operations of a chunk issued after its copies of the next one: the stores of o
     constexpr int NST = SO ? 0 : 2 * (ES == 4 ? NCT : 1);
+    // Order of a chunk's work: each step's LDS reads are issued a step ahead of
+    // the products that use them, and the elementwise work (w v, P, the
+    // output) sits between products that do not depend on it.  sched_barrier
+    // keeps the steps apart; within one the compiler orders freely.
     auto body = [&](IO *cur, IO *next, int c) {
         if (NBUF == 1) {
             __syncthreads();
@@ -413,36 +434,87 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU)) void lina
         int nc, lo;
         chunk(c, nc, lo);
         const IO *Qs = cur, *Ks = Qs + L * DKP, *Vs = Ks + L * DKP;
+        // The decay of X costs nothing while sigma carries it, and no rounded
+        // factor is applied again and again; below kRenorm it is folded in.
+        const float fade = sigma * job.in_scale;
+        held += nc;
+        sigma = gpow(held);
+        const bool renorm = !(sigma >= kRenorm && sigma <= 1.0f / kRenorm);
+        const float fold = sigma;
+        if (renorm) {
+            held = 0;
+            sigma = 1.0f;
+        }
+        const float inv = gpow(-held);
 
-        Frag vf[NCT];
+        Frag vf[NCT], vw[NCT][PARTS];
 #pragma unroll
         for (int bt = 0; bt < NCT; ++bt) vf[bt] = col_frag<VG>(Vs, vc0 + 4 * bt, vq, l16, g4);
-
+        // parts of w v: elements 2 p and 2 p + 1 of tile bt
+        auto weigh = [&](int bt, int p) {
+            float x0 = (float)vf[bt][2 * p] * (w[2 * p] * inv), x1 = (float)vf[bt][2 * p + 1] * (w[2 * p + 1] * inv);
+            split2(x0, x1, vw[bt], p);
+        };
+        Frag kf[2][2];
+        f32x4 O[2][NCT], S00 = {0, 0, 0, 0}, S10 = S00, S11 = S00;
         if constexpr (!SO) {
             // read-out of the carried state and scores, one pass over d_qk
-            f32x4 O[2][NCT], S00 = {0, 0, 0, 0}, S10 = S00, S11 = S00;
+            Frag q[2][2], k[2][2];
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < 2; ++t) {
+                q[0][t] = rows.get(Qs, t, 0);
+                k[0][t] = rows.get(Ks, t, 0);
 #pragma unroll
                 for (int bt = 0; bt < NCT; ++bt) O[t][bt] = f32x4{0, 0, 0, 0};
+            }
 #pragma unroll
             for (int kk = 0; kk < NKS; ++kk) {
-                const Frag q0 = rows.get(Qs, 0, kk), q1 = rows.get(Qs, 1, kk);
-                const Frag k0 = rows.get(Ks, 0, kk), k1 = rows.get(Ks, 1, kk);
-                S00 = mfma(k0, q0, S00);
-                S10 = mfma(k0, q1, S10);
-                S11 = mfma(k1, q1, S11);
+                __builtin_amdgcn_sched_barrier(0);
+                const int u = kk & 1;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (kk + 1 < NKS) {
+                        q[u ^ 1][t] = rows.get(Qs, t, kk + 1);
+                        k[u ^ 1][t] = rows.get(Ks, t, kk + 1);
+                    } else {
+                        kf[0][t] = cols.get(Ks, 0, t);
+                    }
+                }
+                Frag xf[NCT];
 #pragma unroll
                 for (int bt = 0; bt < NCT; ++bt) {
                     float x[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[e] = X[2 * kk + (e >> 2)][bt][e & 3];
-                    Frag xf;
-                    pack(x, xf);
-                    O[0][bt] = mfma(xf, q0, O[0][bt]);
-                    O[1][bt] = mfma(xf, q1, O[1][bt]);
+                    pack(x, xf[bt]);
                 }
+                S00 = mfma(k[u][0], q[u][0], S00);
+                S10 = mfma(k[u][0], q[u][1], S10);
+                S11 = mfma(k[u][1], q[u][1], S11);
+#pragma unroll
+                for (int bt = 0; bt < NCT; ++bt)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) O[t][bt] = mfma(xf[bt], q[u][t], O[t][bt]);
+#pragma unroll
+                for (int i = 0; i < 4 * NCT; ++i)
+                    if (i * NKS / (4 * NCT) == kk) weigh(i >> 2, i & 3);
             }
+        } else {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) kf[0][t] = cols.get(Ks, 0, t);
+#pragma unroll
+            for (int i = 0; i < 4 * NCT; ++i) weigh(i >> 2, i & 3);
+        }
+        if (renorm) {
+#pragma unroll
+            for (int at = 0; at < NAT; ++at)
+#pragma unroll
+                for (int bt = 0; bt < NCT; ++bt) X[at][bt] *= fold;
+        }
+
+        // the output, in three pieces that the state update's steps take along
+        Frag P[2];
+        auto scores = [&]() {
             float p0[8], p1[8];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
@@ -452,78 +524,68 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU)) void lina
                 p1[r] = S10[r] * db[r];
                 p1[4 + r] = seen ? S11[r] * dg[r] : 0.0f;
             }
-            Frag P0, P1;
-            pack(p0, P0);
-            pack(p1, P1);
-            const auto os = __builtin_amdgcn_make_buffer_rsrc((void *)(og + (size_t)lo * ldo), 0,
-                                                              __builtin_amdgcn_readfirstlane(nc * ldo * ES), kBuf);
+            pack(p0, P[0]);
+            pack(p1, P[1]);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                float y[4 * NCT];
+                // steps since the state was carried in; rows in front of a short chunk are not tokens
+                const float f = gpow(max(16 * t + l16 + 1 - job.shift - (L - nc), 0)) * fade;
 #pragma unroll
-                for (int bt = 0; bt < NCT; ++bt) {
-                    O[t][bt] = mfma(vf[bt], t ? P1 : P0, O[t][bt] * ((t ? fade1 : fade0) * sigma));
+                for (int bt = 0; bt < NCT; ++bt) O[t][bt] *= f;
+            }
+        };
+        auto values = [&]() {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) y[4 * bt + r] = O[t][bt][r];
-                }
-                // this lane: token 16 t + l16, columns vc0 + vq g4 + (0 .. 4 NCT - 1)
-                const int row = 16 * t + l16, col = vc0 + vq * g4;
-                const unsigned off = (unsigned)(((rev ? nc - 1 - row : row) * ldo + col) * ES);
-                const unsigned at = row < nc && col0 + col < dv ? off : kOut;
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int bt = 0; bt < NCT; ++bt) O[t][bt] = mfma(vf[bt], P[t], O[t][bt]);
+        };
+        auto output = [&]() {
+            const auto os = __builtin_amdgcn_make_buffer_rsrc((void *)(og + (size_t)lo * ldo), 0,
+                                                              __builtin_amdgcn_readfirstlane(nc * ldo * ES), kBuf);
+            const unsigned sb = short_by(nc, ldo);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const unsigned at = ook ? row_off(16 * t + l16, ldo, ocol) - sb : kOut;
                 if constexpr (ES == 4) {
 #pragma unroll
                     for (int i = 0; i < NCT; ++i)
-                        __builtin_amdgcn_raw_buffer_store_b128(
-                            __builtin_bit_cast(u32x4, f32x4{y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]}), os,
-                            at == kOut ? kOut : at + 16 * i, 0, 0);
-                } else if constexpr (NCT == 2) {
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[t][i]), os, at + 16 * i, 0, 0);
+                } else {
+                    const f32x4 a0 = O[t][0], a1 = O[t][NCT - 1];
+                    const float y[8] = {a0[0], a0[1], a0[2], a0[3], a1[0], a1[1], a1[2], a1[3]};
                     bf16x8 o8;
                     pack(y, o8);
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o8), os, at, 0, 0);
-                } else {
-                    const float z[8] = {y[0], y[1], y[2], y[3], 0, 0, 0, 0};
-                    bf16x8 o8;
-                    pack(z, o8);
                     const u32x4 u = __builtin_bit_cast(u32x4, o8);
-                    __builtin_amdgcn_raw_buffer_store_b64(u32x2{u[0], u[1]}, os, at, 0, 0);
+                    if constexpr (NCT == 2)
+                        __builtin_amdgcn_raw_buffer_store_b128(u, os, at, 0, 0);
+                    else
+                        __builtin_amdgcn_raw_buffer_store_b64(u32x2{u[0], u[1]}, os, at, 0, 0);
                 }
             }
-        }
-
-        // state update: X is held divided by sigma = e^{g held}, so that a chunk's
-        // decay costs nothing and no rounded factor is applied again and again
-        held += nc;
-        sigma = gpow(held);
-        if (!(sigma >= kRenorm && sigma <= 1.0f / kRenorm)) {
+        };
+        // state update
 #pragma unroll
-            for (int at = 0; at < NAT; ++at)
+        for (int kk = 0; kk < NKS; ++kk) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (kk + 1 < NKS) {
 #pragma unroll
-                for (int bt = 0; bt < NCT; ++bt) X[at][bt] *= sigma;
-            held = 0;
-            sigma = 1.0f;
-        }
-        const float inv = gpow(-held);
-        if (nc < L) weights(nc);
-        Frag vw[NCT][PARTS];
-#pragma unroll
-        for (int bt = 0; bt < NCT; ++bt) {
-            float x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = (float)vf[bt][e] * (w[e] * inv);
-            split(x, vw[bt]);
-        }
-#pragma unroll
-        for (int at = 0; at < NAT; at += 2) {
-            Frag kf[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) kf[u] = cols.get(Ks, at >> 1, u);
+                for (int t = 0; t < 2; ++t) kf[(kk + 1) & 1][t] = cols.get(Ks, kk + 1, t);
+            }
 #pragma unroll
             for (int q = 0; q < PARTS; ++q)
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+                for (int t = 0; t < 2; ++t)
 #pragma unroll
-                    for (int bt = 0; bt < NCT; ++bt) X[at + u][bt] = mfma(kf[u], vw[bt][q], X[at + u][bt]);
+                    for (int bt = 0; bt < NCT; ++bt)
+                        X[2 * kk + t][bt] = mfma(kf[kk & 1][t], vw[bt][q], X[2 * kk + t][bt]);
+            if constexpr (!SO) {
+                if (kk == 0) scores();
+                if (kk == 1) values();
+                if (kk == 2) output();
+            }
         }
+        if constexpr (!SO && NKS == 2) output();
     };
     if (NBUF == 2 && nch > 0) load(tile0, 0);
     for (int c = 0; c < nch; c += 2) {
