@@ -111,18 +111,23 @@ __device__ __forceinline__ void pack(const float *x, f32x8 &f) {
 }
 
 // Two floats as a sum of PARTS roundings, elements 2 p and 2 p + 1 of PARTS
-// operands: each part is the rounded rest of the one before
+// operands: each part is the rounded rest of the one before.  `here` keeps the
+// work in place: the compiler would move it behind the next branch.
+template <bool HERE>
 __device__ __forceinline__ void split2(float x0, float x1, bf16x8 *f, int p) {
 #pragma unroll
     for (int q = 0; q < 3; ++q) {
         const bf16x2 h = __builtin_convertvector((f32x2{x0, x1}), bf16x2);
-        f[q][2 * p] = h[0];
-        f[q][2 * p + 1] = h[1];
-        const unsigned b = __builtin_bit_cast(unsigned, h);
+        unsigned b = __builtin_bit_cast(unsigned, h);
+        if constexpr (HERE) asm volatile("" : "+v"(b));
+        u32x4 w = __builtin_bit_cast(u32x4, f[q]);
+        w[p] = b;
+        f[q] = __builtin_bit_cast(bf16x8, w);
         x0 -= __uint_as_float(b << 16);
         x1 -= __uint_as_float(b & 0xffff0000u);
     }
 }
+template <bool HERE>
 __device__ __forceinline__ void split2(float x0, float x1, f32x8 *f, int p) {
     f[0][2 * p] = x0;
     f[0][2 * p + 1] = x1;
@@ -139,8 +144,14 @@ __device__ __forceinline__ int swz(int r) {
     return ((x & 1) << 2) | (x & 2) | ((x >> 2) & 1);
 }
 
+
 __device__ __forceinline__ s16x4 tr_read(const bf16 *p) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
+}
+
+// a value that is the same in all lanes, in a scalar register
+__device__ __forceinline__ float uniform(float x) {
+    return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x)));
 }
 
 // Wait until at most N of this wavefront's memory operations are outstanding
@@ -153,28 +164,32 @@ __device__ __forceinline__ void wait_vm() {
 
 // Whole-granule reads of a row: d_qk index 32 kk + 8 g4 + (0..7) of rows
 // l16 and 16 + l16.  The swizzle touches the low four bits of the granule
-// number at most, so a few addresses and constant offsets serve all kk.
+// number at most, so one address per lane, some constant bits of it flipped, and
+// constant offsets serve all kk.  `fresh` stops the compiler from keeping
+// the flipped addresses in registers over the chunk loop.
+__device__ __forceinline__ int fresh(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
 template <int GPR>
 struct Rows {
     static constexpr int M = GPR >= 16 ? 4 : 2;  // low parts of the granule number, in steps of 4
-    int off[M];
+    int off;
     __device__ __forceinline__ void init(const bf16 *, int l16, int g4) {
-#pragma unroll
-        for (int m = 0; m < M; ++m) off[m] = l16 * GPR * 8 + (((4 * m + g4) ^ swz<GPR>(l16)) << 3);
+        off = l16 * GPR * 8 + ((g4 ^ swz<GPR>(l16)) << 3);
     }
     __device__ __forceinline__ void init(const float *, int l16, int g4) {
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-            off[m] = l16 * GPR * 4 + (((8 * (m >> 1) + 2 * g4 + (m & 1)) ^ swz<GPR>(l16)) << 2);
+        off = l16 * GPR * 4 + (((2 * g4) ^ swz<GPR>(l16)) << 2);
     }
     __device__ __forceinline__ bf16x8 get(const bf16 *t, int half, int kk) const {
-        return *reinterpret_cast<const bf16x8 *>(t + off[kk % M] + half * 16 * GPR * 8 + kk / M * M * 32);
+        return *reinterpret_cast<const bf16x8 *>(t + (off ^ (32 * (kk % M))) + half * 16 * GPR * 8 + kk / M * M * 32);
     }
     __device__ __forceinline__ f32x8 get(const float *t, int half, int kk) const {
         f32x8 f;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const f32x4 x = *reinterpret_cast<const f32x4 *>(t + off[2 * (kk & 1) + h] + half * 16 * GPR * 4 + (kk >> 1) * 64);
+            const f32x4 x = *reinterpret_cast<const f32x4 *>(t + (off ^ (32 * (kk & 1) + 4 * h)) + half * 16 * GPR * 4 +
+                                                             (kk >> 1) * 64);
 #pragma unroll
             for (int e = 0; e < 4; ++e) f[4 * h + e] = x[e];
         }
@@ -183,17 +198,16 @@ struct Rows {
 };
 
 // Transposed reads of all d_qk columns for the state update: columns
-// 32 kk + 4 u + 8 a + (0..3) of quad a, tokens as in col_frag.
+// 32 kk + 4 u + 8 a + (0..3) of quad a, tokens as in v_frag.
 template <int GPR>
 struct Cols {
     static constexpr int M = GPR >= 16 ? 4 : 2;
-    int off[M], l16, g4;
+    int off, l16, g4;
     __device__ __forceinline__ void init(const bf16 *, int l, int g) {
         const int r0 = 4 * g + (l >> 2);
-#pragma unroll
-        for (int m = 0; m < M; ++m) off[m] = r0 * GPR * 8 + (((4 * m + (l & 3)) ^ swz<GPR>(r0)) << 3);
+        off = r0 * GPR * 8 + (((l & 3) ^ swz<GPR>(r0)) << 3);
     }
-    __device__ __forceinline__ void init(const float *, int l, int g) { l16 = l, g4 = g; }
+    __device__ __forceinline__ void init(const float *, int l, int g) { off = 0, l16 = l, g4 = g; }
     __device__ __forceinline__ bf16x8 get(const bf16 *t, int kk, int u) const;
     __device__ __forceinline__ f32x8 get(const float *t, int kk, int u) const;
 };
@@ -201,20 +215,34 @@ struct Cols {
 // Column l16 of 16 columns, tokens 16 (e / 4) + 4 g4 + e % 4 of the chunk.  The
 // columns come in quads of 4 consecutive elements; quad a starts at element
 // c0 + step * a (multiples of 4).
-template <int GPR>
-__device__ __forceinline__ bf16x8 col_frag(const bf16 *t, int c0, int step, int l16, int g4) {
-    const int c = c0 + step * (l16 & 3);
-    const int r0 = 4 * g4 + (l16 >> 2), r1 = r0 + 16;
-    const int gr = c >> 3, h = c & 4;
+__device__ __forceinline__ bf16x8 tr_pair(const bf16 *p, int rows16) {
     typedef short s16x8 __attribute__((ext_vector_type(8)));
-    const s16x4 a = tr_read(t + r0 * GPR * 8 + ((gr ^ swz<GPR>(r0)) << 3) + h);
-    const s16x4 b = tr_read(t + r1 * GPR * 8 + ((gr ^ swz<GPR>(r1)) << 3) + h);
+    const s16x4 a = tr_read(p), b = tr_read(p + rows16);
     const s16x8 r = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
     return __builtin_bit_cast(bf16x8, r);
 }
-template <int GPR>
-__device__ __forceinline__ f32x8 col_frag(const float *t, int c0, int step, int l16, int g4) {
+// ... of a wavefront's V tile (rows of W elements, not swizzled: 16 lanes read
+// 4 whole neighbouring rows)
+template <int W>
+__device__ __forceinline__ bf16x8 v_frag(const bf16 *t, int c0, int step, int l16, int g4) {
+    return tr_pair(t + (4 * g4 + (l16 >> 2)) * W + c0 + step * (l16 & 3), 16 * W);
+}
+template <int W>
+__device__ __forceinline__ f32x8 v_frag(const float *t, int c0, int step, int l16, int g4) {
     const int c = c0 + step * (l16 >> 2) + (l16 & 3);
+    f32x8 f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = t[(16 * (e >> 2) + 4 * g4 + (e & 3)) * W + c];
+    return f;
+}
+// ... of a swizzled K tile
+template <int GPR>
+__device__ __forceinline__ bf16x8 Cols<GPR>::get(const bf16 *t, int kk, int u) const {
+    return tr_pair(t + (off ^ (32 * (kk % M))) + kk / M * M * 32 + 4 * u, 16 * GPR * 8);
+}
+template <int GPR>
+__device__ __forceinline__ f32x8 Cols<GPR>::get(const float *t, int kk, int u) const {
+    const int c = 32 * kk + 4 * u + 8 * (l16 >> 2) + (l16 & 3);
     f32x8 f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -224,47 +252,38 @@ __device__ __forceinline__ f32x8 col_frag(const float *t, int c0, int step, int 
     return f;
 }
 
-template <int GPR>
-__device__ __forceinline__ bf16x8 Cols<GPR>::get(const bf16 *t, int kk, int u) const {
-    typedef short s16x8 __attribute__((ext_vector_type(8)));
-    const bf16 *p = t + off[kk % M] + kk / M * M * 32 + 4 * u;
-    const s16x4 a = tr_read(p), b = tr_read(p + 16 * GPR * 8);
-    const s16x8 r = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-    return __builtin_bit_cast(bf16x8, r);
-}
-template <int GPR>
-__device__ __forceinline__ f32x8 Cols<GPR>::get(const float *t, int kk, int u) const {
-    return col_frag<GPR>(t, 32 * kk + 4 * u, 8, l16, g4);
-}
-
 template <typename IO, int DKP_, int NCT_, int NW_>
 struct Cfg {
     static constexpr int DKP = DKP_, NCT = NCT_, NW = NW_, NTH = 64 * NW_;
     static constexpr int BV = 16 * NCT * NW;               // value columns of a workgroup
     static constexpr int NAT = DKP / 16, NKS = DKP / 32;   // 16-row tiles of X, inner steps over d_qk
     static constexpr int EPG = Types<IO>::EPG;
-    static constexpr int QG = DKP / EPG, VG = BV / EPG;    // granules of a row
-    static constexpr size_t TILE = (size_t)L * (2 * DKP + BV) * sizeof(IO);
-    static constexpr int NBUF = 2 * TILE <= kLds ? 2 : 1;
-    static constexpr int PER_CU = 2 * NBUF * TILE <= kLds ? 2 : 1;  // workgroups of a compute unit
+    static constexpr int QG = DKP / EPG, VG = 16 * NCT / EPG;  // granules of a row: Q and K; a wavefront's V
+    static constexpr size_t TILE = (size_t)L * 2 * DKP * sizeof(IO), VTILE = (size_t)L * BV * sizeof(IO);
+    static constexpr int NBUF = 2 * TILE + VTILE <= kLds ? 2 : 1;
+    static constexpr bool EARLY = NAT * NCT < 32;
+    static constexpr int PER_CU = 2 * (NBUF * TILE + VTILE) <= kLds && NW == 4 ? 2 : 1;  // workgroups of a compute unit
     static constexpr int BLOCK = DKP * BV;                 // floats of a stored state block
-    static_assert(QG >= 8 && VG >= 8, "swizzle");
-    static_assert(TILE <= kLds, "LDS");
+    static_assert(QG >= 8, "swizzle");
+    static_assert(TILE + VTILE <= kLds, "LDS");
 };
 
 // SO (state only): the first pass over segments, each from the zero state.
 template <typename IO, int DKP, int NCT, int NW, bool SO>
-__global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU)) void linattn_kernel(KArgs a) {
+__global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) void linattn_kernel(KArgs a) {
     using C = Cfg<IO, DKP, NCT, NW>;
     using Frag = typename Types<IO>::Frag;
     constexpr int NAT = C::NAT, NKS = C::NKS, QG = C::QG, VG = C::VG, BV = C::BV, NBUF = C::NBUF;
     constexpr int PARTS = Types<IO>::PARTS;
     constexpr int ES = (int)sizeof(IO);
-    // Q, K and V tiles of a chunk, double buffered where two fit.  Two arrays and
+    // Q and K tiles of a chunk, double buffered where two fit.  Two arrays and
     // a loop over pairs of chunks, not one array indexed by parity: the compiler
-    // waits for a copy in flight before any LDS read that may alias it.
-    __shared__ __attribute__((aligned(16))) IO tile0[L * (2 * DKP + BV)];
-    __shared__ __attribute__((aligned(16))) IO tile1[NBUF == 2 ? L * (2 * DKP + BV) : 16];
+    // waits for a copy in flight before any LDS read that may alias it.  A
+    // wavefront's columns of V are its own and go to registers at the start of
+    // the chunk: one buffer each, refilled by the wavefront that has read it.
+    __shared__ __attribute__((aligned(16))) IO tile0[L * 2 * DKP];
+    __shared__ __attribute__((aligned(16))) IO tile1[NBUF == 2 ? L * 2 * DKP : 16];
+    __shared__ __attribute__((aligned(16))) IO vtiles[NW][L * 16 * NCT];
 
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g4 = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -294,20 +313,16 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU)) void lina
     // ---- decays
     const float gl = decay_log2(a.g[h]);
     const auto gpow = [&](int steps) { return __builtin_amdgcn_exp2f(gl * (float)steps); };
-    // P's weights of a score tile on the diagonal, and one tile below it
-    float dg[4], db[4];
+    // Weights are products of a lane's own power and powers common to the
+    // workgroup (scalar registers), all with exponents >= 0.
+    // P of the score tile below the diagonal: e^{g (16 + l16 - 4 g4 - r)}
+    const float below = gpow(13 + l16 - 4 * g4) * job.p_scale;
+    // token 16 (e / 4) + 4 g4 + e % 4 in the state update: a chunk of nc < L tokens
+    // fills its last rows, behind rows of zeros, so the weights are always these
+    const float wlane = gpow(12 - 4 * g4 + job.shift) * job.up_scale;
+    float upow[8];  // e^{g (19 - 16 (e / 4) - e % 4)}: the upper four are e^{g (3 - r)}
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int d = l16 - 4 * g4 - r;
-        dg[r] = gpow(max(d, 0)) * job.p_scale;
-        db[r] = gpow(16 + d) * job.p_scale;
-    }
-    // weights of this lane's tokens in the state update.  A chunk of nc < L
-    // tokens fills its last rows, behind rows of zeros, so they are always these.
-    float w[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        w[e] = gpow(L - 1 + job.shift - (16 * (e >> 2) + 4 * g4 + (e & 3))) * job.up_scale;
+    for (int e = 0; e < 8; ++e) upow[e] = uniform(gpow(19 - 16 * (e >> 2) - (e & 3)));
 
     // ---- state.  Lane (l16, g4) of tile (at, bt) holds rows krow(at) + r
     // of column vcol(bt)
@@ -367,20 +382,16 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU)) void lina
     // Tile copies: 64 granules of LDS per wavefront and instruction, the swizzle
     // is in the source address; columns past the tensor's read as zero.  The
     // swizzle repeats every 16 rows, so a few per-lane offsets serve all instructions.
-    constexpr int QPER = 16 * QG / C::NTH > 1 ? 16 * QG / C::NTH : 1;
-    constexpr int VPER = 16 * VG / C::NTH > 1 ? 16 * VG / C::NTH : 1;
-    auto copy_offsets = [&](unsigned *off, int ld, int ncol, auto gpr_c) {
-        constexpr int GPR = decltype(gpr_c)::value;
-        static_assert(L * GPR % C::NTH == 0, "whole instructions");
+    constexpr int NI = L * QG / C::NTH, RPI = C::NTH / QG, PER = RPI >= 16 ? 1 : 16 / RPI;
+    static_assert(L * QG % C::NTH == 0, "whole instructions");
+    auto copy_offsets = [&](unsigned *off, int ld) {
 #pragma unroll
-        for (int i = 0; i < (16 * GPR / C::NTH > 1 ? 16 * GPR / C::NTH : 1); ++i) {
-            const int gi = i * C::NTH + tid, row = gi / GPR, col = ((gi % GPR) ^ swz<GPR>(row)) * C::EPG;
-            off[i] = col < ncol ? row_off(row & (L - 1), ld, col) : kOut;
+        for (int i = 0; i < PER; ++i) {
+            const int gi = i * C::NTH + tid, row = gi / QG, col = ((gi % QG) ^ swz<QG>(row)) * C::EPG;
+            off[i] = col < dk ? row_off(row, ld, col) : kOut;
         }
     };
-    auto copy = [&](IO *dst, const IO *src, int ld, const unsigned *off, auto gpr_c, int lo, int nc) {
-        constexpr int GPR = decltype(gpr_c)::value, NI = L * GPR / C::NTH, RPI = C::NTH / GPR;
-        constexpr int PER = 16 * GPR / C::NTH > 1 ? 16 * GPR / C::NTH : 1;
+    auto copy = [&](IO *dst, const IO *src, int ld, const unsigned *off, int lo, int nc) {
         const auto rs = __builtin_amdgcn_make_buffer_rsrc((void *)(src + (size_t)lo * ld), 0,
                                                           __builtin_amdgcn_readfirstlane(nc * ld * ES), kBuf);
         const unsigned sb = short_by(nc, ld), step = (unsigned)((rev ? -RPI : RPI) * ld * ES);
@@ -389,24 +400,38 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU)) void lina
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr *)(dst + (i * NW + wave) * 64 * C::EPG), 16,
                                                      off[i % PER] + (i / PER * PER * step - sb), 0, 0, 0);
     };
-    using QGc = std::integral_constant<int, QG>;
-    using VGc = std::integral_constant<int, VG>;
-    unsigned qoff[QPER], koff[QPER], voff[VPER];
-    if constexpr (!SO) copy_offsets(qoff, ldq, dk, QGc{});
-    copy_offsets(koff, ldk, dk, QGc{});
-    copy_offsets(voff, ldv, dv - col0, VGc{});
+    unsigned qoff[PER], koff[PER], voff;
+    if constexpr (!SO) copy_offsets(qoff, ldq);
+    copy_offsets(koff, ldk);
+    // this wavefront's columns of V: 64 / VG rows an instruction
+    constexpr int VI = L * VG / 64;
+    {
+        const int col = vc0 + lane % VG * C::EPG;
+        voff = col0 + col < dv ? row_off(lane / VG, ldv, col) : kOut;
+    }
     auto load = [&](IO *t, int c) {
         int nc, lo;
         chunk(c, nc, lo);
-        if constexpr (!SO) copy(t, qg, ldq, qoff, QGc{}, lo, nc);
-        copy(t + L * DKP, kg, ldk, koff, QGc{}, lo, nc);
-        copy(t + 2 * L * DKP, vg, ldv, voff, VGc{}, lo, nc);
+        if constexpr (!SO) copy(t, qg, ldq, qoff, lo, nc);
+        copy(t + L * DKP, kg, ldk, koff, lo, nc);
+    };
+    IO *Vs = vtiles[wave];
+    auto load_v = [&](int c) {
+        int nc, lo;
+        chunk(c, nc, lo);
+        const auto rs = __builtin_amdgcn_make_buffer_rsrc((void *)(vg + (size_t)lo * ldv), 0,
+                                                          __builtin_amdgcn_readfirstlane(nc * ldv * ES), kBuf);
+        const unsigned sb = short_by(nc, ldv), step = (unsigned)((rev ? -64 / VG : 64 / VG) * ldv * ES);
+#pragma unroll
+        for (int i = 0; i < VI; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr *)(Vs + i * 64 * C::EPG), 16, voff + (i * step - sb),
+                                                     0, 0, 0);
     };
 
-    Rows<QG> rows;
-    Cols<QG> cols;
-    rows.init((const IO *)nullptr, l16, g4);
-    cols.init((const IO *)nullptr, l16, g4);
+    Rows<QG> rows0;
+    Cols<QG> cols0;
+    rows0.init((const IO *)nullptr, l16, g4);
+    cols0.init((const IO *)nullptr, l16, g4);
     // this lane's outputs: tokens l16 and 16 + l16, columns vc0 + vq g4 + (0 .. 4 NCT - 1)
     const int ocol = vc0 + vq * g4;
     const bool ook = col0 + ocol < dv;
@@ -414,6 +439,8 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU)) void lina
     float sigma = 1.0f;
     // memory operations of a chunk issued after its copies of the next one: the stores of o
     constexpr int NST = SO ? 0 : 2 * (ES == 4 ? NCT : 1);
+    // w v among the read-out's products, where the registers allow it
+    constexpr bool EARLY = !SO && C::EARLY;
     // Order of a chunk's work: each step's LDS reads are issued a step ahead of
     // the products that use them, and the elementwise work (w v, P, the
     // output) sits between products that do not depend on it.  sched_barrier
@@ -429,11 +456,30 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU)) void lina
             wait_vm<NST>();  // this wavefront's copies have landed
         }
         __syncthreads();
-        if (NBUF == 2 && c + 1 < nch) load(next, c + 1);
-        __builtin_amdgcn_sched_barrier(0);
         int nc, lo;
         chunk(c, nc, lo);
-        const IO *Qs = cur, *Ks = Qs + L * DKP, *Vs = Ks + L * DKP;
+        const IO *Qs = cur, *Ks = Qs + L * DKP;
+        Rows<QG> rows = rows0;
+        Cols<QG> cols = cols0;
+        if constexpr (!C::EARLY) {
+            rows.off = fresh(rows.off);
+            cols.off = fresh(cols.off);
+        }
+        Frag vf[NCT], vw[NCT][PARTS], kf[2][2], q[2][2], k[2][2];
+#pragma unroll
+        for (int bt = 0; bt < NCT; ++bt) vf[bt] = v_frag<16 * NCT>(Vs, 4 * bt, vq, l16, g4);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            if constexpr (SO) {
+                kf[0][t] = cols.get(Ks, 0, t);
+            } else {
+                q[0][t] = rows.get(Qs, t, 0);
+                k[0][t] = rows.get(Ks, t, 0);
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (NBUF == 2 && c + 1 < nch) load(next, c + 1);
+        __builtin_amdgcn_sched_barrier(0);
         // The decay of X costs nothing while sigma carries it, and no rounded
         // factor is applied again and again; below kRenorm it is folded in.
         const float fade = sigma * job.in_scale;
@@ -447,26 +493,19 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU)) void lina
         }
         const float inv = gpow(-held);
 
-        Frag vf[NCT], vw[NCT][PARTS];
-#pragma unroll
-        for (int bt = 0; bt < NCT; ++bt) vf[bt] = col_frag<VG>(Vs, vc0 + 4 * bt, vq, l16, g4);
         // parts of w v: elements 2 p and 2 p + 1 of tile bt
+        const float winv = wlane * inv;
         auto weigh = [&](int bt, int p) {
-            float x0 = (float)vf[bt][2 * p] * (w[2 * p] * inv), x1 = (float)vf[bt][2 * p + 1] * (w[2 * p + 1] * inv);
-            split2(x0, x1, vw[bt], p);
+            split2<EARLY>((float)vf[bt][2 * p] * (upow[2 * p] * winv), (float)vf[bt][2 * p + 1] * (upow[2 * p + 1] * winv),
+                   vw[bt], p);
         };
-        Frag kf[2][2];
         f32x4 O[2][NCT], S00 = {0, 0, 0, 0}, S10 = S00, S11 = S00;
         if constexpr (!SO) {
             // read-out of the carried state and scores, one pass over d_qk
-            Frag q[2][2], k[2][2];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                q[0][t] = rows.get(Qs, t, 0);
-                k[0][t] = rows.get(Ks, t, 0);
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int bt = 0; bt < NCT; ++bt) O[t][bt] = f32x4{0, 0, 0, 0};
-            }
 #pragma unroll
             for (int kk = 0; kk < NKS; ++kk) {
                 __builtin_amdgcn_sched_barrier(0);
@@ -497,14 +536,18 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU)) void lina
                     for (int t = 0; t < 2; ++t) O[t][bt] = mfma(xf[bt], q[u][t], O[t][bt]);
 #pragma unroll
                 for (int i = 0; i < 4 * NCT; ++i)
-                    if (i * NKS / (4 * NCT) == kk) weigh(i >> 2, i & 3);
+                    if (EARLY && i * NKS / (4 * NCT) == kk) weigh(i >> 2, i & 3);
             }
-        } else {
-#pragma unroll
-            for (int t = 0; t < 2; ++t) kf[0][t] = cols.get(Ks, 0, t);
+        }
+        if constexpr (!EARLY) {
 #pragma unroll
             for (int i = 0; i < 4 * NCT; ++i) weigh(i >> 2, i & 3);
         }
+        // V's next rows over this chunk's, whose reads have returned
+#pragma unroll
+        for (int bt = 0; bt < NCT; ++bt) asm volatile("" : "+v"(vf[bt]));
+        __builtin_amdgcn_sched_barrier(0);
+        if (c + 1 < nch) load_v(c + 1);
         if (renorm) {
 #pragma unroll
             for (int at = 0; at < NAT; ++at)
@@ -518,11 +561,12 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU)) void lina
             float p0[8], p1[8];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const bool seen = l16 >= 4 * g4 + r;  // token j <= i
-                p0[r] = seen ? S00[r] * dg[r] : 0.0f;
+                const int d = l16 - 4 * g4 - r;  // token j <= i: d >= 0
+                const float diag = gpow(max(d, 0)) * job.p_scale;
+                p0[r] = d >= 0 ? S00[r] * diag : 0.0f;
                 p0[4 + r] = 0.0f;
-                p1[r] = S10[r] * db[r];
-                p1[4 + r] = seen ? S11[r] * dg[r] : 0.0f;
+                p1[r] = S10[r] * (upow[4 + r] * below);
+                p1[4 + r] = d >= 0 ? S11[r] * diag : 0.0f;
             }
             pack(p0, P[0]);
             pack(p1, P[1]);
@@ -587,7 +631,10 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU)) void lina
         }
         if constexpr (!SO && NKS == 2) output();
     };
-    if (NBUF == 2 && nch > 0) load(tile0, 0);
+    if (nch > 0) {
+        if (NBUF == 2) load(tile0, 0);
+        load_v(0);
+    }
     for (int c = 0; c < nch; c += 2) {
         body(tile0, tile1, c);
         if (c + 1 < nch) body(NBUF == 2 ? tile1 : tile0, tile0, c + 1);
@@ -672,18 +719,16 @@ __global__ __launch_bounds__(256) void linattn_scan_kernel(KArgs a) {
 // ---- plans
 
 // Kernel shape of a job: rows padded to 64, 128, 256 or 512; 64 columns a
-// workgroup (16 a wavefront) for up to 64 columns and where 512 rows leave no
-// registers for more, else 128 (32 a wavefront).
+// workgroup for up to 64 columns (and for 512 float32 rows, whose tiles fill
+// LDS), else 128.
 int dkp_of(int dk) { return dk <= 64 ? 64 : dk <= 128 ? 128 : dk <= 256 ? 256 : 512; }
-int bv_of(int dkp, int dv) { return dv <= 64 || dkp == 512 ? 64 : 128; }
-
 struct Shape {
     int dkp, bv, tiles;
 };
-Shape shape_of(int dk, int dv) {
+Shape shape_of(int dk, int dv, int io_bf16) {
     Shape s;
     s.dkp = dkp_of(dk);
-    s.bv = bv_of(s.dkp, dv);
+    s.bv = dv <= 64 || (s.dkp == 512 && !io_bf16) ? 64 : 128;
     s.tiles = (dv + s.bv - 1) / s.bv;
     return s;
 }
@@ -711,11 +756,11 @@ int job_dims(int dk, int dv, int backward, int (*d)[2]) {
     return backward ? 3 : 1;
 }
 
-SegPlan call_plan(int B, int H, int T, int dk, int dv, int backward) {
+SegPlan call_plan(int B, int H, int T, int dk, int dv, int io_bf16, int backward) {
     int d[3][2];
     const int n = job_dims(dk, dv, backward, d);
     long long wgs = 0;
-    for (int i = 0; i < n; ++i) wgs += shape_of(d[i][0], d[i][1]).tiles;
+    for (int i = 0; i < n; ++i) wgs += shape_of(d[i][0], d[i][1], io_bf16).tiles;
     return seg_plan(wgs * B * H, T);
 }
 
@@ -735,16 +780,17 @@ hipError_t launch_shape(const KArgs &a, hipStream_t s) {
 
 template <typename IO>
 hipError_t launch_io(const LinArgs &in, hipStream_t s) {
+    constexpr bool BF = sizeof(IO) == 2;
     KArgs a{};
     a.g = in.g;
     a.lengths = in.lengths;
     a.B = in.B, a.H = in.H, a.T = in.T;
     const SegPlan p = call_plan(in.B, in.H, in.T, in.njob > 1 ? in.job[1].dk : in.job[0].dk,
-                                in.njob > 1 ? in.job[1].dv : in.job[0].dv, in.njob > 1);
+                                in.njob > 1 ? in.job[1].dv : in.job[0].dv, BF, in.njob > 1);
     a.nseg = p.nseg, a.seg_len = p.seg_len;
     size_t ws = 0, at[3];
     for (int i = 0; i < in.njob; ++i) {
-        const Shape f = shape_of(in.job[i].dk, in.job[i].dv);
+        const Shape f = shape_of(in.job[i].dk, in.job[i].dv, BF);
         at[i] = ws;
         ws += (size_t)in.B * in.H * p.nseg * f.tiles * f.dkp * f.bv;
     }
@@ -752,10 +798,10 @@ hipError_t launch_io(const LinArgs &in, hipStream_t s) {
     bool done[3] = {false, false, false};
     for (int i = 0; i < in.njob; ++i) {
         if (done[i]) continue;
-        const Shape f = shape_of(in.job[i].dk, in.job[i].dv);
+        const Shape f = shape_of(in.job[i].dk, in.job[i].dv, BF);
         a.njob = a.tiles_all = 0;
         for (int k = i; k < in.njob; ++k) {
-            const Shape fk = shape_of(in.job[k].dk, in.job[k].dv);
+            const Shape fk = shape_of(in.job[k].dk, in.job[k].dv, BF);
             if (done[k] || fk.dkp != f.dkp || fk.bv != f.bv) continue;
             done[k] = true;
             a.job[a.njob] = in.job[k];
@@ -766,12 +812,16 @@ hipError_t launch_io(const LinArgs &in, hipStream_t s) {
         }
         a.ws = p.nseg > 1 ? in.ws : nullptr;
         hipError_t e;
+        // 32 columns a wavefront where its registers hold the state and two
+        // wavefronts a SIMD, else 16
         if (f.dkp == 64)
             e = f.bv == 64 ? launch_shape<IO, 64, 1, 4>(a, s) : launch_shape<IO, 64, 2, 4>(a, s);
         else if (f.dkp == 128)
             e = f.bv == 64 ? launch_shape<IO, 128, 1, 4>(a, s) : launch_shape<IO, 128, 2, 4>(a, s);
         else if (f.dkp == 256)
-            e = f.bv == 64 ? launch_shape<IO, 256, 1, 4>(a, s) : launch_shape<IO, 256, 2, 4>(a, s);
+            e = f.bv == 64 ? launch_shape<IO, 256, 1, 4>(a, s) : launch_shape<IO, 256, BF ? 2 : 1, BF ? 4 : 8>(a, s);
+        else if constexpr (BF)
+            e = f.bv == 64 ? launch_shape<IO, 512, 1, 4>(a, s) : launch_shape<IO, 512, 1, 8>(a, s);
         else
             e = launch_shape<IO, 512, 1, 4>(a, s);
         if (e != hipSuccess) return e;
@@ -781,14 +831,14 @@ hipError_t launch_io(const LinArgs &in, hipStream_t s) {
 
 }  // namespace
 
-size_t linattn_workspace_floats(int B, int H, int T, int dk, int dv, int, int backward) {
-    const SegPlan p = call_plan(B, H, T, dk, dv, backward);
+size_t linattn_workspace_floats(int B, int H, int T, int dk, int dv, int io_bf16, int backward) {
+    const SegPlan p = call_plan(B, H, T, dk, dv, io_bf16, backward);
     if (p.nseg == 1) return 0;
     int d[3][2];
     const int n = job_dims(dk, dv, backward, d);
     size_t f = 0;
     for (int i = 0; i < n; ++i) {
-        const Shape s = shape_of(d[i][0], d[i][1]);
+        const Shape s = shape_of(d[i][0], d[i][1], io_bf16);
         f += (size_t)B * H * p.nseg * s.tiles * s.dkp * s.bv;
     }
     return f;
