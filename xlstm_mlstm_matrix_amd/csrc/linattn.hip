@@ -52,12 +52,7 @@ constexpr int L = 32;           // tokens of a chunk
 constexpr int kBuf = 0x00020000; // word 3 of a raw, range-checked buffer descriptor
 constexpr unsigned kOut = 0xf0000000u;  // an offset past any range: reads zero, writes nothing
 constexpr size_t kLds = 160 * 1024;
-constexpr float kRenorm = 1.0f / 65536.0f;  // sigma's least value
-
-// How the states of a pass are cut into segments.
-struct SegPlan {
-    int nseg, seg_len;
-};
+constexpr float kRenorm = 9.094947e-13f;  // sigma's least value, 2^-40
 
 struct KArgs {
     LinJob job[3];
@@ -221,12 +216,13 @@ __device__ __forceinline__ bf16x8 tr_pair(const bf16 *p, int rows16) {
     const s16x8 r = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
     return __builtin_bit_cast(bf16x8, r);
 }
-// ... of a wavefront's V tile (rows of W elements, not swizzled: 16 lanes read
-// 4 whole neighbouring rows)
+// ... of a shared, swizzled V tile (rows of W elements)
 template <int W>
 __device__ __forceinline__ bf16x8 v_frag(const bf16 *t, int c0, int step, int l16, int g4) {
-    return tr_pair(t + (4 * g4 + (l16 >> 2)) * W + c0 + step * (l16 & 3), 16 * W);
+    const int r0 = 4 * g4 + (l16 >> 2), c = c0 + step * (l16 & 3);
+    return tr_pair(t + r0 * W + (((c >> 3) ^ swz<W / 8>(r0)) << 3) + (c & 4), 16 * W);
 }
+// ... of a wavefront's own V tile (not swizzled)
 template <int W>
 __device__ __forceinline__ f32x8 v_frag(const float *t, int c0, int step, int l16, int g4) {
     const int c = c0 + step * (l16 >> 2) + (l16 & 3);
@@ -258,10 +254,16 @@ struct Cfg {
     static constexpr int BV = 16 * NCT * NW;               // value columns of a workgroup
     static constexpr int NAT = DKP / 16, NKS = DKP / 32;   // 16-row tiles of X, inner steps over d_qk
     static constexpr int EPG = Types<IO>::EPG;
-    static constexpr int QG = DKP / EPG, VG = 16 * NCT / EPG;  // granules of a row: Q and K; a wavefront's V
-    static constexpr size_t TILE = (size_t)L * 2 * DKP * sizeof(IO), VTILE = (size_t)L * BV * sizeof(IO);
+    static constexpr int QG = DKP / EPG, VG = 16 * NCT / EPG, WG = BV / EPG;  // granules of a row: Q and K; a wavefront's V; V
+    // V: with Q and K in the double-buffered tile; for float32, where that leaves no
+    // room for a second workgroup, in one buffer a wavefront (its columns are
+    // its own and go to registers at the start of the chunk).  The shared tile
+    // moves whole rows: 10% faster for 64 bfloat16 columns.
+    static constexpr bool VOWN = sizeof(IO) == 4;
+    static constexpr int TROW = 2 * DKP + (VOWN ? 0 : BV);  // elements of a tile for each token
+    static constexpr size_t TILE = (size_t)L * TROW * sizeof(IO), VTILE = VOWN ? (size_t)L * BV * sizeof(IO) : 0;
     static constexpr int NBUF = 2 * TILE + VTILE <= kLds ? 2 : 1;
-    static constexpr bool EARLY = NAT * NCT < 32;
+    static constexpr bool EARLY = NCT == 1 || DKP < 256;  // else the registers do not suffice
     static constexpr int PER_CU = 2 * (NBUF * TILE + VTILE) <= kLds && NW == 4 ? 2 : 1;  // workgroups of a compute unit
     static constexpr int BLOCK = DKP * BV;                 // floats of a stored state block
     static_assert(QG >= 8, "swizzle");
@@ -278,12 +280,10 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
     constexpr int ES = (int)sizeof(IO);
     // Q and K tiles of a chunk, double buffered where two fit.  Two arrays and
     // a loop over pairs of chunks, not one array indexed by parity: the compiler
-    // waits for a copy in flight before any LDS read that may alias it.  A
-    // wavefront's columns of V are its own and go to registers at the start of
-    // the chunk: one buffer each, refilled by the wavefront that has read it.
-    __shared__ __attribute__((aligned(16))) IO tile0[L * 2 * DKP];
-    __shared__ __attribute__((aligned(16))) IO tile1[NBUF == 2 ? L * 2 * DKP : 16];
-    __shared__ __attribute__((aligned(16))) IO vtiles[NW][L * 16 * NCT];
+    // waits for a copy in flight before any LDS read that may alias it.
+    __shared__ __attribute__((aligned(16))) IO tile0[L * C::TROW];
+    __shared__ __attribute__((aligned(16))) IO tile1[NBUF == 2 ? L * C::TROW : 16];
+    __shared__ __attribute__((aligned(16))) IO vtiles[NW][C::VOWN ? L * 16 * NCT : 8];
 
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g4 = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -370,7 +370,7 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
     const int nch = tau1 > tau0 ? (tau1 - tau0 + L - 1) / L : 0;
     auto chunk = [&](int c, int &nc, int &lo) {
         const int s = tau0 + c * L;
-        nc = min(L, tau1 - s);
+        nc = max(0, min(L, tau1 - s));  // 0 past the last chunk: its copies read nothing
         lo = rev ? n - s - nc : s;
     };
     // Byte offset of (row, element col) from token lo: rows run up or down in
@@ -382,40 +382,50 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
     // Tile copies: 64 granules of LDS per wavefront and instruction, the swizzle
     // is in the source address; columns past the tensor's read as zero.  The
     // swizzle repeats every 16 rows, so a few per-lane offsets serve all instructions.
-    constexpr int NI = L * QG / C::NTH, RPI = C::NTH / QG, PER = RPI >= 16 ? 1 : 16 / RPI;
-    static_assert(L * QG % C::NTH == 0, "whole instructions");
-    auto copy_offsets = [&](unsigned *off, int ld) {
+    auto copy_offsets = [&](unsigned *off, int ld, int ncol, auto gpr_c) {
+        constexpr int GPR = decltype(gpr_c)::value, RPI = C::NTH / GPR;
+        static_assert(L * GPR % C::NTH == 0, "whole instructions");
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int gi = i * C::NTH + tid, row = gi / QG, col = ((gi % QG) ^ swz<QG>(row)) * C::EPG;
-            off[i] = col < dk ? row_off(row, ld, col) : kOut;
+        for (int i = 0; i < (RPI >= 16 ? 1 : 16 / RPI); ++i) {
+            const int gi = i * C::NTH + tid, row = gi / GPR, col = ((gi % GPR) ^ swz<GPR>(row)) * C::EPG;
+            off[i] = col < ncol ? row_off(row, ld, col) : kOut;
         }
     };
-    auto copy = [&](IO *dst, const IO *src, int ld, const unsigned *off, int lo, int nc) {
+    // instructions [i0, i1) of a tile's copy
+    auto copy = [&](IO *dst, const IO *src, int ld, const unsigned *off, auto gpr_c, int lo, int nc, int i0, int i1) {
+        constexpr int GPR = decltype(gpr_c)::value, RPI = C::NTH / GPR, PER = RPI >= 16 ? 1 : 16 / RPI;
         const auto rs = __builtin_amdgcn_make_buffer_rsrc((void *)(src + (size_t)lo * ld), 0,
                                                           __builtin_amdgcn_readfirstlane(nc * ld * ES), kBuf);
         const unsigned sb = short_by(nc, ld), step = (unsigned)((rev ? -RPI : RPI) * ld * ES);
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
+        for (int i = i0; i < i1; ++i)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr *)(dst + (i * NW + wave) * 64 * C::EPG), 16,
                                                      off[i % PER] + (i / PER * PER * step - sb), 0, 0, 0);
     };
-    unsigned qoff[PER], koff[PER], voff;
-    if constexpr (!SO) copy_offsets(qoff, ldq);
-    copy_offsets(koff, ldk);
-    // this wavefront's columns of V: 64 / VG rows an instruction
-    constexpr int VI = L * VG / 64;
-    {
+    using QGc = std::integral_constant<int, QG>;
+    using WGc = std::integral_constant<int, C::WG>;
+    constexpr int NI = L * QG / C::NTH, NIV = L * C::WG / C::NTH;
+    constexpr int QPER = 16 * QG > C::NTH ? 16 * QG / C::NTH : 1, WPER = 16 * C::WG > C::NTH ? 16 * C::WG / C::NTH : 1;
+    unsigned qoff[QPER], koff[QPER], voff[WPER], ownoff = kOut;
+    if constexpr (!SO) copy_offsets(qoff, ldq, dk, QGc{});
+    copy_offsets(koff, ldk, dk, QGc{});
+    constexpr int VI = L * VG / 64;  // own tile: 64 / VG rows an instruction
+    if constexpr (C::VOWN) {
         const int col = vc0 + lane % VG * C::EPG;
-        voff = col0 + col < dv ? row_off(lane / VG, ldv, col) : kOut;
+        ownoff = col0 + col < dv ? row_off(lane / VG, ldv, col) : kOut;
+    } else {
+        copy_offsets(voff, ldv, dv - col0, WGc{});
     }
-    auto load = [&](IO *t, int c) {
+    // part p of np of the copies of chunk c's shared tile
+    auto load = [&](IO *t, int c, int p, int np) {
         int nc, lo;
         chunk(c, nc, lo);
-        if constexpr (!SO) copy(t, qg, ldq, qoff, lo, nc);
-        copy(t + L * DKP, kg, ldk, koff, lo, nc);
+        if constexpr (!SO) copy(t, qg, ldq, qoff, QGc{}, lo, nc, p * NI / np, (p + 1) * NI / np);
+        copy(t + L * DKP, kg, ldk, koff, QGc{}, lo, nc, p * NI / np, (p + 1) * NI / np);
+        if constexpr (!C::VOWN) copy(t + 2 * L * DKP, vg, ldv, voff, WGc{}, lo, nc, p * NIV / np, (p + 1) * NIV / np);
     };
-    IO *Vs = vtiles[wave];
+    // this wavefront's own V tile
+    IO *own = vtiles[wave];
     auto load_v = [&](int c) {
         int nc, lo;
         chunk(c, nc, lo);
@@ -424,8 +434,8 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
         const unsigned sb = short_by(nc, ldv), step = (unsigned)((rev ? -64 / VG : 64 / VG) * ldv * ES);
 #pragma unroll
         for (int i = 0; i < VI; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr *)(Vs + i * 64 * C::EPG), 16, voff + (i * step - sb),
-                                                     0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr *)(own + i * 64 * C::EPG), 16,
+                                                     ownoff + (i * step - sb), 0, 0, 0);
     };
 
     Rows<QG> rows0;
@@ -448,7 +458,7 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
     auto body = [&](IO *cur, IO *next, int c) {
         if (NBUF == 1) {
             __syncthreads();
-            load(cur, c);
+            load(cur, c, 0, 1);
             wait_vm<0>();
         } else if (c == 0) {
             wait_vm<0>();
@@ -467,7 +477,8 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
         }
         Frag vf[NCT], vw[NCT][PARTS], kf[2][2], q[2][2], k[2][2];
 #pragma unroll
-        for (int bt = 0; bt < NCT; ++bt) vf[bt] = v_frag<16 * NCT>(Vs, 4 * bt, vq, l16, g4);
+        for (int bt = 0; bt < NCT; ++bt) vf[bt] = C::VOWN ? v_frag<16 * NCT>((const IO *)own, 4 * bt, vq, l16, g4)
+                             : v_frag<BV>(cur + 2 * L * DKP, vc0 + 4 * bt, vq, l16, g4);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             if constexpr (SO) {
@@ -478,7 +489,7 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
             }
         }
         __builtin_amdgcn_sched_barrier(0);
-        if (NBUF == 2 && c + 1 < nch) load(next, c + 1);
+        if constexpr (NBUF == 2 && SO) load(next, c + 1, 0, 1);
         __builtin_amdgcn_sched_barrier(0);
         // The decay of X costs nothing while sigma carries it, and no rounded
         // factor is applied again and again; below kRenorm it is folded in.
@@ -508,6 +519,7 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
                 for (int bt = 0; bt < NCT; ++bt) O[t][bt] = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int kk = 0; kk < NKS; ++kk) {
+                if constexpr (NBUF == 2) load(next, c + 1, kk, NKS);
                 __builtin_amdgcn_sched_barrier(0);
                 const int u = kk & 1;
 #pragma unroll
@@ -543,11 +555,13 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
 #pragma unroll
             for (int i = 0; i < 4 * NCT; ++i) weigh(i >> 2, i & 3);
         }
-        // V's next rows over this chunk's, whose reads have returned
+        if constexpr (C::VOWN) {
+            // V's next rows over this chunk's, whose reads have returned
 #pragma unroll
-        for (int bt = 0; bt < NCT; ++bt) asm volatile("" : "+v"(vf[bt]));
-        __builtin_amdgcn_sched_barrier(0);
-        if (c + 1 < nch) load_v(c + 1);
+            for (int bt = 0; bt < NCT; ++bt) asm volatile("" : "+v"(vf[bt]));
+            __builtin_amdgcn_sched_barrier(0);
+            load_v(c + 1);
+        }
         if (renorm) {
 #pragma unroll
             for (int at = 0; at < NAT; ++at)
@@ -632,13 +646,14 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
         if constexpr (!SO && NKS == 2) output();
     };
     if (nch > 0) {
-        if (NBUF == 2) load(tile0, 0);
-        load_v(0);
+        if (NBUF == 2) load(tile0, 0, 0, 1);
+        if constexpr (C::VOWN) load_v(0);
     }
     for (int c = 0; c < nch; c += 2) {
         body(tile0, tile1, c);
         if (c + 1 < nch) body(NBUF == 2 ? tile1 : tile0, tile0, c + 1);
     }
+    wait_vm<0>();  // no copy may still be on its way into LDS when the workgroup ends
 
     // ---- state out
 #pragma unroll
@@ -718,50 +733,69 @@ __global__ __launch_bounds__(256) void linattn_scan_kernel(KArgs a) {
 
 // ---- plans
 
-// Kernel shape of a job: rows padded to 64, 128, 256 or 512; 64 columns a
-// workgroup for up to 64 columns (and for 512 float32 rows, whose tiles fill
-// LDS), else 128.
-int dkp_of(int dk) { return dk <= 64 ? 64 : dk <= 128 ? 128 : dk <= 256 ? 256 : 512; }
-struct Shape {
-    int dkp, bv, tiles;
+// One launch: the jobs of a call whose rows are padded to the same width.
+struct Group {
+    int dkp, bv;              // rows padded to 64, 128, 256 or 512; columns of a workgroup
+    int njob, job[3], tiles[3], tiles_all;
+    int nseg, seg_len;
+    size_t ws_job[3];         // floats from the workspace's start
 };
-Shape shape_of(int dk, int dv, int io_bf16) {
-    Shape s;
-    s.dkp = dkp_of(dk);
-    s.bv = dv <= 64 || (s.dkp == 512 && !io_bf16) ? 64 : 128;
-    s.tiles = (dv + s.bv - 1) / s.bv;
-    return s;
-}
+struct Plan {
+    int ngroup;
+    Group group[3];
+    size_t floats;            // of workspace
+};
 
-// Enough segments for two workgroups on every compute unit, each at least four
-// chunks long; one where the column blocks alone give them.
-SegPlan seg_plan(long long wgs, int T) {
-    const int nch = (T + L - 1) / L;
-    long long want = wgs >= 256 ? 1 : (512 + wgs - 1) / wgs;
-    if (want > nch / 4) want = nch / 4;
-    if (want < 1) want = 1;
-    SegPlan p;
-    const int cps = (int)((nch + want - 1) / want);
-    p.seg_len = cps * L;
-    p.nseg = (T + p.seg_len - 1) / p.seg_len;
+#ifndef WGA
+#define WGA 256
+#define WGB 256
+#define WGN 512
+#endif
+// Columns of a workgroup and segments of a sequence, for enough workgroups to
+// fill the 256 compute units.  128 columns move Q and K through LDS half as
+// often as 64 do; segments cost a second reading of K and V and the states'
+// way through memory; so: 128 if that gives a workgroup each, else 64 if that
+// does, else 128 and segments (each at least four chunks long).
+Plan make_plan(int B, int H, int T, int dk, int dv, int io_bf16, int backward) {
+    Plan p{};
+    const int dims[3][2] = {{backward ? dv : dk, backward ? dk : dv}, {dk, dv}, {dv, dk}};
+    const long long cells = (long long)B * H;
+    for (int j = 0; j < (backward ? 3 : 1); ++j) {
+        const int r = dims[j][0], dkp = r <= 64 ? 64 : r <= 128 ? 128 : r <= 256 ? 256 : 512;
+        int i = 0;
+        while (i < p.ngroup && p.group[i].dkp != dkp) ++i;
+        if (i == p.ngroup) p.group[p.ngroup++].dkp = dkp;
+        Group &g = p.group[i];
+        g.job[g.njob++] = j;
+    }
+    for (int i = 0; i < p.ngroup; ++i) {
+        Group &g = p.group[i];
+        long long n64 = 0, n128 = 0;
+        bool wide = false;
+        for (int k = 0; k < g.njob; ++k) {
+            const int c = dims[g.job[k]][1];
+            n64 += cells * ((c + 63) / 64);
+            n128 += cells * ((c + 127) / 128);
+            wide |= c > 64;
+        }
+        // 512 float32 rows: the tiles fill LDS
+        if (g.dkp == 512 && !io_bf16) wide = false;
+        g.bv = wide && (n128 >= WGA || n64 < WGB) ? 128 : 64;
+        const long long wgs = g.bv == 128 ? n128 : n64;
+        const int nch = (T + L - 1) / L;
+        long long want = wgs >= 256 ? 1 : (WGN + wgs - 1) / wgs;
+        if (want > nch / 4) want = nch / 4;
+        if (want < 1) want = 1;
+        g.seg_len = (int)((nch + want - 1) / want) * L;
+        g.nseg = (T + g.seg_len - 1) / g.seg_len;
+        for (int k = 0; k < g.njob; ++k) {
+            g.tiles[k] = (dims[g.job[k]][1] + g.bv - 1) / g.bv;
+            g.tiles_all += g.tiles[k];
+            g.ws_job[k] = p.floats;
+            if (g.nseg > 1) p.floats += (size_t)cells * g.nseg * g.tiles[k] * g.dkp * g.bv;
+        }
+    }
     return p;
-}
-
-// jobs' rows and columns of a call
-int job_dims(int dk, int dv, int backward, int (*d)[2]) {
-    d[0][0] = backward ? dv : dk;
-    d[0][1] = backward ? dk : dv;
-    d[1][0] = dk, d[1][1] = dv;
-    d[2][0] = dv, d[2][1] = dk;
-    return backward ? 3 : 1;
-}
-
-SegPlan call_plan(int B, int H, int T, int dk, int dv, int io_bf16, int backward) {
-    int d[3][2];
-    const int n = job_dims(dk, dv, backward, d);
-    long long wgs = 0;
-    for (int i = 0; i < n; ++i) wgs += shape_of(d[i][0], d[i][1], io_bf16).tiles;
-    return seg_plan(wgs * B * H, T);
 }
 
 template <typename IO, int DKP, int NCT, int NW>
@@ -781,47 +815,33 @@ hipError_t launch_shape(const KArgs &a, hipStream_t s) {
 template <typename IO>
 hipError_t launch_io(const LinArgs &in, hipStream_t s) {
     constexpr bool BF = sizeof(IO) == 2;
-    KArgs a{};
-    a.g = in.g;
-    a.lengths = in.lengths;
-    a.B = in.B, a.H = in.H, a.T = in.T;
-    const SegPlan p = call_plan(in.B, in.H, in.T, in.njob > 1 ? in.job[1].dk : in.job[0].dk,
-                                in.njob > 1 ? in.job[1].dv : in.job[0].dv, BF, in.njob > 1);
-    a.nseg = p.nseg, a.seg_len = p.seg_len;
-    size_t ws = 0, at[3];
-    for (int i = 0; i < in.njob; ++i) {
-        const Shape f = shape_of(in.job[i].dk, in.job[i].dv, BF);
-        at[i] = ws;
-        ws += (size_t)in.B * in.H * p.nseg * f.tiles * f.dkp * f.bv;
-    }
-    // jobs of one kernel shape go in one launch
-    bool done[3] = {false, false, false};
-    for (int i = 0; i < in.njob; ++i) {
-        if (done[i]) continue;
-        const Shape f = shape_of(in.job[i].dk, in.job[i].dv, BF);
-        a.njob = a.tiles_all = 0;
-        for (int k = i; k < in.njob; ++k) {
-            const Shape fk = shape_of(in.job[k].dk, in.job[k].dv, BF);
-            if (done[k] || fk.dkp != f.dkp || fk.bv != f.bv) continue;
-            done[k] = true;
-            a.job[a.njob] = in.job[k];
-            a.tiles[a.njob] = fk.tiles;
-            a.ws_job[a.njob] = at[k];
-            a.tiles_all += fk.tiles;
-            ++a.njob;
+    const LinJob &whole = in.job[in.njob > 1 ? 1 : 0];  // the job of d_qk rows and d_v columns
+    const Plan p = make_plan(in.B, in.H, in.T, whole.dk, whole.dv, BF, in.njob > 1);
+    for (int i = 0; i < p.ngroup; ++i) {
+        const Group &g = p.group[i];
+        KArgs a{};
+        a.g = in.g;
+        a.lengths = in.lengths;
+        a.B = in.B, a.H = in.H, a.T = in.T;
+        a.nseg = g.nseg, a.seg_len = g.seg_len;
+        a.njob = g.njob, a.tiles_all = g.tiles_all;
+        a.ws = g.nseg > 1 ? in.ws : nullptr;
+        for (int k = 0; k < g.njob; ++k) {
+            a.job[k] = in.job[g.job[k]];
+            a.tiles[k] = g.tiles[k];
+            a.ws_job[k] = g.ws_job[k];
         }
-        a.ws = p.nseg > 1 ? in.ws : nullptr;
         hipError_t e;
         // 32 columns a wavefront where its registers hold the state and two
         // wavefronts a SIMD, else 16
-        if (f.dkp == 64)
-            e = f.bv == 64 ? launch_shape<IO, 64, 1, 4>(a, s) : launch_shape<IO, 64, 2, 4>(a, s);
-        else if (f.dkp == 128)
-            e = f.bv == 64 ? launch_shape<IO, 128, 1, 4>(a, s) : launch_shape<IO, 128, 2, 4>(a, s);
-        else if (f.dkp == 256)
-            e = f.bv == 64 ? launch_shape<IO, 256, 1, 4>(a, s) : launch_shape<IO, 256, BF ? 2 : 1, BF ? 4 : 8>(a, s);
+        if (g.dkp == 64)
+            e = g.bv == 64 ? launch_shape<IO, 64, 1, 4>(a, s) : launch_shape<IO, 64, 2, 4>(a, s);
+        else if (g.dkp == 128)
+            e = g.bv == 64 ? launch_shape<IO, 128, 1, 4>(a, s) : launch_shape<IO, 128, 2, 4>(a, s);
+        else if (g.dkp == 256)
+            e = g.bv == 64 ? launch_shape<IO, 256, 1, 4>(a, s) : launch_shape<IO, 256, BF ? 2 : 1, BF ? 4 : 8>(a, s);
         else if constexpr (BF)
-            e = f.bv == 64 ? launch_shape<IO, 512, 1, 4>(a, s) : launch_shape<IO, 512, 1, 8>(a, s);
+            e = g.bv == 64 ? launch_shape<IO, 512, 1, 4>(a, s) : launch_shape<IO, 512, 1, 8>(a, s);
         else
             e = launch_shape<IO, 512, 1, 4>(a, s);
         if (e != hipSuccess) return e;
@@ -832,16 +852,7 @@ hipError_t launch_io(const LinArgs &in, hipStream_t s) {
 }  // namespace
 
 size_t linattn_workspace_floats(int B, int H, int T, int dk, int dv, int io_bf16, int backward) {
-    const SegPlan p = call_plan(B, H, T, dk, dv, io_bf16, backward);
-    if (p.nseg == 1) return 0;
-    int d[3][2];
-    const int n = job_dims(dk, dv, backward, d);
-    size_t f = 0;
-    for (int i = 0; i < n; ++i) {
-        const Shape s = shape_of(d[i][0], d[i][1], io_bf16);
-        f += (size_t)B * H * p.nseg * s.tiles * s.dkp * s.bv;
-    }
-    return f;
+    return make_plan(B, H, T, dk, dv, io_bf16, backward).floats;
 }
 
 hipError_t launch_linattn(const LinArgs &a, int io_bf16, hipStream_t s) {
