@@ -7,7 +7,9 @@ fails to load, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -402,12 +404,32 @@ def step_noalloc(q, k, v, i_pre, f_pre, o_pre, C=None, n=None, m=None, *, h=None
 
 # ---- operators of include/mlstm_ops.h
 
+_NO_GUARD = contextlib.nullcontext()
+_LONGS = {n: ctypes.c_longlong * n for n in (6, 9, 12, 21)}
+
+
+def _guard(device):
+    """The device as the current one (torch's guard only where it is not: a few
+    microseconds, as much as a small kernel runs)."""
+    import torch
+    if device.index == torch.cuda.current_device():
+        return _NO_GUARD
+    return torch.cuda.device(device)
+
+
+def _raw_stream(device) -> int:
+    """torch's current stream of the device, without building a Stream object."""
+    import torch
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(device.index) if get is not None else _stream(device)
+
+
 def _view(t, name, shape, dtype, device):
     """Check a strided tensor whose last dimension is contiguous."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -422,7 +444,7 @@ def _dense(t, name, shape, dtype, device):
     if t is None:
         return
     _req(t, name, dtype, device)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -430,8 +452,8 @@ def _strides(*ts):
     """mlstm_strides_t array of [., ., ., d] tensors (of [., ., d] ones: s2 = 0)."""
     flat = []
     for t in ts:
-        flat += (list(t.stride()[:-1]) + [0])[:3]
-    return (ctypes.c_longlong * len(flat))(*flat)
+        flat += t.stride()[:-1] if t.dim() == 4 else (*t.stride()[:-1], 0)
+    return _LONGS[len(flat)](*flat)
 
 
 def _hip_device(t, name):
@@ -458,6 +480,7 @@ def _workspace(workspace, nbytes, device):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
+@functools.lru_cache(maxsize=4096)
 def linattn_workspace_size(B, H, T, d_qk, d_v, io: int, backward: bool = False) -> int:
     """Bytes of workspace of linattn_fwd, or of linattn_bwd."""
     n = ctypes.c_size_t(0)
@@ -492,7 +515,7 @@ def linattn_fwd(q, k, v, log_decay, S0=None, *, lengths=None, scale: float = 1.0
     _dense(log_decay, "log_decay", (H,), torch.float32, dev)
     _dense(S0, "S0", (B, H, dk, dv), torch.float32, dev)
     _dense(lengths, "lengths", (B,), torch.int32, dev)
-    with torch.cuda.device(dev):
+    with _guard(dev):
         if o is None:
             o = torch.empty((B, H, T, dv), dtype=q.dtype, device=dev)
         if return_state and S_T is None:
@@ -502,7 +525,7 @@ def linattn_fwd(q, k, v, log_decay, S0=None, *, lengths=None, scale: float = 1.0
         wp, wn, _keep = _workspace(workspace, linattn_workspace_size(B, H, T, dk, dv, io), dev)
         _check(lib().mlstm_linattn_fwd(
             _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(S0), _ptr(lengths), _ptr(o), _ptr(S_T),
-            _strides(q, k, v, o), scale, B, H, T, dk, dv, io, wp, wn, _stream(dev)))
+            _strides(q, k, v, o), scale, B, H, T, dk, dv, io, wp, wn, _raw_stream(dev)))
     return (o, S_T) if return_state else o
 
 
@@ -526,7 +549,7 @@ def linattn_step(q, k, v, log_decay, S=None, *, scale: float = 1.0, o=None, S_ou
     _view(v, "v", (B, H, dv), q.dtype, dev)
     _dense(log_decay, "log_decay", (H,), torch.float32, dev)
     _dense(S, "S", (B, H, dk, dv), torch.float32, dev)
-    with torch.cuda.device(dev):
+    with _guard(dev):
         if o is None:
             o = torch.empty((B, H, dv), dtype=q.dtype, device=dev)
         if S_out is None:
@@ -536,7 +559,7 @@ def linattn_step(q, k, v, log_decay, S=None, *, scale: float = 1.0, o=None, S_ou
         _dense(S_out, "S_out", (B, H, dk, dv), torch.float32, dev)
         _check(lib().mlstm_linattn_step(
             _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(S), _ptr(o), _ptr(S_out),
-            _strides(q, k, v, o), scale, B, H, dk, dv, io, _stream(dev)))
+            _strides(q, k, v, o), scale, B, H, dk, dv, io, _raw_stream(dev)))
     return o, S_out
 
 
@@ -563,7 +586,7 @@ def linattn_bwd(q, k, v, log_decay, do, S0=None, dS_T=None, *, lengths=None, sca
     _dense(S0, "S0", ns, torch.float32, dev)
     _dense(dS_T, "dS_T", ns, torch.float32, dev)
     _dense(lengths, "lengths", (B,), torch.int32, dev)
-    with torch.cuda.device(dev):
+    with _guard(dev):
         new = lambda t, shape: torch.empty(shape, dtype=q.dtype, device=dev) if t is None else t
         dq, dk, dv = new(dq, nk), new(dk, nk), new(dv, nv)
         for name, t, shape in (("dq", dq, nk), ("dk", dk, nk), ("dv", dv, nv)):
@@ -573,7 +596,7 @@ def linattn_bwd(q, k, v, log_decay, do, S0=None, dS_T=None, *, lengths=None, sca
         _check(lib().mlstm_linattn_bwd(
             _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(S0), _ptr(lengths), _ptr(do), _ptr(dS_T),
             _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dS0), _strides(q, k, v, do, dq, dk, dv), scale,
-            B, H, T, d_qk, d_v, io, wp, wn, _stream(dev)))
+            B, H, T, d_qk, d_v, io, wp, wn, _raw_stream(dev)))
     return (dq, dk, dv, dS0) if state_grad else (dq, dk, dv)
 
 
@@ -583,6 +606,7 @@ def _choice(table, key, name):
     return table[key]
 
 
+@functools.lru_cache(maxsize=4096)
 def groupnorm_workspace_size(N, S, G, D, over: str, io: int, backward: bool = False) -> int:
     """Bytes of workspace of groupnorm_fwd, or of groupnorm_bwd."""
     n = ctypes.c_size_t(0)
@@ -613,7 +637,7 @@ def groupnorm_fwd(x, weight=None, bias=None, *, eps: float = 1e-5, act: str = "n
     _dense(weight, "weight", (G, D), torch.float32, dev)
     _dense(bias, "bias", (G, D), torch.float32, dev)
     ov, ac = _choice(NORM_OVER, over, "over"), _choice(ACTIVATIONS, act, "act")
-    with torch.cuda.device(dev):
+    with _guard(dev):
         if y is None:
             y = torch.empty((N, S, G, D), dtype=x.dtype, device=dev)
         _view(y, "y", x.shape, x.dtype, dev)
@@ -625,7 +649,7 @@ def groupnorm_fwd(x, weight=None, bias=None, *, eps: float = 1e-5, act: str = "n
         wp, wn, _keep = _workspace(workspace, groupnorm_workspace_size(N, S, G, D, over, io), dev)
         _check(lib().mlstm_groupnorm_fwd(
             _ptr(x), _ptr(weight), _ptr(bias), _ptr(y), _ptr(mean), _ptr(rstd), _strides(x, y),
-            N, S, G, D, ov, ac, eps, io, wp, wn, _stream(dev)))
+            N, S, G, D, ov, ac, eps, io, wp, wn, _raw_stream(dev)))
     return (y, mean, rstd) if return_stats else y
 
 
@@ -650,7 +674,7 @@ def groupnorm_bwd(x, dy, mean, rstd, weight=None, bias=None, *, act: str = "none
         _dense(t, name, stat, torch.float32, dev)
     _dense(weight, "weight", (G, D), torch.float32, dev)
     _dense(bias, "bias", (G, D), torch.float32, dev)
-    with torch.cuda.device(dev):
+    with _guard(dev):
         if dx is None:
             dx = torch.empty((N, S, G, D), dtype=x.dtype, device=dev)
         _view(dx, "dx", x.shape, x.dtype, dev)
@@ -661,5 +685,5 @@ def groupnorm_bwd(x, dy, mean, rstd, weight=None, bias=None, *, act: str = "none
         wp, wn, _keep = _workspace(workspace, groupnorm_workspace_size(N, S, G, D, over, io, True), dev)
         _check(lib().mlstm_groupnorm_bwd(
             _ptr(x), _ptr(dy), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(bias), _ptr(dx), _ptr(dw), _ptr(db),
-            _strides(x, dy, dx), N, S, G, D, ov, ac, io, wp, wn, _stream(dev)))
+            _strides(x, dy, dx), N, S, G, D, ov, ac, io, wp, wn, _raw_stream(dev)))
     return dx, dw, db

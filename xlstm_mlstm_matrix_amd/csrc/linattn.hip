@@ -52,6 +52,7 @@ constexpr int L = 32;           // tokens of a chunk
 constexpr int kBuf = 0x00020000; // word 3 of a raw, range-checked buffer descriptor
 constexpr unsigned kOut = 0xf0000000u;  // an offset past any range: reads zero, writes nothing
 constexpr size_t kLds = 160 * 1024;
+constexpr long long kCUs = 256;  // compute units of an MI355X
 constexpr float kRenorm = 9.094947e-13f;  // sigma's least value, 2^-40
 
 struct KArgs {
@@ -451,6 +452,9 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
     constexpr int NST = SO ? 0 : 2 * (ES == 4 ? NCT : 1);
     // w v among the read-out's products, where the registers allow it
     constexpr bool EARLY = !SO && C::EARLY;
+    // Copies in front of the read-out; among its steps for 512 rows only (4%
+    // faster there, up to 7% slower for fewer rows).
+    constexpr bool SPREAD = !SO && NKS > 8;
     // Order of a chunk's work: each step's LDS reads are issued a step ahead of
     // the products that use them, and the elementwise work (w v, P, the
     // output) sits between products that do not depend on it.  sched_barrier
@@ -489,7 +493,7 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
             }
         }
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (NBUF == 2 && SO) load(next, c + 1, 0, 1);
+        if constexpr (NBUF == 2 && !SPREAD) load(next, c + 1, 0, 1);
         __builtin_amdgcn_sched_barrier(0);
         // The decay of X costs nothing while sigma carries it, and no rounded
         // factor is applied again and again; below kRenorm it is folded in.
@@ -519,7 +523,7 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
                 for (int bt = 0; bt < NCT; ++bt) O[t][bt] = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int kk = 0; kk < NKS; ++kk) {
-                if constexpr (NBUF == 2) load(next, c + 1, kk, NKS);
+                if constexpr (NBUF == 2 && SPREAD) load(next, c + 1, kk, NKS);
                 __builtin_amdgcn_sched_barrier(0);
                 const int u = kk & 1;
 #pragma unroll
@@ -746,16 +750,14 @@ struct Plan {
     size_t floats;            // of workspace
 };
 
-#ifndef WGA
-#define WGA 256
-#define WGB 256
-#define WGN 512
-#endif
 // Columns of a workgroup and segments of a sequence, for enough workgroups to
 // fill the 256 compute units.  128 columns move Q and K through LDS half as
 // often as 64 do; segments cost a second reading of K and V and the states'
 // way through memory; so: 128 if that gives a workgroup each, else 64 if that
-// does, else 128 and segments (each at least four chunks long).
+// does, else 128 and segments for two each (of at least four chunks).  Measured:
+// backward of 64 heads of 128 x 128, 4096 tokens, 212 us with 64 columns, 237
+// with 128 and 3 segments; 64 heads forward 93 us with 8 segments of 128
+// columns, 127 with 4; 32 heads of 256 x 512 backward 604 us against 762.
 Plan make_plan(int B, int H, int T, int dk, int dv, int io_bf16, int backward) {
     Plan p{};
     const int dims[3][2] = {{backward ? dv : dk, backward ? dk : dv}, {dk, dv}, {dv, dk}};
@@ -780,10 +782,10 @@ Plan make_plan(int B, int H, int T, int dk, int dv, int io_bf16, int backward) {
         }
         // 512 float32 rows: the tiles fill LDS
         if (g.dkp == 512 && !io_bf16) wide = false;
-        g.bv = wide && (n128 >= WGA || n64 < WGB) ? 128 : 64;
+        g.bv = wide && (n128 >= kCUs || n64 < kCUs) ? 128 : 64;
         const long long wgs = g.bv == 128 ? n128 : n64;
         const int nch = (T + L - 1) / L;
-        long long want = wgs >= 256 ? 1 : (WGN + wgs - 1) / wgs;
+        long long want = wgs >= kCUs ? 1 : (2 * kCUs + wgs - 1) / wgs;
         if (want > nch / 4) want = nch / 4;
         if (want < 1) want = 1;
         g.seg_len = (int)((nch + want - 1) / want) * L;
