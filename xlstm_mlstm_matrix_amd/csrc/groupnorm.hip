@@ -20,21 +20,57 @@ namespace mlstm {
 
 namespace {
 
+// Phi(z), the normal distribution function, and e = e^{-z^2/2}.  Abramowitz and
+// Stegun, Handbook of Mathematical Functions, 7.1.26 (erf to 1.5e-7): a
+// polynomial in 1 / (1 + p x) times e^{-x^2}, with x = |z| / sqrt(2), whose
+// exponential the derivative needs too; the backward is bound by this arithmetic.
+__device__ __forceinline__ float phi(float z, float *e) {
+    const float x = fabsf(z) * 0.70710678f;
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.0f));
+    *e = exp_e(-0.5f * z * z);
+    float q = fmaf(1.061405429f, t, -1.453152027f);
+    q = fmaf(q, t, 1.421413741f);
+    q = fmaf(q, t, -0.284496736f);
+    q = fmaf(q, t, 0.254829592f);
+    q *= 0.5f * t * *e;
+    return z < 0.0f ? q : 1.0f - q;
+}
 template <int ACT>
 __device__ __forceinline__ float act_f(float z) {
-    if constexpr (ACT == 1) return z / (1.0f + exp_e(-z));
-    if constexpr (ACT == 2) return 0.5f * z * (1.0f + erff(z * 0.70710678f));
+    if constexpr (ACT == 1) return z * __builtin_amdgcn_rcpf(1.0f + exp_e(-z));
+    if constexpr (ACT == 2) {
+        float e;
+        return z * phi(z, &e);
+    }
     return z;
 }
 template <int ACT>
 __device__ __forceinline__ float act_d(float z) {
     if constexpr (ACT == 1) {
-        const float sg = sigmoid(z);
+        const float sg = __builtin_amdgcn_rcpf(1.0f + exp_e(-z));
         return sg * (1.0f + z * (1.0f - sg));
     }
-    if constexpr (ACT == 2)
-        return 0.5f * (1.0f + erff(z * 0.70710678f)) + z * 0.39894228f * exp_e(-0.5f * z * z);
+    if constexpr (ACT == 2) {
+        float e;
+        const float p = phi(z, &e);
+        return p + z * 0.39894228f * e;
+    }
     return 1.0f;
+}
+
+// Sum over aligned groups of n lanes (n a power of two), in every lane of them.
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+    return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float lane_sum(float v, int n) {
+    if (n >= 2) v = dpp_add<0xb1>(v);    // quad_perm 1,0,3,2
+    if (n >= 4) v = dpp_add<0x4e>(v);    // quad_perm 2,3,0,1
+    if (n >= 8) v = dpp_add<0x141>(v);   // row_half_mirror
+    if (n >= 16) v = dpp_add<0x140>(v);  // row_mirror
+    if (n >= 32) v += __shfl_xor(v, 16, 64);
+    if (n >= 64) v += __shfl_xor(v, 32, 64);
+    return v;
 }
 
 // V consecutive elements, V * sizeof(IO) = 16 bytes or one element.
@@ -62,6 +98,24 @@ __device__ __forceinline__ void store_v(IO *p, const float *x) {
     }
 }
 
+// V weights from p (16-byte aligned where V > 1), or `other` without one
+template <int V>
+__device__ __forceinline__ void load_w(const float *p, size_t at, bool ok, float other, float *w) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) w[i] = other;
+    if (!p || !ok) return;
+    if constexpr (V == 1) {
+        w[0] = p[at];
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            const f32x4 t = *(const f32x4 *)(p + at + i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[i + j] = t[j];
+        }
+    }
+}
+
 // ---- over tokens, D <= 64 V K: lanes of a row
 //
 // A wavefront is cut into subgroups of `lpr` lanes, each holding one group's D
@@ -70,16 +124,18 @@ __device__ __forceinline__ void store_v(IO *p, const float *x) {
 // take further positions.  A workgroup stays with its groups, so weights are
 // loaded once and the weight gradients add up in registers.
 struct RowGeom {
-    int lpr, gp, gblk, rblk;  // lanes per row, groups side by side, blocks of groups, blocks of positions
+    int lpr, gp;              // log2 of the lanes per row, of the groups side by side
+    int gblk, rblk;           // blocks of groups, blocks of positions
+    unsigned long long div;   // ceil(2^64 / S): r / S is the upper half of r * div
 };
 
 template <typename IO, int V, int K, int ACT, bool BWD>
 __global__ __launch_bounds__(256) void gn_row_kernel(GnArgs a, RowGeom q) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int sub = lane / q.lpr, ln = lane % q.lpr;
-    const int rpi = 64 / (q.lpr * q.gp);  // positions of a wavefront at a time
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lpr = 1 << q.lpr, sub = lane >> q.lpr, ln = lane & (lpr - 1);
+    const int rpi = 64 >> (q.lpr + q.gp);  // positions side by side in a wavefront
     const int gb = blockIdx.x % q.gblk, rb = blockIdx.x / q.gblk;
-    const int g = gb * q.gp + sub % q.gp, rsub = sub / q.gp;
+    const int g = (gb << q.gp) + (sub & ((1 << q.gp) - 1)), rsub = sub >> q.gp;
     const int D = a.D, nrow = a.N * a.S;
     const IO *x = (const IO *)a.x + g * a.sx.s2;
     const IO *dy = BWD ? (const IO *)a.dy + g * a.sdy.s2 : nullptr;
@@ -89,24 +145,18 @@ __global__ __launch_bounds__(256) void gn_row_kernel(GnArgs a, RowGeom q) {
     float w[K][V], bb[K][V], aw[K][V], ab[K][V];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        d[k] = (k * q.lpr + ln) * V;
+        d[k] = (k * lpr + ln) * V;
         ok[k] = d[k] < D;
+        load_w<V>(a.w, (size_t)g * D + d[k], ok[k], 1.0f, w[k]);
+        load_w<V>(a.b, (size_t)g * D + d[k], ok[k], 0.0f, bb[k]);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            w[k][i] = ok[k] && a.w ? a.w[(size_t)g * D + d[k] + i] : 1.0f;
-            bb[k][i] = ok[k] && a.b ? a.b[(size_t)g * D + d[k] + i] : 0.0f;
-            aw[k][i] = ab[k][i] = 0.0f;
-        }
+        for (int i = 0; i < V; ++i) aw[k][i] = ab[k][i] = 0.0f;
     }
     const float inv = 1.0f / (float)D;
-    auto sum = [&](float v) {
-        for (int m = q.lpr >> 1; m > 0; m >>= 1) v += __shfl_xor(v, m, 64);
-        return v;
-    };
     for (long long r0 = (long long)(rb * 4 + wave) * rpi; r0 < nrow; r0 += (long long)q.rblk * 4 * rpi) {
-        const int r = (int)r0 + rsub;
         const bool rok = r0 + rsub < nrow;
-        const int n = rok ? r / a.S : 0, s = rok ? r % a.S : 0;
+        const int r = rok ? (int)r0 + rsub : 0;
+        const int n = rok ? (a.S == 1 ? r : (int)__umul64hi((unsigned long long)r, q.div)) : 0, s = rok ? r - n * a.S : 0;
         float v[K][V];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -121,7 +171,7 @@ __global__ __launch_bounds__(256) void gn_row_kernel(GnArgs a, RowGeom q) {
             for (int k = 0; k < K; ++k)
 #pragma unroll
                 for (int i = 0; i < V; ++i) t += v[k][i];
-            const float mu = sum(t) * inv;
+            const float mu = lane_sum(t, lpr) / (float)D;  // divided: exact for a constant row
             t = 0.0f;
 #pragma unroll
             for (int k = 0; k < K; ++k)
@@ -130,7 +180,7 @@ __global__ __launch_bounds__(256) void gn_row_kernel(GnArgs a, RowGeom q) {
                     const float c = v[k][i] - mu;
                     t += ok[k] ? c * c : 0.0f;
                 }
-            const float rs = rsqrtf(sum(t) * inv + a.eps);
+            const float rs = rsqrtf(lane_sum(t, lpr) * inv + a.eps);
             if (a.mean && rok && ln == 0) {
                 a.mean[si] = mu;
                 a.rstd[si] = rs;
@@ -165,8 +215,8 @@ __global__ __launch_bounds__(256) void gn_row_kernel(GnArgs a, RowGeom q) {
                     c1 += u[k][i];
                     c2 += u[k][i] * xh;
                 }
-            c1 = sum(c1) * inv;
-            c2 = sum(c2) * inv;
+            c1 = lane_sum(c1, lpr) * inv;
+            c2 = lane_sum(c2, lpr) * inv;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
 #pragma unroll
@@ -180,14 +230,14 @@ __global__ __launch_bounds__(256) void gn_row_kernel(GnArgs a, RowGeom q) {
         // the positions that the lanes of one channel took: over the
         // wavefront's subgroups, then over the wavefronts
         __shared__ float red[2][4][64];
-        const int step = q.lpr * q.gp;
+        const int span = lpr << q.gp;
         float *ws = a.ws + (size_t)rb * 2 * a.G * D;
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 float pw = aw[k][i], pb = ab[k][i];
-                for (int m = step; m < 64; m <<= 1) {
+                for (int m = span; m < 64; m <<= 1) {
                     pw += __shfl_xor(pw, m, 64);
                     pb += __shfl_xor(pb, m, 64);
                 }
@@ -195,7 +245,7 @@ __global__ __launch_bounds__(256) void gn_row_kernel(GnArgs a, RowGeom q) {
                 red[0][wave][lane] = pw;
                 red[1][wave][lane] = pb;
                 __syncthreads();
-                if (wave < 2 && lane < step && ok[k]) {
+                if (wave < 2 && lane < span && ok[k]) {
                     const float t = (red[wave][0][lane] + red[wave][1][lane]) +
                                     (red[wave][2][lane] + red[wave][3][lane]);
                     ws[(size_t)wave * a.G * D + (size_t)g * D + d[k] + i] = t;
@@ -204,15 +254,15 @@ __global__ __launch_bounds__(256) void gn_row_kernel(GnArgs a, RowGeom q) {
     }
 }
 
+// Sum over a workgroup of up to 1024 threads, in every thread; red [16]
 __device__ __forceinline__ float gn_block_sum(float v, float *red) {
+    v = lane_sum(v, 64);
     __syncthreads();
-    red[threadIdx.x] = v;
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();
-    for (int m = 128; m > 0; m >>= 1) {
-        if ((int)threadIdx.x < m) red[threadIdx.x] += red[threadIdx.x + m];
-        __syncthreads();
-    }
-    return red[0];
+    float t = 0.0f;
+    for (int i = 0; i < (int)blockDim.x >> 6; ++i) t += red[i];
+    return t;
 }
 
 // ---- over tokens, rows too long for the registers: a workgroup for each row,
@@ -220,7 +270,7 @@ __device__ __forceinline__ float gn_block_sum(float v, float *red) {
 // come from gn_channel_kernel.
 template <typename IO, int V, int ACT, bool BWD>
 __global__ __launch_bounds__(256) void gn_long_row_kernel(GnArgs a, long long rows) {
-    __shared__ float red[256];
+    __shared__ float red[16];
     const float inv = 1.0f / (float)a.D;
     for (long long r = blockIdx.x; r < rows; r += gridDim.x) {
         const int g = (int)(r % a.G), ns = (int)(r / a.G);
@@ -237,7 +287,7 @@ __global__ __launch_bounds__(256) void gn_long_row_kernel(GnArgs a, long long ro
 #pragma unroll
                 for (int i = 0; i < V; ++i) s0 += v[i];
             }
-            mu = gn_block_sum(s0, red) * inv;
+            mu = gn_block_sum(s0, red) / (float)a.D;
             for (int d = threadIdx.x * V; d < a.D; d += 256 * V) {
                 load_v<IO, V>(x + d, v);
 #pragma unroll
@@ -282,24 +332,58 @@ __global__ __launch_bounds__(256) void gn_long_row_kernel(GnArgs a, long long ro
     }
 }
 
-// dw, db: sums of the partials [rblk][2][C] in ws over rblk; blockIdx.y is 0 for dw.
-__global__ __launch_bounds__(256) void gn_wsum_kernel(const float *ws, float *dw, float *db, int C, int rblk) {
-    __shared__ float red[16][17];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int c = blockIdx.x * 16 + tx, which = blockIdx.y;
-    float *out = which ? db : dw;
-    if (!out) return;
-    float t = 0.0f;
-    if (c < C)
-#pragma unroll 4
-        for (int r = ty; r < rblk; r += 16) t += ws[((size_t)r * 2 + which) * C + c];
-    red[ty][tx] = t;
-    __syncthreads();
-    for (int m = 8; m > 0; m >>= 1) {
-        if (ty < m) red[ty][tx] += red[ty + m][tx];
-        __syncthreads();
+// ---- over sequences, groups of up to 16384 values: a workgroup holds a
+// group in registers (NE values a thread), one launch instead of three.
+template <typename IO, int V, int NE, int ACT>
+__global__ __launch_bounds__(1024) void gn_group_kernel(GnArgs a) {
+    constexpr int NV = NE / V;
+    __shared__ float red[16];
+    // neighbouring groups, which share cache lines, on one XCD (workgroups go round the 8)
+    const int nwg = gridDim.x, xq = nwg >> 3, xr = nwg & 7, xcd = blockIdx.x & 7;
+    const int id = xcd * xq + min(xcd, xr) + (blockIdx.x >> 3);
+    const int g = id % a.G, n = id / a.G;
+    const int rv = a.D / V, total = a.S * rv;  // vectors of a position, of the group
+    const IO *x = (const IO *)a.x + n * a.sx.s0 + g * a.sx.s2;
+    float v[NV][V], t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int e = threadIdx.x + i * blockDim.x;
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[i][j] = 0.0f;
+        if (e < total) load_v<IO, V>(x + e / rv * a.sx.s1 + e % rv * V, v[i]);
     }
-    if (ty == 0 && c < C) out[c] = red[0][tx];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) t += v[i][j];
+    const float inv = 1.0f / ((float)a.S * (float)a.D);
+    const float mu = gn_block_sum(t, red) / ((float)a.S * (float)a.D);
+    t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float c = v[i][j] - mu;
+            t += (int)(threadIdx.x + i * blockDim.x) < total ? c * c : 0.0f;
+        }
+    const float rs = rsqrtf(gn_block_sum(t, red) * inv + a.eps);
+    if (a.mean && threadIdx.x == 0) {
+        a.mean[id] = mu;
+        a.rstd[id] = rs;
+    }
+    IO *y = (IO *)a.y + n * a.sy.s0 + g * a.sy.s2;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int e = threadIdx.x + i * blockDim.x;
+        if (e >= total) break;
+        const int p = e / rv, d = e % rv * V;
+        float w[V], b[V];
+        load_w<V>(a.w, (size_t)g * a.D + d, true, 1.0f, w);
+        load_w<V>(a.b, (size_t)g * a.D + d, true, 0.0f, b);
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[i][j] = act_f<ACT>((v[i][j] - mu) * rs * w[j] + b[j]);
+        store_v<IO, V>(y + p * a.sy.s1 + d, v[i]);
+    }
 }
 
 // ---- split over positions
@@ -357,6 +441,7 @@ __global__ __launch_bounds__(256) void gn_channel_kernel(GnArgs a, PosGeom q) {
             // sums of x - (the block's first x): its square adds at most what
             // that value itself adds to the centred sum, times the row count
             load_v<IO, V>(x + p0 * a.sx.s1, shift);
+#pragma unroll 4
             for (int p = p0 + ty; p < p1; p += TY) {
                 float v[V];
                 load_v<IO, V>(x + p * a.sx.s1, v);
@@ -377,6 +462,7 @@ __global__ __launch_bounds__(256) void gn_channel_kernel(GnArgs a, PosGeom q) {
                 w[i] = a.w ? a.w[c + i] : 1.0f;
                 bb[i] = a.b ? a.b[c + i] : 0.0f;
             }
+#pragma unroll 2
             for (int p = p0 + ty; p < p1; p += TY) {
                 float v[V], u[V];
                 load_v<IO, V>(x + p * a.sx.s1, v);
@@ -416,14 +502,44 @@ __global__ __launch_bounds__(256) void gn_channel_kernel(GnArgs a, PosGeom q) {
     }
 }
 
+// Sum over r of channel c's two partials: 16 channels x 16 rows of a workgroup.
+__device__ __forceinline__ void gn_wsum(const float *ws, float *dw, float *db, int C, int rblk, int cblk, int which) {
+    __shared__ float red[16][17];
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int c = cblk * 16 + tx;
+    float *out = which ? db : dw;
+    if (!out) return;
+    float t = 0.0f;
+    if (c < C)
+#pragma unroll 4
+        for (int r = ty; r < rblk; r += 16) t += ws[((size_t)r * 2 + which) * C + c];
+    red[ty][tx] = t;
+    __syncthreads();
+    for (int m = 8; m > 0; m >>= 1) {
+        if (ty < m) red[ty][tx] += red[ty + m][tx];
+        __syncthreads();
+    }
+    if (ty == 0 && c < C) out[c] = red[0][tx];
+}
+
+// dw, db: sums of the partials [rblk][2][C] in ws over rblk; blockIdx.y is 0 for dw.
+__global__ __launch_bounds__(256) void gn_wsum_kernel(const float *ws, float *dw, float *db, int C, int rblk) {
+    gn_wsum(ws, dw, db, C, rblk, blockIdx.x, blockIdx.y);
+}
+
 // One workgroup per (sample, group).  Forward: mean and rstd from the channels'
 // means and centred sums.  Backward: mean(u) and mean(u xh).  Written to
-// out0, out1 [N][G].
+// out0, out1 [N][G].  The workgroups past those sum dw and db.
 template <bool BWD>
 __global__ __launch_bounds__(256) void gn_combine_kernel(GnArgs a, PosGeom q, float *out0, float *out1) {
-    __shared__ float red[256];
-    const int g = blockIdx.x % a.G, o = blockIdx.x / a.G;
+    __shared__ float red[16];
     const int C = a.G * a.D, n = q.pblk * a.D;
+    if (BWD && (int)blockIdx.x >= a.N * a.G) {
+        const int i = blockIdx.x - a.N * a.G;
+        gn_wsum(a.ws, a.dw, a.db, C, a.N * q.pblk, i >> 1, i & 1);
+        return;
+    }
+    const int g = blockIdx.x % a.G, o = blockIdx.x / a.G;
     const float *ws = a.ws + (size_t)o * q.pblk * 2 * C + (size_t)g * a.D;
     const float total = (float)a.D * (float)a.S;
     float s0 = 0.0f, s1 = 0.0f;
@@ -488,7 +604,7 @@ __global__ __launch_bounds__(256) void gn_apply_kernel(GnArgs a, PosGeom q, cons
     const IO *x = (const IO *)a.x + gn_at(a.sx, a.D, o, c);
     const IO *dy = BWD ? (const IO *)a.dy + gn_at(a.sdy, a.D, o, c) : nullptr;
     IO *y = (IO *)a.y + gn_at(a.sy, a.D, o, c);
-#pragma unroll 2
+#pragma unroll 4
     for (int p = p0 + ty; p < p1; p += TY) {
         float v[V], u[V];
         load_v<IO, V>(x + p * a.sx.s1, v);
@@ -510,6 +626,12 @@ __global__ __launch_bounds__(256) void gn_apply_kernel(GnArgs a, PosGeom q, cons
 int pow2_at_least(int x) {
     int p = 1;
     while (p < x) p <<= 1;
+    return p;
+}
+
+int log2_at_least(int x) {
+    int p = 0;
+    while ((1 << p) < x) ++p;
     return p;
 }
 
@@ -536,16 +658,20 @@ bool vec_ok(const GnArgs &a, int V) {
 RowGeom row_geom(int N, int S, int G, int D, int V, int K, bool token_major, bool bwd) {
     RowGeom q;
     const int vecs = (D + V - 1) / V;
-    q.lpr = K > 1 ? 64 : pow2_at_least(vecs);
+    q.lpr = K > 1 ? 6 : log2_at_least(vecs);
     // neighbouring groups side by side where they are neighbours in memory
-    q.gp = 1;
-    while (token_major && q.gp * 2 * q.lpr <= 64 && G % (q.gp * 2) == 0) q.gp *= 2;
-    q.gblk = G / q.gp;
+    q.gp = 0;
+    while (token_major && q.gp + 1 + q.lpr <= 6 && G % (2 << q.gp) == 0) ++q.gp;
+    q.gblk = G >> q.gp;
+    q.div = ~0ull / (unsigned)S + 1;  // 0 for S = 1, which does not use it
     const long long rows = (long long)N * S;
-    const long long per = 4 * (64 / (q.lpr * q.gp));
+    const long long per = 4 * (64 >> (q.lpr + q.gp));
     long long want = (rows + per - 1) / per;
-    // the backward leaves one set of partials for each block of positions
-    const long long cap = bwd ? (2048 + q.gblk - 1) / q.gblk : (8192 + q.gblk - 1) / q.gblk;
+    // A workgroup loads its weights once, so it should not be too short, and the
+    // backward leaves one set of partials for each block of positions.  32768
+    // rows of 8 heads of 512, bfloat16: 8192 workgroups 113 us, 1024 take 146;
+    // the backward with 1024 173 us, 2048 185, 512 271.
+    const long long cap = ((bwd ? 1024 : 8192) + q.gblk - 1) / q.gblk;
     if (want > cap) want = cap;
     q.rblk = (int)want;
     return q;
@@ -556,6 +682,8 @@ PosGeom pos_geom(int N, int S, int C, int V) {
     const int cv = (C + V - 1) / V;
     const int p = pow2_at_least(cv);
     q.tx = p > 64 ? 64 : p;
+    // narrower where an eighth of the threads would have no channels
+    while (q.tx > 16 && ((cv + q.tx - 1) / q.tx * q.tx - cv) * 8 > cv) q.tx >>= 1;
     q.cblk = (cv + q.tx - 1) / q.tx;
     // about eight workgroups a compute unit, at least 16 positions a block
     const long long per = (long long)N * q.cblk;
@@ -567,12 +695,33 @@ PosGeom pos_geom(int N, int S, int C, int V) {
     return q;
 }
 
+bool group_fits(int S, int D) { return (long long)S * D <= 16384; }
+
+template <typename IO, int V, int ACT>
+hipError_t launch_group(const GnArgs &a, hipStream_t s) {
+    const int n = a.S * a.D;
+    const dim3 grid((unsigned)(a.N * a.G));
+    // 8 values a thread, 16 where 1024 threads need it
+    if (n > 8192) {
+        gn_group_kernel<IO, V, 16, ACT><<<grid, 1024, 0, s>>>(a);
+    } else {
+        const int th = ((n + 7) / 8 + 63) / 64 * 64;
+        gn_group_kernel<IO, V, 8, ACT><<<grid, th, 0, s>>>(a);
+    }
+    return hipGetLastError();
+}
+
 template <typename IO, int V, int ACT>
 hipError_t launch_seq(const GnArgs &a, hipStream_t s) {
     const int C = a.G * a.D;
     const PosGeom q = pos_geom(a.N, a.S, C, V);
     const dim3 grid((unsigned)(q.cblk * q.pblk * a.N)), groups((unsigned)(a.N * a.G));
     float *m0 = a.ws + (size_t)a.N * q.pblk * 2 * C, *m1 = m0 + (size_t)a.N * a.G;
+    if (!a.dy && group_fits(a.S, a.D)) {
+        // vectors only where none crosses into the next group
+        if (V == 1 || a.D % V == 0) return launch_group<IO, V, ACT>(a, s);
+        return launch_group<IO, 1, ACT>(a, s);
+    }
     if (!a.dy) {
         gn_channel_kernel<IO, V, ACT, false><<<grid, 256, 0, s>>>(a, q);
         if (a.mean) {
@@ -583,10 +732,9 @@ hipError_t launch_seq(const GnArgs &a, hipStream_t s) {
         gn_apply_kernel<IO, V, ACT, false><<<grid, 256, 0, s>>>(a, q, m0, m1);
     } else {
         gn_channel_kernel<IO, V, ACT, true><<<grid, 256, 0, s>>>(a, q);
-        gn_combine_kernel<true><<<groups, 256, 0, s>>>(a, q, m0, m1);
+        const unsigned sums = a.dw || a.db ? (C + 15) / 16 * 2 : 0;
+        gn_combine_kernel<true><<<dim3(groups.x + sums), 256, 0, s>>>(a, q, m0, m1);
         gn_apply_kernel<IO, V, ACT, true><<<grid, 256, 0, s>>>(a, q, m0, m1);
-        if (a.dw || a.db)
-            gn_wsum_kernel<<<dim3((C + 15) / 16, 2), 256, 0, s>>>(a.ws, a.dw, a.db, C, a.N * q.pblk);
     }
     return hipGetLastError();
 }

@@ -11,9 +11,25 @@ namespace mlstm {
 
 namespace {
 
+constexpr long long kCacheBytes = 256ll << 20;  // Infinity Cache
+
+// 16 bytes of state, past the caches' replacement order when STREAM
+template <bool STREAM>
+__device__ __forceinline__ f32x4 load(const float *p) {
+    if constexpr (STREAM) return __builtin_nontemporal_load((const f32x4 *)p);
+    return *(const f32x4 *)p;
+}
+template <bool STREAM>
+__device__ __forceinline__ void store(float *p, f32x4 x) {
+    if constexpr (STREAM)
+        __builtin_nontemporal_store(x, (f32x4 *)p);
+    else
+        *(f32x4 *)p = x;
+}
+
 // Workgroup: 256 threads = CT column threads (4 columns, 16 bytes each) x
 // 256 / CT row groups; thread (rg, ct) walks rows rg, rg + RG, ...
-template <typename IO, int CT>
+template <typename IO, int CT, bool STREAM>
 __global__ __launch_bounds__(256) void linattn_step_kernel(LinStepArgs a, int ntile) {
     constexpr int RG = 256 / CT;
     __shared__ float qs[256], ks[256];
@@ -38,12 +54,13 @@ __global__ __launch_bounds__(256) void linattn_step_kernel(LinStepArgs a, int nt
         const size_t base = (size_t)bh * a.dk * a.dv + col;
         const float *S = a.S_in ? a.S_in + base : nullptr;
         float *So = a.S_out + base;
-#pragma unroll 8
+        constexpr int UNROLL = STREAM ? 16 : 8;  // rows in flight
+#pragma unroll UNROLL
         for (int r = rg; r < a.dk; r += RG) {
             f32x4 x = vv * ks[r];
-            if (S) x += gam * *(const f32x4 *)(S + (size_t)r * a.dv);
+            if (S) x += gam * load<STREAM>(S + (size_t)r * a.dv);
             acc += qs[r] * x;
-            *(f32x4 *)(So + (size_t)r * a.dv) = x;
+            store<STREAM>(So + (size_t)r * a.dv, x);
         }
     }
     red[rg][ct] = acc;
@@ -60,17 +77,22 @@ __global__ __launch_bounds__(256) void linattn_step_kernel(LinStepArgs a, int nt
     }
 }
 
+template <typename IO, int CT, bool STREAM>
+hipError_t launch_ct(const LinStepArgs &a, hipStream_t s) {
+    const int ntile = (a.dv / 4 + CT - 1) / CT;
+    linattn_step_kernel<IO, CT, STREAM><<<dim3((unsigned)(a.B * a.H * ntile)), 256, 0, s>>>(a, ntile);
+    return hipGetLastError();
+}
+
 template <typename IO>
 hipError_t launch_t(const LinStepArgs &a, hipStream_t s) {
+    const long long cells = (long long)a.B * a.H;
     const int quads = a.dv / 4;
-    const int ct = quads >= 32 ? 32 : 16;
-    const int ntile = (quads + ct - 1) / ct;
-    const dim3 grid((unsigned)(a.B * a.H * ntile));
-    if (ct == 32)
-        linattn_step_kernel<IO, 32><<<grid, 256, 0, s>>>(a, ntile);
-    else
-        linattn_step_kernel<IO, 16><<<grid, 256, 0, s>>>(a, ntile);
-    return hipGetLastError();
+    if (cells * a.dk * a.dv * 8 > kCacheBytes && quads >= 64) return launch_ct<IO, 64, true>(a, s);
+    auto wgs = [&](int ct) { return cells * ((quads + ct - 1) / ct); };
+    if (quads >= 32 && wgs(32) >= 512) return launch_ct<IO, 32, false>(a, s);
+    if (quads >= 16 && wgs(16) >= 512) return launch_ct<IO, 16, false>(a, s);
+    return launch_ct<IO, 8, false>(a, s);
 }
 
 }  // namespace
