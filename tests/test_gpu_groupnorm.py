@@ -236,3 +236,27 @@ def test_behind_linear_attention():
         ot, _ = B.linattn_step(q[:, :, t], k[:, :, t], v[:, :, t], g, St)
         yt = B.groupnorm_fwd(ot[:, None], w, b, act="silu", return_stats=False)
         torch.testing.assert_close(yt[:, 0], y[:, t], rtol=0, atol=2e-4)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_layer_with_head_norm(io):
+    """layer_fwd(norm=...) is the layer's h, normalised head by head, token-major."""
+    from xlstm_mlstm_matrix_amd import inputs as I
+    w = I.layer_workload("layer_small", io=io)
+    d = {k: None if v is None else v.cuda() for k, v in I.gen_layer(w).items()}
+    args = [d[k] for k in ("x", "W_q", "W_k", "W_v", "W_o", "W_i", "W_f", "b_q", "b_k", "b_v", "b_o", "b_i", "b_f",
+                           "C0", "n0", "m0")]
+    h, st = B.layer_fwd(*args)
+    H, Bn, T, dv = h.shape
+    r = torch.Generator(device="cuda").manual_seed(1)
+    wt, bs = (torch.randn((H, dv), generator=r, device="cuda") for _ in range(2))
+    y, st2 = B.layer_fwd(*args, norm=dict(weight=wt, bias=bs, act="silu"))
+    assert y.shape == (Bn, T, H, dv) and y.is_contiguous()
+    assert all(torch.equal(a, b) for a, b in zip(st, st2))
+    ref = B.groupnorm_fwd(h.permute(1, 2, 0, 3).contiguous(), wt, bs, act="silu", return_stats=False)
+    assert torch.equal(y, ref)
+    ry, _, _ = O.groupnorm_forward(h.permute(1, 2, 0, 3), wt, bs, 1e-5, "silu")
+    assert np.abs(y.double().cpu().numpy() - ry).max() <= (HALF[io] * 1.01 + 2.0 ** -16) * np.abs(ry).max()
+    for bad in (dict(gamma=wt), dict(weight=wt[:, :8]), dict(act="tanh"), dict(eps=0.0)):
+        with pytest.raises((TypeError, ValueError)):
+            B.layer_fwd(*args, norm=bad)

