@@ -401,6 +401,23 @@ __device__ __forceinline__ long long gn_at(const Strides &st, int D, int n, int 
     return n * st.s0 + g * st.s2 + (c - g * D);
 }
 
+// Two values of each of V channels' groups (p0, p1 [.][G], `at` the first group's)
+template <int V>
+__device__ __forceinline__ void load_groups(const float *p0, const float *p1, size_t at, int c, int D, float *x0, float *x1) {
+    if (D % V == 0) {  // one group for the whole vector
+        const float a = p0[at + c / D], b = p1[at + c / D];
+#pragma unroll
+        for (int i = 0; i < V; ++i) x0[i] = a, x1[i] = b;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int g = (c + i) / D;
+            x0[i] = p0[at + g];
+            x1[i] = p1[at + g];
+        }
+    }
+}
+
 // sum over the rows ty of a workgroup, for V channels of each tx
 template <int V>
 __device__ __forceinline__ void gn_reduce(float *red, float (*t)[V], int tx, int TX, int ty, int TY) {
@@ -454,27 +471,16 @@ __global__ __launch_bounds__(256) void gn_channel_kernel(GnArgs a, PosGeom q) {
             }
         } else {
             const IO *dy = (const IO *)a.dy + gn_at(a.sdy, a.D, o, c);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const size_t si = (size_t)o * a.G + (c + i) / a.D;
-                mu[i] = a.seq ? a.mean[si] : 0.0f;
-                rs[i] = a.seq ? a.rstd[si] : 0.0f;
-                w[i] = a.w ? a.w[c + i] : 1.0f;
-                bb[i] = a.b ? a.b[c + i] : 0.0f;
-            }
+            if (a.seq) load_groups<V>(a.mean, a.rstd, (size_t)o * a.G, c, a.D, mu, rs);
+            load_w<V>(a.w, c, true, 1.0f, w);
+            load_w<V>(a.b, c, true, 0.0f, bb);
 #pragma unroll 2
             for (int p = p0 + ty; p < p1; p += TY) {
                 float v[V], u[V];
                 load_v<IO, V>(x + p * a.sx.s1, v);
                 load_v<IO, V>(dy + p * a.sdy.s1, u);
-                if (!a.seq) {  // each position has its own statistics
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const size_t si = ((size_t)o * a.S + p) * a.G + (c + i) / a.D;
-                        mu[i] = a.mean[si];
-                        rs[i] = a.rstd[si];
-                    }
-                }
+                // each position has its own statistics
+                if (!a.seq) load_groups<V>(a.mean, a.rstd, ((size_t)o * a.S + p) * a.G, c, a.D, mu, rs);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     const float xh = (v[i] - mu[i]) * rs[i];
@@ -502,9 +508,10 @@ __global__ __launch_bounds__(256) void gn_channel_kernel(GnArgs a, PosGeom q) {
     }
 }
 
-// Sum over r of channel c's two partials: 16 channels x 16 rows of a workgroup.
+// Sum over r of channel c's two partials: 16 channels x TY rows of a workgroup.
+template <int TY>
 __device__ __forceinline__ void gn_wsum(const float *ws, float *dw, float *db, int C, int rblk, int cblk, int which) {
-    __shared__ float red[16][17];
+    __shared__ float red[TY][17];
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int c = cblk * 16 + tx;
     float *out = which ? db : dw;
@@ -512,10 +519,10 @@ __device__ __forceinline__ void gn_wsum(const float *ws, float *dw, float *db, i
     float t = 0.0f;
     if (c < C)
 #pragma unroll 4
-        for (int r = ty; r < rblk; r += 16) t += ws[((size_t)r * 2 + which) * C + c];
+        for (int r = ty; r < rblk; r += TY) t += ws[((size_t)r * 2 + which) * C + c];
     red[ty][tx] = t;
     __syncthreads();
-    for (int m = 8; m > 0; m >>= 1) {
+    for (int m = TY / 2; m > 0; m >>= 1) {
         if (ty < m) red[ty][tx] += red[ty + m][tx];
         __syncthreads();
     }
@@ -523,56 +530,57 @@ __device__ __forceinline__ void gn_wsum(const float *ws, float *dw, float *db, i
 }
 
 // dw, db: sums of the partials [rblk][2][C] in ws over rblk; blockIdx.y is 0 for dw.
-__global__ __launch_bounds__(256) void gn_wsum_kernel(const float *ws, float *dw, float *db, int C, int rblk) {
-    gn_wsum(ws, dw, db, C, rblk, blockIdx.x, blockIdx.y);
+__global__ __launch_bounds__(1024) void gn_wsum_kernel(const float *ws, float *dw, float *db, int C, int rblk) {
+    gn_wsum<64>(ws, dw, db, C, rblk, blockIdx.x, blockIdx.y);
 }
 
 // One workgroup per (sample, group).  Forward: mean and rstd from the channels'
 // means and centred sums.  Backward: mean(u) and mean(u xh).  Written to
 // out0, out1 [N][G].  The workgroups past those sum dw and db.
+// Threads: tx channels x 1024 / tx blocks of positions.
 template <bool BWD>
-__global__ __launch_bounds__(256) void gn_combine_kernel(GnArgs a, PosGeom q, float *out0, float *out1) {
+__global__ __launch_bounds__(1024) void gn_combine_kernel(GnArgs a, PosGeom q, float *out0, float *out1) {
     __shared__ float red[16];
-    const int C = a.G * a.D, n = q.pblk * a.D;
+    const int C = a.G * a.D;
     if (BWD && (int)blockIdx.x >= a.N * a.G) {
         const int i = blockIdx.x - a.N * a.G;
-        gn_wsum(a.ws, a.dw, a.db, C, a.N * q.pblk, i >> 1, i & 1);
+        gn_wsum<64>(a.ws, a.dw, a.db, C, a.N * q.pblk, i >> 1, i & 1);
         return;
     }
     const int g = blockIdx.x % a.G, o = blockIdx.x / a.G;
+    const int sh = a.D >= 64 ? 6 : a.D >= 16 ? 4 : 2;  // log2 of the channels side by side
+    const int tx = threadIdx.x & ((1 << sh) - 1), ty = threadIdx.x >> sh, TY = 1024 >> sh;
     const float *ws = a.ws + (size_t)o * q.pblk * 2 * C + (size_t)g * a.D;
     const float total = (float)a.D * (float)a.S;
+    auto rows = [&](int pb) { return (float)(min(a.S, (pb + 1) * q.plen) - pb * q.plen); };
     float s0 = 0.0f, s1 = 0.0f;
-    for (int e = threadIdx.x; e < n; e += 256) {
-        const int pb = e / a.D, d = e % a.D;
-        const float *r = ws + (size_t)pb * 2 * C + d;
-        if constexpr (BWD) {
-            const float w = a.w ? a.w[g * a.D + d] : 1.0f;
-            s0 += w * r[C];
-            s1 += w * r[0];
-        } else {
-            s0 += r[0] * (float)(min(a.S, (pb + 1) * q.plen) - pb * q.plen);
+    for (int d = tx; d < a.D; d += 1 << sh) {
+        const float w = BWD && a.w ? a.w[g * a.D + d] : 1.0f;
+#pragma unroll 4
+        for (int pb = ty; pb < q.pblk; pb += TY) {
+            const float *r = ws + (size_t)pb * 2 * C + d;
+            if constexpr (BWD) {
+                s0 += w * r[C];
+                s1 += w * r[0];
+            } else {
+                s0 += r[0] * rows(pb);
+            }
         }
     }
-    float m0 = gn_block_sum(s0, red) / total;
-    if constexpr (BWD) {
-        const float m1 = gn_block_sum(s1, red) / total;
-        if (threadIdx.x == 0) {
-            out0[blockIdx.x] = m0;
-            out1[blockIdx.x] = m1;
-        }
-    } else {
-        for (int e = threadIdx.x; e < n; e += 256) {
-            const int pb = e / a.D, d = e % a.D;
-            const float *r = ws + (size_t)pb * 2 * C + d;
-            const float c = r[0] - m0;
-            s1 += r[C] + c * c * (float)(min(a.S, (pb + 1) * q.plen) - pb * q.plen);
-        }
-        const float var = gn_block_sum(s1, red) / total;
-        if (threadIdx.x == 0) {
-            out0[blockIdx.x] = m0;
-            out1[blockIdx.x] = rsqrtf(var + a.eps);
-        }
+    const float m0 = gn_block_sum(s0, red) / total;
+    if constexpr (!BWD) {
+        for (int d = tx; d < a.D; d += 1 << sh)
+#pragma unroll 4
+            for (int pb = ty; pb < q.pblk; pb += TY) {
+                const float *r = ws + (size_t)pb * 2 * C + d;
+                const float c = r[0] - m0;
+                s1 += r[C] + c * c * rows(pb);
+            }
+    }
+    const float m1 = gn_block_sum(s1, red) / total;
+    if (threadIdx.x == 0) {
+        out0[blockIdx.x] = m0;
+        out1[blockIdx.x] = BWD ? m1 : rsqrtf(m1 + a.eps);
     }
 }
 
@@ -586,21 +594,14 @@ __global__ __launch_bounds__(256) void gn_apply_kernel(GnArgs a, PosGeom q, cons
     if (c >= C) return;
     const int p0 = pb * q.plen, p1 = min(p0 + q.plen, a.S);
     float mu[V], rs[V], w[V], bb[V], c1[V], c2[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const size_t si = (size_t)o * a.G + (c + i) / a.D;
-        if constexpr (BWD) {
-            mu[i] = a.mean[si];
-            rs[i] = a.rstd[si];
-            c1[i] = in0[si];
-            c2[i] = in1[si];
-        } else {
-            mu[i] = in0[si];
-            rs[i] = in1[si];
-        }
-        w[i] = a.w ? a.w[c + i] : 1.0f;
-        bb[i] = a.b ? a.b[c + i] : 0.0f;
+    if constexpr (BWD) {
+        load_groups<V>(a.mean, a.rstd, (size_t)o * a.G, c, a.D, mu, rs);
+        load_groups<V>(in0, in1, (size_t)o * a.G, c, a.D, c1, c2);
+    } else {
+        load_groups<V>(in0, in1, (size_t)o * a.G, c, a.D, mu, rs);
     }
+    load_w<V>(a.w, c, true, 1.0f, w);
+    load_w<V>(a.b, c, true, 0.0f, bb);
     const IO *x = (const IO *)a.x + gn_at(a.sx, a.D, o, c);
     const IO *dy = BWD ? (const IO *)a.dy + gn_at(a.sdy, a.D, o, c) : nullptr;
     IO *y = (IO *)a.y + gn_at(a.sy, a.D, o, c);
@@ -685,10 +686,10 @@ PosGeom pos_geom(int N, int S, int C, int V) {
     // narrower where an eighth of the threads would have no channels
     while (q.tx > 16 && ((cv + q.tx - 1) / q.tx * q.tx - cv) * 8 > cv) q.tx >>= 1;
     q.cblk = (cv + q.tx - 1) / q.tx;
-    // about eight workgroups a compute unit, at least 16 positions a block
+    // about four workgroups a compute unit, at least 32 positions a block
     const long long per = (long long)N * q.cblk;
-    long long want = (2048 + per - 1) / per;
-    const long long most = (S + 15) / 16;
+    long long want = (1024 + per - 1) / per;
+    const long long most = (S + 31) / 32;
     if (want > most) want = most;
     q.plen = (int)((S + want - 1) / want);
     q.pblk = (S + q.plen - 1) / q.plen;
@@ -728,12 +729,12 @@ hipError_t launch_seq(const GnArgs &a, hipStream_t s) {
             m0 = a.mean;
             m1 = a.rstd;
         }
-        gn_combine_kernel<false><<<groups, 256, 0, s>>>(a, q, m0, m1);
+        gn_combine_kernel<false><<<groups, 1024, 0, s>>>(a, q, m0, m1);
         gn_apply_kernel<IO, V, ACT, false><<<grid, 256, 0, s>>>(a, q, m0, m1);
     } else {
         gn_channel_kernel<IO, V, ACT, true><<<grid, 256, 0, s>>>(a, q);
         const unsigned sums = a.dw || a.db ? (C + 15) / 16 * 2 : 0;
-        gn_combine_kernel<true><<<dim3(groups.x + sums), 256, 0, s>>>(a, q, m0, m1);
+        gn_combine_kernel<true><<<dim3(groups.x + sums), 1024, 0, s>>>(a, q, m0, m1);
         gn_apply_kernel<IO, V, ACT, true><<<grid, 256, 0, s>>>(a, q, m0, m1);
     }
     return hipGetLastError();
@@ -751,7 +752,7 @@ hipError_t launch_long_row(const GnArgs &a, hipStream_t s) {
             const int C = a.G * a.D;
             const PosGeom q = pos_geom(a.N, a.S, C, V);
             gn_channel_kernel<IO, V, ACT, true><<<dim3((unsigned)(q.cblk * q.pblk * a.N)), 256, 0, s>>>(a, q);
-            gn_wsum_kernel<<<dim3((C + 15) / 16, 2), 256, 0, s>>>(a.ws, a.dw, a.db, C, a.N * q.pblk);
+            gn_wsum_kernel<<<dim3((C + 15) / 16, 2), 1024, 0, s>>>(a.ws, a.dw, a.db, C, a.N * q.pblk);
         }
     }
     return hipGetLastError();
@@ -766,7 +767,7 @@ hipError_t launch_row(const GnArgs &a, hipStream_t s) {
     } else {
         gn_row_kernel<IO, V, K, ACT, true><<<grid, 256, 0, s>>>(a, q);
         const int C = a.G * a.D;
-        if (a.dw || a.db) gn_wsum_kernel<<<dim3((C + 15) / 16, 2), 256, 0, s>>>(a.ws, a.dw, a.db, C, q.rblk);
+        if (a.dw || a.db) gn_wsum_kernel<<<dim3((C + 15) / 16, 2), 1024, 0, s>>>(a.ws, a.dw, a.db, C, q.rblk);
     }
     return hipGetLastError();
 }
