@@ -27,7 +27,11 @@
  * a dimension of size 1 a stride is ignored.  An input may repeat rows along
  * the first and second dimension (stride 0).  An output's elements must not
  * overlap one another, and its extent (first to last byte) must not overlap
- * the extent of any other argument (MLSTM_ERR_ALIAS).
+ * the extent of any other argument (MLSTM_ERR_ALIAS); a layout whose
+ * dimensions do not nest by rising stride is taken for an overlap.
+ *
+ * Workspaces are scratch: nothing is kept in them, and two calls that may run
+ * at the same time (other streams, overlapping graphs) need separate ones.
  */
 #ifndef MLSTM_OPS_H
 #define MLSTM_OPS_H
@@ -63,7 +67,15 @@ typedef struct {
  *             when that is 0); contents on entry are irrelevant
  *
  * d_qk is a multiple of 16 up to 256 and d_v one up to 512, as for the cell
- * (MLSTM_ERR_UNSUPPORTED otherwise); B, H, T >= 1.
+ * (MLSTM_ERR_UNSUPPORTED otherwise); 1 <= T <= 2^30, B, H >= 1 and
+ * B * H < 2^19 (MLSTM_ERR_SHAPE).  q, k, v of a sequence's own tokens are
+ * finite, and so are S0 and what they add up to, below 1e26 in magnitude (the
+ * kernel holds the state scaled by up to 2^40); a NaN or an infinity reaches
+ * the outputs of its own 32-token chunk and everything after it.
+ *
+ * Precision.  float32: float32 products and sums.  bfloat16: scores and the
+ * read-out's copy of the state are rounded to bfloat16 once before they are
+ * multiplied, o once at the end; the state itself is exact to float32 sums.
  */
 mlstm_status_t mlstm_linattn_fwd_workspace_size(int B, int H, int T, int d_qk, int d_v,
                                                 mlstm_dtype_t io, size_t *bytes);
@@ -135,8 +147,9 @@ typedef enum {
  *  eps           > 0 (MLSTM_ERR_UNSUPPORTED otherwise)
  *  workspace     at least mlstm_groupnorm_workspace_size bytes, or NULL if that is 0
  *
- * N, S, G, D >= 1, any D.  D and the strides being multiples of 16 bytes
- * makes it faster, and is not required.  y may not be x.
+ * N, S, G, D >= 1, any D; N * S, G * D and N * G below 2^30 (MLSTM_ERR_SHAPE).
+ * D and the strides being multiples of 16 bytes makes it faster, and is not
+ * required.  y may not be x.
  */
 mlstm_status_t mlstm_groupnorm_workspace_size(int N, int S, int G, int D, mlstm_norm_over_t over,
                                               mlstm_dtype_t io, int backward, size_t *bytes);

@@ -103,6 +103,17 @@ def test_parity(io, over, shape):
     run(io, shape, over, {0: "none", 1: "silu", 2: "gelu"}[sum(shape) % 3], seed=sum(shape))
 
 
+@pytest.mark.parametrize("shape", [(2, 1700, 32, 10), (1, 3001, 3, 7), (2, 310, 2, 80), (1, 500, 1, 33), (3, 129, 4, 136),
+                                   (1, 2, 2, 9000)], ids=str)
+@pytest.mark.parametrize("head_major", [False, True])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_groups_too_large_for_one_workgroup(io, head_major, shape):
+    """Statistics joined from blocks of positions; vectors that cross groups,
+    vectors that do not, and single elements."""
+    assert shape[1] * shape[3] > 16384
+    run(io, shape, "sequence", "silu", head_major=head_major)
+
+
 @pytest.mark.parametrize("act", ["none", "silu", "gelu"])
 @pytest.mark.parametrize("over", ["token", "sequence"])
 @pytest.mark.parametrize("io", ["f32", "bf16"])

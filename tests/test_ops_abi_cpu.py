@@ -79,6 +79,7 @@ def test_linattn_common_refusals(call, need):
 
 def test_linattn_fwd_refusals():
     assert fwd(T=0) == SHAPE
+    assert fwd(T=(1 << 30) + 1, B=1, H=1) == SHAPE and bwd(T=(1 << 30) + 1, B=1, H=1) == SHAPE
     need = B.linattn_workspace_size(2, 3, 100, 64, 128, 1)
     if need:
         assert fwd(ws=None) == WS and fwd(n=need - 1) == WS
@@ -145,7 +146,7 @@ def test_groupnorm_refusals():
             assert call(**{n: 0}) == SHAPE
         assert call(io=5) == UNSUP and call(act=3) == UNSUP and call(over=2) == UNSUP
         assert call(x=M + 2) == ALIGN
-        assert call(ws=None) == WS
+        assert call(ws=None, S=4000) == WS
         assert call(G=1 << 20, D=1 << 12) == SHAPE
         assert call(N=1 << 20, S=1 << 12) == SHAPE
     for eps in (0.0, -1.0, float("nan")):
@@ -166,6 +167,9 @@ def test_workspace_queries():
     assert B.lib().mlstm_groupnorm_workspace_size(2, 3, 4, 0, 0, 1, 0, ctypes.byref(n)) == SHAPE
     assert n.value == 77
     assert B.groupnorm_workspace_size(2, 10, 3, 20, "sequence", B.BF16, True) > 0
+    assert B.groupnorm_workspace_size(2, 10, 3, 20, "sequence", B.BF16) == 0       # a workgroup holds a group
+    assert B.groupnorm_workspace_size(2, 4000, 3, 20, "sequence", B.BF16) > 0
+    assert B.groupnorm_workspace_size(2, 4000, 3, 64, "token", B.BF16) == 0
     with pytest.raises(ValueError):
         B.groupnorm_workspace_size(2, 10, 3, 20, "batch", B.BF16)
 

@@ -156,15 +156,22 @@ __global__ __launch_bounds__(256) void gn_row_kernel(GnArgs a, RowGeom q) {
     for (long long r0 = (long long)(rb * 4 + wave) * rpi; r0 < nrow; r0 += (long long)q.rblk * 4 * rpi) {
         const bool rok = r0 + rsub < nrow;
         const int r = rok ? (int)r0 + rsub : 0;
-        const int n = rok ? (a.S == 1 ? r : (int)__umul64hi((unsigned long long)r, q.div)) : 0, s = rok ? r - n * a.S : 0;
-        float v[K][V];
+        const int n = a.S == 1 ? r : (int)__umul64hi((unsigned long long)r, q.div), s = r - n * a.S;
+        const size_t si = ((size_t)n * a.S + s) * a.G + g;
+        // lanes without a position or channel hold zeros: they add nothing to any sum
+        float v[K][V], u[BWD ? K : 1][V];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) v[k][i] = 0.0f;
-            if (rok && ok[k]) load_v<IO, V>(x + n * a.sx.s0 + s * a.sx.s1 + d[k], v[k]);
+            for (int i = 0; i < V; ++i) {
+                v[k][i] = 0.0f;
+                if constexpr (BWD) u[k][i] = 0.0f;
+            }
+            if (rok && ok[k]) {
+                load_v<IO, V>(x + n * a.sx.s0 + s * a.sx.s1 + d[k], v[k]);
+                if constexpr (BWD) load_v<IO, V>(dy + n * a.sdy.s0 + s * a.sdy.s1 + d[k], u[k]);
+            }
         }
-        const size_t si = ((size_t)n * a.S + s) * a.G + g;
         if constexpr (!BWD) {
             float t = 0.0f;
 #pragma unroll
@@ -192,20 +199,12 @@ __global__ __launch_bounds__(256) void gn_row_kernel(GnArgs a, RowGeom q) {
                 if (rok && ok[k]) store_v<IO, V>(y + n * a.sy.s0 + s * a.sy.s1 + d[k], v[k]);
             }
         } else {
-            float u[K][V];
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) u[k][i] = 0.0f;
-                if (rok && ok[k]) load_v<IO, V>(dy + n * a.sdy.s0 + s * a.sdy.s1 + d[k], u[k]);
-            }
             const float mu = rok ? a.mean[si] : 0.0f, rs = rok ? a.rstd[si] : 0.0f;
             float c1 = 0.0f, c2 = 0.0f;
 #pragma unroll
             for (int k = 0; k < K; ++k)
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    if (!(rok && ok[k])) continue;
                     const float xh = (v[k][i] - mu) * rs;
                     const float dz = u[k][i] * act_d<ACT>(xh * w[k][i] + bb[k][i]);
                     ab[k][i] += dz;
@@ -809,7 +808,7 @@ size_t groupnorm_workspace_floats(int N, int S, int G, int D, int seq, int io_bf
                     const size_t r = (size_t)row_geom(N, S, G, D, V, k, tm, true).rblk;
                     f = r * 2 * C > f ? r * 2 * C : f;
                 }
-        } else if (seq || bwd) {
+        } else if (bwd || (seq && !group_fits(S, D))) {
             const PosGeom q = pos_geom(N, S, C, V);
             f = (size_t)N * q.pblk * 2 * C + (seq ? 2 * (size_t)N * G : 0);
         }

@@ -689,9 +689,10 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
         // rows behind the sequence's length
         const int z1 = min(tau0 + a.seg_len, T);
         constexpr int QPR = BV / 4;  // quads of a row
-        for (int e = tid; e < (z1 - max(n, tau0)) * QPR; e += C::NTH) {
+        const long long quads = (long long)max(z1 - max(n, tau0), 0) * QPR;
+        for (long long e = tid; e < quads; e += C::NTH) {
             const long long t = max(n, tau0) + e / QPR;
-            const int c = e % QPR * 4;
+            const int c = (int)(e % QPR) * 4;
             if (col0 + c < dv) {
                 if constexpr (ES == 4)
                     *(f32x4 *)(og + t * ldo + c) = f32x4{0, 0, 0, 0};

@@ -16,6 +16,7 @@ namespace {
 constexpr int kMaxDk = 256, kMaxDv = 512;
 // a chunk's rows are addressed through 32-bit byte offsets from its first one
 constexpr long long kMaxRowStride = ((long long)1 << 22) - 1;
+constexpr int kMaxT = 1 << 30;  // token indices, one segment past the last included, fit 32 bits
 
 // One strided tensor of a call: rows of `d` elements at (i0, i1, i2).
 struct View {
@@ -94,7 +95,7 @@ struct Extents {
 
 // Shapes of a linear attention call; *cells = B * H.
 mlstm_status_t lin_dims(int B, int H, int T, int dk, int dv, mlstm_dtype_t io, size_t *cells) {
-    if (B <= 0 || H <= 0 || T <= 0 || dk <= 0 || dv <= 0) return MLSTM_ERR_SHAPE;
+    if (B <= 0 || H <= 0 || T <= 0 || T > kMaxT || dk <= 0 || dv <= 0) return MLSTM_ERR_SHAPE;
     if (io != MLSTM_F32 && io != MLSTM_BF16) return MLSTM_ERR_UNSUPPORTED;
     if (dk > kMaxDk || dk % 16 || dv > kMaxDv || dv % 16) return MLSTM_ERR_UNSUPPORTED;
     // workgroups are counted in 32 bits; a cell has at most 4096 of them
