@@ -343,13 +343,17 @@ __global__ __launch_bounds__(1024) void gn_group_kernel(GnArgs a) {
     const int g = id % a.G, n = id / a.G;
     const int rv = a.D / V, total = a.S * rv;  // vectors of a position, of the group
     const IO *x = (const IO *)a.x + n * a.sx.s0 + g * a.sx.s2;
+    // e / rv for e < 2^15 and rv <= 2^14: the upper half of e * ceil(2^32 / rv)
+    const unsigned magic = 0xffffffffu / (unsigned)rv + 1;  // 0 for rv = 1
+    auto position = [&](int e) { return rv == 1 ? e : (int)__umulhi((unsigned)e, magic); };
     float v[NV][V], t = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int e = threadIdx.x + i * blockDim.x;
 #pragma unroll
         for (int j = 0; j < V; ++j) v[i][j] = 0.0f;
-        if (e < total) load_v<IO, V>(x + e / rv * a.sx.s1 + e % rv * V, v[i]);
+        const int p = position(e);
+        if (e < total) load_v<IO, V>(x + p * a.sx.s1 + (e - p * rv) * V, v[i]);
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -375,7 +379,7 @@ __global__ __launch_bounds__(1024) void gn_group_kernel(GnArgs a) {
     for (int i = 0; i < NV; ++i) {
         const int e = threadIdx.x + i * blockDim.x;
         if (e >= total) break;
-        const int p = e / rv, d = e % rv * V;
+        const int p = position(e), d = (e - p * rv) * V;
         float w[V], b[V];
         load_w<V>(a.w, (size_t)g * a.D + d, true, 1.0f, w);
         load_w<V>(a.b, (size_t)g * a.D + d, true, 0.0f, b);
