@@ -442,6 +442,9 @@ def _raw_stream(device) -> int:
 def _view(t, name, shape, dtype, device):
     """Check a strided tensor whose last dimension is contiguous."""
     import torch
+    if isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.device == device \
+            and (t.stride(-1) == 1 or shape[-1] == 1):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.shape != shape:
@@ -450,21 +453,27 @@ def _view(t, name, shape, dtype, device):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name} must have a contiguous last dimension")
+    raise ValueError(f"{name} must have a contiguous last dimension")
 
 
 def _dense(t, name, shape, dtype, device):
     """Check a dense tensor (None passes)."""
-    if t is None:
+    import torch
+    if t is None or (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype
+                     and t.device == device and t.is_contiguous()):
         return
     _req(t, name, dtype, device)
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _strides(*ts):
-    """mlstm_strides_t array of [., ., ., d] tensors (of [., ., d] ones: s2 = 0)."""
+    """mlstm_strides_t array of [., ., ., d] tensors (of [., ., d] ones: s2 = 0),
+    None where all are dense."""
+    for t in ts:
+        if not t.is_contiguous():
+            break
+    else:
+        return None
     flat = []
     for t in ts:
         flat += t.stride()[:-1] if t.dim() == 4 else (*t.stride()[:-1], 0)
