@@ -73,9 +73,9 @@ typedef struct {
  * kernel holds the state scaled by up to 2^40); a NaN or an infinity reaches
  * the outputs of its own 32-token chunk and everything after it.
  *
- * Precision.  float32: float32 products and sums.  bfloat16: scores and the
- * read-out's copy of the state are rounded to bfloat16 once before they are
- * multiplied, o once at the end; the state itself is exact to float32 sums.
+ * Precision.  float32: float32 products and sums.  bfloat16: the read-out's
+ * copy of the state is rounded to bfloat16 before it is multiplied, o at the
+ * end; scores keep 16 bits, the state itself is exact to float32 sums.
  */
 mlstm_status_t mlstm_linattn_fwd_workspace_size(int B, int H, int T, int d_qk, int d_v,
                                                 mlstm_dtype_t io, size_t *bytes);

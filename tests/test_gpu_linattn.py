@@ -7,10 +7,10 @@ number of terms of a sum.
  * float32: a sum of N terms in any order is off by at most N 2^-24 A, its
    products and decays by a few 2^-24 A each (a decay e^{gn} whose exponent
    still matters has |gn| < 32, so it is off by 32 * 2^-23 relative).
- * bfloat16 inputs are exact; scores (or their decayed products) may be
-   rounded to bfloat16 once before they meet v, 2^-8 A, and the state enters
-   a product as a high part and a remainder, 2^-16 A; the output is rounded once, 2^-8 |o|.
-   The states are float32 and only see the 2^-16 of decayed values in two parts.
+ * bfloat16 inputs are exact; the state's copy that meets q, or the scores that
+   meet v, may be rounded to bfloat16 once, 2^-8 A, the other of the two to 16
+   bits, 2^-16 A; the output is rounded once, 2^-8 |o|.  The states are float32:
+   2^-16 A is left for decayed values in parts.
 """
 import numpy as np
 import pytest

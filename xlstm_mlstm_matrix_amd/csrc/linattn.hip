@@ -26,8 +26,10 @@
 // lane group g4 stands for d_qk index 32 kk + 8 g4 + e, and for token
 // 16 (e / 4) + 4 g4 + e % 4.
 //
-// Roundings (bfloat16 I/O).  P and the read-out's copy of X are rounded to
-// bfloat16 once, which adds to the output about what its own rounding does.
+// Roundings (bfloat16 I/O).  The read-out's copy of X is rounded to bfloat16
+// once, which adds to the output about what its own rounding does.  P goes in two
+// parts (8 + 8 bits): with few tokens a single rounded score is all that an
+// output has, and its error does not average out (4 of 160 products more).
 // w_j v_j enters the state in three parts (8 + 8 + 8 bits of its 24), because
 // the state is handed out in float32 and carried over the whole sequence:
 // two parts would leave it 3e-6 off, three leave what float32 sums do.  X
@@ -74,13 +76,13 @@ template <>
 struct Types<bf16> {
     typedef bf16x8 Frag;
     static constexpr int EPG = 8;  // elements of a 16-byte granule
-    static constexpr int PARTS = 3;
+    static constexpr int PARTS = 3, PPARTS = 2;
 };
 template <>
 struct Types<float> {
     typedef f32x8 Frag;
     static constexpr int EPG = 4;
-    static constexpr int PARTS = 1;
+    static constexpr int PARTS = 1, PPARTS = 1;
 };
 
 __device__ __forceinline__ f32x4 mfma(const bf16x8 &a, const bf16x8 &b, f32x4 c) {
@@ -109,10 +111,10 @@ __device__ __forceinline__ void pack(const float *x, f32x8 &f) {
 // Two floats as a sum of PARTS roundings, elements 2 p and 2 p + 1 of PARTS
 // operands: each part is the rounded rest of the one before.  `here` keeps the
 // work in place: the compiler would move it behind the next branch.
-template <bool HERE>
+template <int PARTS, bool HERE>
 __device__ __forceinline__ void split2(float x0, float x1, bf16x8 *f, int p) {
 #pragma unroll
-    for (int q = 0; q < 3; ++q) {
+    for (int q = 0; q < PARTS; ++q) {
         const bf16x2 h = __builtin_convertvector((f32x2{x0, x1}), bf16x2);
         unsigned b = __builtin_bit_cast(unsigned, h);
         if constexpr (HERE) asm volatile("" : "+v"(b));
@@ -123,7 +125,7 @@ __device__ __forceinline__ void split2(float x0, float x1, bf16x8 *f, int p) {
         x1 -= __uint_as_float(b & 0xffff0000u);
     }
 }
-template <bool HERE>
+template <int PARTS, bool HERE>
 __device__ __forceinline__ void split2(float x0, float x1, f32x8 *f, int p) {
     f[0][2 * p] = x0;
     f[0][2 * p + 1] = x1;
@@ -277,7 +279,7 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
     using C = Cfg<IO, DKP, NCT, NW>;
     using Frag = typename Types<IO>::Frag;
     constexpr int NAT = C::NAT, NKS = C::NKS, QG = C::QG, VG = C::VG, BV = C::BV, NBUF = C::NBUF;
-    constexpr int PARTS = Types<IO>::PARTS;
+    constexpr int PARTS = Types<IO>::PARTS, PPARTS = Types<IO>::PPARTS;
     constexpr int ES = (int)sizeof(IO);
     // Q and K tiles of a chunk, double buffered where two fit.  Two arrays and
     // a loop over pairs of chunks, not one array indexed by parity: the compiler
@@ -511,7 +513,7 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
         // parts of w v: elements 2 p and 2 p + 1 of tile bt
         const float winv = wlane * inv;
         auto weigh = [&](int bt, int p) {
-            split2<EARLY>((float)vf[bt][2 * p] * (upow[2 * p] * winv), (float)vf[bt][2 * p + 1] * (upow[2 * p + 1] * winv),
+            split2<PARTS, EARLY>((float)vf[bt][2 * p] * (upow[2 * p] * winv), (float)vf[bt][2 * p + 1] * (upow[2 * p + 1] * winv),
                    vw[bt], p);
         };
         f32x4 O[2][NCT], S00 = {0, 0, 0, 0}, S10 = S00, S11 = S00;
@@ -574,7 +576,7 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
         }
 
         // the output, in three pieces that the state update's steps take along
-        Frag P[2];
+        Frag P[2][PPARTS];
         auto scores = [&]() {
             float p0[8], p1[8];
 #pragma unroll
@@ -586,8 +588,11 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
                 p1[r] = S10[r] * (upow[4 + r] * below);
                 p1[4 + r] = d >= 0 ? S11[r] * diag : 0.0f;
             }
-            pack(p0, P[0]);
-            pack(p1, P[1]);
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                split2<PPARTS, false>(p0[2 * p], p0[2 * p + 1], P[0], p);
+                split2<PPARTS, false>(p1[2 * p], p1[2 * p + 1], P[1], p);
+            }
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 // steps since the state was carried in; rows in front of a short chunk are not tokens
@@ -600,7 +605,9 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int bt = 0; bt < NCT; ++bt) O[t][bt] = mfma(vf[bt], P[t], O[t][bt]);
+                for (int bt = 0; bt < NCT; ++bt)
+#pragma unroll
+                    for (int q = 0; q < PPARTS; ++q) O[t][bt] = mfma(vf[bt], P[t][q], O[t][bt]);
         };
         auto output = [&]() {
             const auto os = __builtin_amdgcn_make_buffer_rsrc((void *)(og + (size_t)lo * ldo), 0,
