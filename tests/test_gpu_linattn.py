@@ -340,3 +340,25 @@ def test_step_of_states_larger_than_the_cache(io):
     u = 2.0 ** -24
     assert bool(((S1.double() - S64).abs() <= 16 * u * A).all())
     assert bool(((o.double() - ref).abs() <= HALF[io] * 1.01 * ref.abs() + (dk + 64) * u * oA).all())
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 1, 16, 16), (2, 2, 65, 64, 64), (1, 2, 700, 128, 128), (1, 1, 191, 256, 512),
+                                   (2, 3, 130, 80, 112)], ids=str)
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_outputs_without_state(io, shape):
+    """Calls that hand out no state (their kernels carry it less finely)."""
+    d = make(io, *shape, seed=7)
+    g, m = cu(d), mag(d)
+    s = shape[3] ** -0.5
+    N = shape[2] + 2 * max(shape[3], shape[4])
+    o = B.linattn_fwd(g["q"], g["k"], g["v"], g["g"], g["S0"], scale=s, return_state=False)
+    assert torch.is_tensor(o)
+    ro, _ = O.linattn_forward(d["q"], d["k"], d["v"], d["g"], d["S0"], scale=s)
+    Ao, _ = O.linattn_forward(m["q"], m["k"], m["v"], m["g"], m["S0"], scale=s)
+    check(o, ro, Ao, io, N, f"{io} {shape} o, no state")
+    got = B.linattn_bwd(g["q"], g["k"], g["v"], g["g"], g["do"], g["S0"], g["dS"], scale=s)
+    assert len(got) == 3
+    ref = O.linattn_backward(d["q"], d["k"], d["v"], d["g"], d["do"], d["S0"], d["dS"], scale=s)
+    A = O.linattn_backward(m["q"], m["k"], m["v"], m["g"], m["do"], m["S0"], m["dS"], scale=s)
+    for n, x, r, a in zip(("dq", "dk", "dv"), got, ref, A):
+        check(x, r, a, io, N, f"{io} {shape} {n}, no state")

@@ -29,11 +29,11 @@
 // Roundings (bfloat16 I/O).  The read-out's copy of X is rounded to bfloat16
 // once, which adds to the output about what its own rounding does.  P goes in two
 // parts (8 + 8 bits): with few tokens a single rounded score is all that an
-// output has, and its error does not average out (4 of 160 products more).
-// w_j v_j enters the state in three parts (8 + 8 + 8 bits of its 24), because
-// the state is handed out in float32 and carried over the whole sequence:
-// two parts would leave it 3e-6 off, three leave what float32 sums do.  X
-// itself, every decay and every sum are float32.  float32 I/O runs on the
+// output has, and its error does not average out (a fortieth more products).
+// w_j v_j enters the state in three parts (8 + 8 + 8 bits of its 24) where the
+// state is handed out: two parts would leave its float32 values 3e-6 off, three
+// leave what float32 sums do.  Where nobody sees the state but the read-out,
+// whose copy has 8 bits, two parts do.  X itself, every decay and every sum are float32.  float32 I/O runs on the
 // float32 MFMA without further rounding.
 #include "ops.hpp"
 
@@ -76,13 +76,13 @@ template <>
 struct Types<bf16> {
     typedef bf16x8 Frag;
     static constexpr int EPG = 8;  // elements of a 16-byte granule
-    static constexpr int PARTS = 3, PPARTS = 2;
+    static constexpr int PPARTS = 2;  // parts of P
 };
 template <>
 struct Types<float> {
     typedef f32x8 Frag;
     static constexpr int EPG = 4;
-    static constexpr int PARTS = 1, PPARTS = 1;
+    static constexpr int PPARTS = 1;
 };
 
 __device__ __forceinline__ f32x4 mfma(const bf16x8 &a, const bf16x8 &b, f32x4 c) {
@@ -274,12 +274,13 @@ struct Cfg {
 };
 
 // SO (state only): the first pass over segments, each from the zero state.
-template <typename IO, int DKP, int NCT, int NW, bool SO>
+// PARTS: parts of w v (1 for float32).
+template <typename IO, int DKP, int NCT, int NW, int PARTS, bool SO>
 __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) void linattn_kernel(KArgs a) {
     using C = Cfg<IO, DKP, NCT, NW>;
     using Frag = typename Types<IO>::Frag;
     constexpr int NAT = C::NAT, NKS = C::NKS, QG = C::QG, VG = C::VG, BV = C::BV, NBUF = C::NBUF;
-    constexpr int PARTS = Types<IO>::PARTS, PPARTS = Types<IO>::PPARTS;
+    constexpr int PPARTS = Types<IO>::PPARTS;
     constexpr int ES = (int)sizeof(IO);
     // Q and K tiles of a chunk, double buffered where two fit.  Two arrays and
     // a loop over pairs of chunks, not one array indexed by parity: the compiler
@@ -819,18 +820,29 @@ Plan make_plan(int B, int H, int T, int dk, int dv, int io_bf16, int backward) {
     return p;
 }
 
-template <typename IO, int DKP, int NCT, int NW>
-hipError_t launch_shape(const KArgs &a, hipStream_t s) {
+template <typename IO, int DKP, int NCT, int NW, int PARTS>
+hipError_t launch_parts(const KArgs &a, hipStream_t s) {
     const int cells = a.B * a.H;
     if (a.nseg > 1) {
-        linattn_kernel<IO, DKP, NCT, NW, true><<<dim3((unsigned)(cells * (a.nseg - 1) * a.tiles_all)), 64 * NW, 0, s>>>(a);
+        linattn_kernel<IO, DKP, NCT, NW, PARTS, true><<<dim3((unsigned)(cells * (a.nseg - 1) * a.tiles_all)), 64 * NW, 0, s>>>(a);
         int most = 0;
         for (int i = 0; i < a.njob; ++i) most = a.tiles[i] > most ? a.tiles[i] : most;
         const int quads = most * DKP * 4 * NCT * NW;
         linattn_scan_kernel<DKP, NCT, NW><<<dim3((unsigned)((quads + 255) / 256), (unsigned)cells, (unsigned)a.njob), 256, 0, s>>>(a);
     }
-    linattn_kernel<IO, DKP, NCT, NW, false><<<dim3((unsigned)(cells * a.nseg * a.tiles_all)), 64 * NW, 0, s>>>(a);
+    linattn_kernel<IO, DKP, NCT, NW, PARTS, false><<<dim3((unsigned)(cells * a.nseg * a.tiles_all)), 64 * NW, 0, s>>>(a);
     return hipGetLastError();
+}
+
+template <typename IO, int DKP, int NCT, int NW>
+hipError_t launch_shape(const KArgs &a, hipStream_t s) {
+    if constexpr (sizeof(IO) == 4) {
+        return launch_parts<IO, DKP, NCT, NW, 1>(a, s);
+    } else {
+        bool state = false;
+        for (int i = 0; i < a.njob; ++i) state |= a.job[i].Xn != nullptr;
+        return state ? launch_parts<IO, DKP, NCT, NW, 3>(a, s) : launch_parts<IO, DKP, NCT, NW, 2>(a, s);
+    }
 }
 
 template <typename IO>
