@@ -6,7 +6,10 @@
 //   dw = sum dz xh,  db = sum dz        (sums over samples and positions).
 //
 // All of it is bound by memory: x read and y written once (forward), x and dy
-// read and dx written once (backward).
+// read and dx written once (backward).  Measured over tokens, bfloat16,
+// 32768 rows of 8 heads of 512: 110 us (4.9 TB/s) forward, 194 us (4.15 TB/s)
+// backward; a large copy runs at 4.8.  Over long sequences x, and dy, are read
+// twice: 41 us forward and 59 backward at 15000 positions of 1280 channels.
 //
 // Over tokens a group is D contiguous channels: gn_row_kernel holds it in the
 // registers of a few lanes.  Over sequences, and for rows too long for that,
@@ -23,7 +26,8 @@ namespace {
 // Phi(z), the normal distribution function, and e = e^{-z^2/2}.  Abramowitz and
 // Stegun, Handbook of Mathematical Functions, 7.1.26 (erf to 1.5e-7): a
 // polynomial in 1 / (1 + p x) times e^{-x^2}, with x = |z| / sqrt(2), whose
-// exponential the derivative needs too; the backward is bound by this arithmetic.
+// exponential the derivative needs too.  Over 15000 positions of 1280 channels,
+// bfloat16, the backward takes 59 us with it, 52 with SiLU, 50 with neither.
 __device__ __forceinline__ float phi(float z, float *e) {
     const float x = fabsf(z) * 0.70710678f;
     const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.0f));
@@ -673,8 +677,8 @@ RowGeom row_geom(int N, int S, int G, int D, int V, int K, bool token_major, boo
     long long want = (rows + per - 1) / per;
     // A workgroup loads its weights once, so it should not be too short, and the
     // backward leaves one set of partials for each block of positions.  32768
-    // rows of 8 heads of 512, bfloat16: 8192 workgroups 113 us, 1024 take 146;
-    // the backward with 1024 173 us, 2048 185, 512 271.
+    // rows of 8 heads of 512, bfloat16: 8192 workgroups 115 us, 1024 take 148;
+    // the backward with 1024 194 us, 2048 take 203.
     const long long cap = ((bwd ? 1024 : 8192) + q.gblk - 1) / q.gblk;
     if (want > cap) want = cap;
     q.rblk = (int)want;
@@ -689,7 +693,9 @@ PosGeom pos_geom(int N, int S, int C, int V) {
     // narrower where an eighth of the threads would have no channels
     while (q.tx > 16 && ((cv + q.tx - 1) / q.tx * q.tx - cv) * 8 > cv) q.tx >>= 1;
     q.cblk = (cv + q.tx - 1) / q.tx;
-    // about four workgroups a compute unit, at least 32 positions a block
+    // About four workgroups a compute unit, at least 32 positions a block: the
+    // backward of 8192 positions of 2048 channels 42 us and of 320 channels 21;
+    // eight workgroups of at least 16 positions take 50 and 25.
     const long long per = (long long)N * q.cblk;
     long long want = (1024 + per - 1) / per;
     const long long most = (S + 31) / 32;
@@ -699,6 +705,8 @@ PosGeom pos_geom(int N, int S, int C, int V) {
     return q;
 }
 
+// Groups that a workgroup's registers hold need one launch for the forward: 8 x 32
+// groups of 1024 x 10 take 14.5 us, over blocks of positions 19.6.
 bool group_fits(int S, int D) { return (long long)S * D <= 16384; }
 
 template <typename IO, int V, int ACT>

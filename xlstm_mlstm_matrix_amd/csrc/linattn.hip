@@ -33,8 +33,14 @@
 // w_j v_j enters the state in three parts (8 + 8 + 8 bits of its 24) where the
 // state is handed out: two parts would leave its float32 values 3e-6 off, three
 // leave what float32 sums do.  Where nobody sees the state but the read-out,
-// whose copy has 8 bits, two parts do.  X itself, every decay and every sum are float32.  float32 I/O runs on the
-// float32 MFMA without further rounding.
+// whose copy has 8 bits, two parts do.  X itself, every decay and every sum are
+// float32.  float32 I/O runs on the float32 MFMA without further rounding.
+//
+// Measured (bfloat16, 4096 tokens, state handed out): 256 heads of 128 x 128 240
+// us, 4.5 TB/s, near a large copy's 4.8; 64 heads of 256 x 512 346 us, 2.4 TB/s.
+// There 256 workgroups leave a SIMD one wavefront, and its 526 vector
+// instructions a chunk, 160 of them MFMA, overlap little: the matrix units work
+// half of the time.  Without a state 310 us.
 #include "ops.hpp"
 
 namespace mlstm {
@@ -774,10 +780,11 @@ struct Plan {
 // fill the 256 compute units.  128 columns move Q and K through LDS half as
 // often as 64 do; segments cost a second reading of K and V and the states'
 // way through memory; so: 128 if that gives a workgroup each, else 64 if that
-// does, else 128 and segments for two each (of at least four chunks).  Measured:
-// backward of 64 heads of 128 x 128, 4096 tokens, 212 us with 64 columns, 237
-// with 128 and 3 segments; 64 heads forward 93 us with 8 segments of 128
-// columns, 127 with 4; 32 heads of 256 x 512 backward 604 us against 762.
+// does, else 128 and segments for two each (of at least four chunks).  Measured
+// (bfloat16, 4096 tokens): backward of 64 heads of 128 x 128 206 us with 64
+// columns, 220 with 128 and segments; of 32 heads of 256 x 512 580 against 676.
+// Segments for two workgroups a unit against one: forward of 128 heads of
+// 64 x 64 86 us against 110, of 64 heads of 128 x 128 95 against 98.
 Plan make_plan(int B, int H, int T, int dk, int dv, int io_bf16, int backward) {
     Plan p{};
     const int dims[3][2] = {{backward ? dv : dk, backward ? dk : dv}, {dk, dv}, {dv, dk}};
