@@ -362,3 +362,23 @@ def test_outputs_without_state(io, shape):
     A = O.linattn_backward(m["q"], m["k"], m["v"], m["g"], m["do"], m["S0"], m["dS"], scale=s)
     for n, x, r, a in zip(("dq", "dk", "dv"), got, ref, A):
         check(x, r, a, io, N, f"{io} {shape} {n}, no state")
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_largest_token_stride(io):
+    """Rows of 16 columns at the largest token stride, NaN between them: columns
+    past the tensor's count as zeros, whatever a row's offset adds up to."""
+    T, d = 40, 16
+    ld = (1 << 22) - (4 if io == "f32" else 8)
+    r = torch.Generator(device="cuda").manual_seed(9)
+    buf = torch.full((T * ld,), float("nan"), device="cuda", dtype=DT[io])
+    view = [torch.as_strided(buf, (1, 1, T, d), (0, 0, ld, 1), 64 * i) for i in range(4)]
+    for x in view:
+        x.copy_(torch.randn((1, 1, T, d), generator=r, device="cuda"))
+    flat = [x.contiguous() for x in view]
+    g = torch.tensor([-0.1], device="cuda")
+    for a, b in zip(B.linattn_fwd(*view[:3], g), B.linattn_fwd(*flat[:3], g)):
+        assert bool(torch.isfinite(b).all()) and torch.equal(a, b)
+    for a, b in zip(B.linattn_bwd(*view[:3], g, view[3], state_grad=True),
+                    B.linattn_bwd(*flat[:3], g, flat[3], state_grad=True)):
+        assert bool(torch.isfinite(b).all()) and torch.equal(a, b)

@@ -58,7 +58,10 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr int L = 32;           // tokens of a chunk
 constexpr int kBuf = 0x00020000; // word 3 of a raw, range-checked buffer descriptor
-constexpr unsigned kOut = 0xf0000000u;  // an offset past any range: reads zero, writes nothing
+// An offset past any range: reads zero, writes nothing.  A chunk's range and the
+// steps added to an offset are at most 2^29 bytes (32 rows of 2^22 floats), so it
+// stays past the range, and below 2^32, whatever is added or taken away.
+constexpr unsigned kOut = 0x80000000u;
 constexpr size_t kLds = 160 * 1024;
 constexpr long long kCUs = 256;  // compute units of an MI355X
 constexpr float kRenorm = 9.094947e-13f;  // sigma's least value, 2^-40
