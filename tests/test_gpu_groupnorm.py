@@ -271,3 +271,28 @@ def test_layer_with_head_norm(io):
     for bad in (dict(gamma=wt), dict(weight=wt[:, :8]), dict(act="tanh"), dict(eps=0.0)):
         with pytest.raises((TypeError, ValueError)):
             B.layer_fwd(*args, norm=bad)
+
+
+@pytest.mark.parametrize("out", [1e3, 1e5])
+def test_outlier_in_front_of_long_blocks(out):
+    """A first position far from all others, samples enough for one block each.
+
+    All terms of the centred sums are positive, so relative errors carry over.
+    Each of a lane's 32 steps is off by at most 4 u (difference, mean, product,
+    sum): 128 u.  The lanes' means and the joined one are off by 40 u of the latter
+    or of their own size, squared 80 u of their share.  Joining 64 lanes and 16
+    channels adds 40 u: 250 u of the variance, half of it in rstd, 7.5e-6, and 2 u
+    for the root.
+    """
+    N, S, G, D = 1024, 2048, 1, 16
+    x = torch.randn((N, S, G, D), generator=torch.Generator(device="cuda").manual_seed(4), device="cuda") + 3.0
+    x[:, 0] += out
+    _, m, r = B.groupnorm_fwd(x, over="sequence")
+    X = x.double()
+    mu = X.mean((1, 3))
+    rs = ((X - mu[:, None, :, None]) ** 2).mean((1, 3)).add(1e-5).rsqrt()
+    e = float((r.double() / rs - 1).abs().max())
+    print(f"[groupnorm] outlier {out}: rstd off by {e:.1e}", flush=True)
+    assert e <= 8e-6
+    # the mean: the bound of every other test
+    assert bool(((m.double() - mu).abs() <= (S * D / 64 + 64) * U * X.abs().mean((1, 3))).all())
