@@ -382,3 +382,26 @@ def test_largest_token_stride(io):
     for a, b in zip(B.linattn_bwd(*view[:3], g, view[3], state_grad=True),
                     B.linattn_bwd(*flat[:3], g, flat[3], state_grad=True)):
         assert bool(torch.isfinite(b).all()) and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dv", [128, 208])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_step_of_many_narrow_states(io, dv):
+    """More than 256 MB of states of 128 to 255 columns, a block that ends inside
+    one among them; float64 on the device."""
+    Bn, H, dk = 161, 16, 112
+    r = torch.Generator(device="cuda").manual_seed(3)
+    q, k = (torch.randn((Bn, H, dk), generator=r, device="cuda").to(DT[io]) for _ in range(2))
+    v = torch.randn((Bn, H, dv), generator=r, device="cuda").to(DT[io])
+    S = torch.randn((Bn, H, dk, dv), generator=r, device="cuda")
+    assert S.numel() * 8 > 256 << 20
+    g = torch.linspace(-2.0, 0.0, H, device="cuda")
+    G = torch.exp(g.double())[:, None, None]
+    kv = k.double()[..., None] * v.double()[..., None, :]
+    S64, A = G * S.double() + kv, G * S.double().abs() + kv.abs()
+    ref, oA = ((x[..., None] * y).sum(-2) for x, y in ((q.double(), S64), (q.double().abs(), A)))
+    o, S1 = B.linattn_step(q, k, v, g, S)
+    assert S1 is S
+    u = 2.0 ** -24
+    assert bool(((S1.double() - S64).abs() <= 16 * u * A).all())
+    assert bool(((o.double() - ref).abs() <= HALF[io] * 1.01 * ref.abs() + (dk + 64) * u * oA).all())

@@ -89,9 +89,13 @@ hipError_t launch_t(const LinStepArgs &a, hipStream_t s) {
     const long long cells = (long long)a.B * a.H;
     const int quads = a.dv / 4;
     // A state that the cache cannot hold is streamed past it (2 GB read and
-    // written: 386 us, 411 without); one that it holds is not (64 heads of
-    // 256 x 512: 12.7 us, streamed 38.7).
-    if (cells * a.dk * a.dv * 8 > kCacheBytes && quads >= 64) return launch_ct<IO, 64, true>(a, s);
+    // written: 386 us, 411 without; 1 GB of 128 x 128: 188 against 206); one that
+    // it holds is not (64 heads of 256 x 512: 12.7 us, streamed 38.7), nor are rows
+    // too short for it (1 GB of 64 x 64: 186 us, streamed 202).
+    if (cells * a.dk * a.dv * 8 > kCacheBytes) {
+        if (quads >= 64) return launch_ct<IO, 64, true>(a, s);
+        if (quads >= 32) return launch_ct<IO, 32, true>(a, s);
+    }
     // Two workgroups a compute unit where the columns allow it: those 64 heads
     // take 17.2 us with blocks of 128 columns throughout.
     auto wgs = [&](int ct) { return cells * ((quads + ct - 1) / ct); };
