@@ -73,11 +73,11 @@ typedef struct {
  * kernel holds the state scaled by up to 2^40); a NaN or an infinity reaches
  * the outputs of its own 32-token chunk and everything after it.
  *
- * Precision.  float32: float32 products and sums.  bfloat16: the read-out's
- * copy of the state is rounded to bfloat16 before it is multiplied, o at the
- * end; scores keep 16 bits, a state that is handed out is exact to float32
- * sums.  (Without S_T the carried state keeps 16 bits of each decayed product,
- * so o may differ in its last bit from that of a call with S_T.)
+ * Precision.  float32: float32 products and sums.  bfloat16: o is rounded once,
+ * at the end; the scores and the read-out's copy of the state keep 16 bits, a
+ * state that is handed out is exact to float32 sums.  (Without S_T the carried
+ * state keeps 16 bits of each decayed product, so o may differ in its last bit
+ * from that of a call with S_T.)
  */
 mlstm_status_t mlstm_linattn_fwd_workspace_size(int B, int H, int T, int d_qk, int d_v,
                                                 mlstm_dtype_t io, size_t *bytes);

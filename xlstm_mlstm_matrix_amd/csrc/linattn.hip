@@ -26,21 +26,22 @@
 // lane group g4 stands for d_qk index 32 kk + 8 g4 + e, and for token
 // 16 (e / 4) + 4 g4 + e % 4.
 //
-// Roundings (bfloat16 I/O).  The read-out's copy of X is rounded to bfloat16
-// once, which adds to the output about what its own rounding does.  P goes in two
-// parts (8 + 8 bits): with few tokens a single rounded score is all that an
-// output has, and its error does not average out (a fortieth more products).
+// Roundings (bfloat16 I/O).  The outputs are float32 work rounded once: the
+// read-out's copy of X goes in two parts (8 + 8 bits), and so does P, each off by
+// 2^-16 where the output's own rounding is off by 2^-8.  One part of X adds to
+// the output as much as its rounding does (2.2e-3 root mean square instead of
+// 1.7e-3), and far more where the products cancel; it is 20% faster (64 heads of
+// 256 x 512 340 us instead of 422, 256 heads of 128 x 128 238 instead of 280).
 // w_j v_j enters the state in three parts (8 + 8 + 8 bits of its 24) where the
 // state is handed out: two parts would leave its float32 values 3e-6 off, three
 // leave what float32 sums do.  Where nobody sees the state but the read-out,
-// whose copy has 8 bits, two parts do.  X itself, every decay and every sum are
+// whose copy has 16 bits, two parts do.  X itself, every decay and every sum are
 // float32.  float32 I/O runs on the float32 MFMA without further rounding.
 //
-// Measured (bfloat16, 4096 tokens, state handed out): 256 heads of 128 x 128 240
-// us, 4.5 TB/s, near a large copy's 4.8; 64 heads of 256 x 512 346 us, 2.4 TB/s.
-// There 256 workgroups leave a SIMD one wavefront, and its 526 vector
-// instructions a chunk, 160 of them MFMA, overlap little: the matrix units work
-// half of the time.  Without a state 310 us.
+// Measured (bfloat16, 4096 tokens, state handed out): 256 heads of 128 x 128 280
+// us, 3.8 TB/s, where a large copy has 4.8; 64 heads of 256 x 512 422 us, 1.9
+// TB/s.  There 256 workgroups leave a SIMD one wavefront, whose vector
+// instructions, 192 of them MFMA a chunk, overlap little.
 #include "ops.hpp"
 
 namespace mlstm {
@@ -85,13 +86,13 @@ template <>
 struct Types<bf16> {
     typedef bf16x8 Frag;
     static constexpr int EPG = 8;  // elements of a 16-byte granule
-    static constexpr int PPARTS = 2;  // parts of P
+    static constexpr int PPARTS = 2, XPARTS = 2;  // parts of P, of the read-out's copy of X
 };
 template <>
 struct Types<float> {
     typedef f32x8 Frag;
     static constexpr int EPG = 4;
-    static constexpr int PPARTS = 1;
+    static constexpr int PPARTS = 1, XPARTS = 1;
 };
 
 __device__ __forceinline__ f32x4 mfma(const bf16x8 &a, const bf16x8 &b, f32x4 c) {
@@ -111,10 +112,6 @@ __device__ __forceinline__ void pack(const float *x, bf16x8 &f) {
         f[2 * p] = h[0];
         f[2 * p + 1] = h[1];
     }
-}
-__device__ __forceinline__ void pack(const float *x, f32x8 &f) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = x[e];
 }
 
 // Two floats as a sum of PARTS roundings, elements 2 p and 2 p + 1 of PARTS
@@ -289,7 +286,7 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
     using C = Cfg<IO, DKP, NCT, NW>;
     using Frag = typename Types<IO>::Frag;
     constexpr int NAT = C::NAT, NKS = C::NKS, QG = C::QG, VG = C::VG, BV = C::BV, NBUF = C::NBUF;
-    constexpr int PPARTS = Types<IO>::PPARTS;
+    constexpr int PPARTS = Types<IO>::PPARTS, XPARTS = Types<IO>::XPARTS;
     constexpr int ES = (int)sizeof(IO);
     // Q and K tiles of a chunk, double buffered where two fit.  Two arrays and
     // a loop over pairs of chunks, not one array indexed by parity: the compiler
@@ -547,21 +544,24 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
                         kf[0][t] = cols.get(Ks, 0, t);
                     }
                 }
-                Frag xf[NCT];
+                Frag xf[NCT][XPARTS];
 #pragma unroll
                 for (int bt = 0; bt < NCT; ++bt) {
                     float x[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[e] = X[2 * kk + (e >> 2)][bt][e & 3];
-                    pack(x, xf[bt]);
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) split2<XPARTS, false>(x[2 * p], x[2 * p + 1], xf[bt], p);
                 }
                 S00 = mfma(k[u][0], q[u][0], S00);
                 S10 = mfma(k[u][0], q[u][1], S10);
                 S11 = mfma(k[u][1], q[u][1], S11);
 #pragma unroll
-                for (int bt = 0; bt < NCT; ++bt)
+                for (int r = 0; r < XPARTS; ++r)
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) O[t][bt] = mfma(xf[bt], q[u][t], O[t][bt]);
+                    for (int bt = 0; bt < NCT; ++bt)
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) O[t][bt] = mfma(xf[bt][r], q[u][t], O[t][bt]);
 #pragma unroll
                 for (int i = 0; i < 4 * NCT; ++i)
                     if (EARLY && i * NKS / (4 * NCT) == kk) weigh(i >> 2, i & 3);
