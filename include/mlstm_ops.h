@@ -149,7 +149,8 @@ typedef enum {
  *  eps           > 0 (MLSTM_ERR_UNSUPPORTED otherwise)
  *  workspace     at least mlstm_groupnorm_workspace_size bytes, or NULL if that is 0
  *
- * N, S, G, D >= 1, any D; N * S, G * D and N * G below 2^30 (MLSTM_ERR_SHAPE).
+ * N, S, G, D >= 1, any D; N * S, G * D and N * G below 2^30 and N * ceil(G D / 64)
+ * below 2^28 (MLSTM_ERR_SHAPE).
  * D and the strides being multiples of 16 bytes makes it faster, and is not
  * required.  y may not be x.
  */

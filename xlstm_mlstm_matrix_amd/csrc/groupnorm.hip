@@ -134,11 +134,11 @@ struct RowGeom {
 };
 
 template <typename IO, int V, int K, int ACT, bool BWD>
-__global__ __launch_bounds__(256) void gn_row_kernel(GnArgs a, RowGeom q) {
+__global__ __launch_bounds__(256) void gn_row_kernel(GnArgs a, RowGeom q, int first) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lpr = 1 << q.lpr, sub = lane >> q.lpr, ln = lane & (lpr - 1);
     const int rpi = 64 >> (q.lpr + q.gp);  // positions side by side in a wavefront
-    const int gb = blockIdx.x % q.gblk, rb = blockIdx.x / q.gblk;
+    const int block = first + blockIdx.x, gb = block % q.gblk, rb = block / q.gblk;
     const int g = (gb << q.gp) + (sub & ((1 << q.gp) - 1)), rsub = sub >> q.gp;
     const int D = a.D, nrow = a.N * a.S;
     const IO *x = (const IO *)a.x + g * a.sx.s2;
@@ -338,12 +338,12 @@ __global__ __launch_bounds__(256) void gn_long_row_kernel(GnArgs a, long long ro
 // ---- over sequences, groups of up to 16384 values: a workgroup holds a
 // group in registers (NE values a thread), one launch instead of three.
 template <typename IO, int V, int NE, int ACT>
-__global__ __launch_bounds__(1024) void gn_group_kernel(GnArgs a) {
+__global__ __launch_bounds__(1024) void gn_group_kernel(GnArgs a, int first) {
     constexpr int NV = NE / V;
     __shared__ float red[16];
     // neighbouring groups, which share cache lines, on one XCD (workgroups go round the 8)
     const int nwg = gridDim.x, xq = nwg >> 3, xr = nwg & 7, xcd = blockIdx.x & 7;
-    const int id = xcd * xq + min(xcd, xr) + (blockIdx.x >> 3);
+    const int id = first + xcd * xq + min(xcd, xr) + (blockIdx.x >> 3);
     const int g = id % a.G, n = id / a.G;
     const int rv = a.D / V, total = a.S * rv;  // vectors of a position, of the group
     const IO *x = (const IO *)a.x + n * a.sx.s0 + g * a.sx.s2;
@@ -444,12 +444,12 @@ __device__ __forceinline__ void gn_reduce(float *red, float *t, int tx, int TX, 
 // BWD false: mean and centred sum of squares of each channel of the block;
 // true: sum dz and sum dz xh.
 template <typename IO, int V, int ACT, bool BWD>
-__global__ __launch_bounds__(256) void gn_channel_kernel(GnArgs a, PosGeom q) {
+__global__ __launch_bounds__(256) void gn_channel_kernel(GnArgs a, PosGeom q, int first) {
     __shared__ float red[256];
     const int C = a.G * a.D;
     const int tx = threadIdx.x % q.tx, ty = threadIdx.x / q.tx, TY = 256 / q.tx;
-    const int cb = blockIdx.x % q.cblk;
-    const int pb = blockIdx.x / q.cblk % q.pblk, o = blockIdx.x / q.cblk / q.pblk;
+    const int block = first + blockIdx.x, cb = block % q.cblk;
+    const int pb = block / q.cblk % q.pblk, o = block / q.cblk / q.pblk;
     const int c = (cb * q.tx + tx) * V;
     const bool ok = c < C;
     const int p0 = pb * q.plen, p1 = min(p0 + q.plen, a.S);
@@ -552,8 +552,8 @@ __device__ __forceinline__ void gn_wsum(const float *ws, float *dw, float *db, i
 }
 
 // dw, db: sums of the partials [rblk][2][C] in ws over rblk; blockIdx.y is 0 for dw.
-__global__ __launch_bounds__(1024) void gn_wsum_kernel(const float *ws, float *dw, float *db, int C, int rblk) {
-    gn_wsum<64>(ws, dw, db, C, rblk, blockIdx.x, blockIdx.y);
+__global__ __launch_bounds__(1024) void gn_wsum_kernel(const float *ws, float *dw, float *db, int C, int rblk, int first) {
+    gn_wsum<64>(ws, dw, db, C, rblk, first + blockIdx.x, blockIdx.y);
 }
 
 // One workgroup per (sample, group).  Forward: mean and rstd from the channels'
@@ -561,15 +561,16 @@ __global__ __launch_bounds__(1024) void gn_wsum_kernel(const float *ws, float *d
 // out0, out1 [N][G].  The workgroups past those sum dw and db.
 // Threads: tx channels x 1024 / tx blocks of positions.
 template <bool BWD>
-__global__ __launch_bounds__(1024) void gn_combine_kernel(GnArgs a, PosGeom q, float *out0, float *out1) {
+__global__ __launch_bounds__(1024) void gn_combine_kernel(GnArgs a, PosGeom q, float *out0, float *out1, int first) {
     __shared__ float red[16];
     const int C = a.G * a.D;
-    if (BWD && (int)blockIdx.x >= a.N * a.G) {
-        const int i = blockIdx.x - a.N * a.G;
+    const int block = first + blockIdx.x;
+    if (BWD && block >= a.N * a.G) {
+        const int i = block - a.N * a.G;
         gn_wsum<64>(a.ws, a.dw, a.db, C, a.N * q.pblk, i >> 1, i & 1);
         return;
     }
-    const int g = blockIdx.x % a.G, o = blockIdx.x / a.G;
+    const int g = block % a.G, o = block / a.G;
     const int sh = a.D >= 64 ? 6 : a.D >= 16 ? 4 : 2;  // log2 of the channels side by side
     const int tx = threadIdx.x & ((1 << sh) - 1), ty = threadIdx.x >> sh, TY = 1024 >> sh;
     const float *ws = a.ws + (size_t)o * q.pblk * 2 * C + (size_t)g * a.D;
@@ -601,17 +602,17 @@ __global__ __launch_bounds__(1024) void gn_combine_kernel(GnArgs a, PosGeom q, f
     }
     const float m1 = gn_block_sum(s1, red) / total;
     if (threadIdx.x == 0) {
-        out0[blockIdx.x] = m0;
-        out1[blockIdx.x] = BWD ? m1 : rsqrtf(m1 + a.eps);
+        out0[block] = m0;
+        out1[block] = BWD ? m1 : rsqrtf(m1 + a.eps);
     }
 }
 
 template <typename IO, int V, int ACT, bool BWD>
-__global__ __launch_bounds__(256) void gn_apply_kernel(GnArgs a, PosGeom q, const float *in0, const float *in1) {
+__global__ __launch_bounds__(256) void gn_apply_kernel(GnArgs a, PosGeom q, const float *in0, const float *in1, int first) {
     const int C = a.G * a.D;
     const int tx = threadIdx.x % q.tx, ty = threadIdx.x / q.tx, TY = 256 / q.tx;
-    const int cb = blockIdx.x % q.cblk;
-    const int pb = blockIdx.x / q.cblk % q.pblk, o = blockIdx.x / q.cblk / q.pblk;
+    const int block = first + blockIdx.x, cb = block % q.cblk;
+    const int pb = block / q.cblk % q.pblk, o = block / q.cblk / q.pblk;
     const int c = (cb * q.tx + tx) * V;
     if (c >= C) return;
     const int p0 = pb * q.plen, p1 = min(p0 + q.plen, a.S);
@@ -645,6 +646,19 @@ __global__ __launch_bounds__(256) void gn_apply_kernel(GnArgs a, PosGeom q, cons
 }
 
 // ---- plans
+
+// HIP takes fewer than 2^32 threads a launch: launch(workgroups, first one) for
+// runs of at most 2^31 threads, until one fails.
+template <typename F>
+hipError_t in_runs(long long blocks, int threads, F launch) {
+    const long long run = (1ll << 31) / threads;
+    for (long long first = 0; first < blocks; first += run) {
+        launch((unsigned)(blocks - first < run ? blocks - first : run), (int)first);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
 
 int pow2_at_least(int x) {
     int p = 1;
@@ -727,75 +741,88 @@ bool group_fits(int S, int D) { return (long long)S * D <= 16384; }
 template <typename IO, int V, int ACT>
 hipError_t launch_group(const GnArgs &a, hipStream_t s) {
     const int n = a.S * a.D;
-    const dim3 grid((unsigned)(a.N * a.G));
+    const long long groups = (long long)a.N * a.G;
     // 8 values a thread, 16 where 1024 threads need it
-    if (n > 8192) {
-        gn_group_kernel<IO, V, 16, ACT><<<grid, 1024, 0, s>>>(a);
-    } else {
-        const int th = ((n + 7) / 8 + 63) / 64 * 64;
-        gn_group_kernel<IO, V, 8, ACT><<<grid, th, 0, s>>>(a);
-    }
-    return hipGetLastError();
+    if (n > 8192)
+        return in_runs(groups, 1024, [&](unsigned grid, int first) {
+            gn_group_kernel<IO, V, 16, ACT><<<grid, 1024, 0, s>>>(a, first);
+        });
+    const int th = ((n + 7) / 8 + 63) / 64 * 64;
+    return in_runs(groups, th, [&](unsigned grid, int first) {
+        gn_group_kernel<IO, V, 8, ACT><<<grid, th, 0, s>>>(a, first);
+    });
+}
+
+// the channels' sums over each block of positions
+template <typename IO, int V, int ACT, bool BWD>
+hipError_t launch_channel(const GnArgs &a, const PosGeom &q, hipStream_t s) {
+    return in_runs((long long)q.cblk * q.pblk * a.N, 256, [&](unsigned grid, int first) {
+        gn_channel_kernel<IO, V, ACT, BWD><<<grid, 256, 0, s>>>(a, q, first);
+    });
+}
+
+// dw and db from rblk sets of partials
+hipError_t launch_wsum(const GnArgs &a, int rblk, hipStream_t s) {
+    const int C = a.G * a.D;
+    return in_runs((C + 15) / 16, 2 * 1024, [&](unsigned grid, int first) {
+        gn_wsum_kernel<<<dim3(grid, 2), 1024, 0, s>>>(a.ws, a.dw, a.db, C, rblk, first);
+    });
+}
+
+template <typename IO, int V, int ACT, bool BWD>
+hipError_t launch_blocks(const GnArgs &a, const PosGeom &q, float *m0, float *m1, hipStream_t s) {
+    hipError_t e = launch_channel<IO, V, ACT, BWD>(a, q, s);
+    if (e != hipSuccess) return e;
+    const long long sums = a.dw || a.db ? (a.G * a.D + 15) / 16 * 2 : 0;
+    e = in_runs((long long)a.N * a.G + sums, 1024, [&](unsigned grid, int first) {
+        gn_combine_kernel<BWD><<<grid, 1024, 0, s>>>(a, q, m0, m1, first);
+    });
+    if (e != hipSuccess) return e;
+    return in_runs((long long)q.cblk * q.pblk * a.N, 256, [&](unsigned grid, int first) {
+        gn_apply_kernel<IO, V, ACT, BWD><<<grid, 256, 0, s>>>(a, q, m0, m1, first);
+    });
 }
 
 template <typename IO, int V, int ACT>
 hipError_t launch_seq(const GnArgs &a, hipStream_t s) {
     const int C = a.G * a.D;
     const PosGeom q = pos_geom(a.N, a.S, C, V);
-    const dim3 grid((unsigned)(q.cblk * q.pblk * a.N)), groups((unsigned)(a.N * a.G));
     float *m0 = a.ws + (size_t)a.N * q.pblk * 2 * C, *m1 = m0 + (size_t)a.N * a.G;
-    if (!a.dy && group_fits(a.S, a.D)) {
+    if (a.dy) return launch_blocks<IO, V, ACT, true>(a, q, m0, m1, s);
+    if (group_fits(a.S, a.D)) {
         // vectors only where none crosses into the next group
         if (V == 1 || a.D % V == 0) return launch_group<IO, V, ACT>(a, s);
         return launch_group<IO, 1, ACT>(a, s);
     }
-    if (!a.dy) {
-        gn_channel_kernel<IO, V, ACT, false><<<grid, 256, 0, s>>>(a, q);
-        if (a.mean) {
-            m0 = a.mean;
-            m1 = a.rstd;
-        }
-        gn_combine_kernel<false><<<groups, 1024, 0, s>>>(a, q, m0, m1);
-        gn_apply_kernel<IO, V, ACT, false><<<grid, 256, 0, s>>>(a, q, m0, m1);
-    } else {
-        gn_channel_kernel<IO, V, ACT, true><<<grid, 256, 0, s>>>(a, q);
-        const unsigned sums = a.dw || a.db ? (C + 15) / 16 * 2 : 0;
-        gn_combine_kernel<true><<<dim3(groups.x + sums), 1024, 0, s>>>(a, q, m0, m1);
-        gn_apply_kernel<IO, V, ACT, true><<<grid, 256, 0, s>>>(a, q, m0, m1);
-    }
-    return hipGetLastError();
+    return launch_blocks<IO, V, ACT, false>(a, q, a.mean ? a.mean : m0, a.mean ? a.rstd : m1, s);
 }
 
 template <typename IO, int V, int ACT>
 hipError_t launch_long_row(const GnArgs &a, hipStream_t s) {
     const long long rows = (long long)a.N * a.S * a.G;
     const dim3 grid((unsigned)(rows < 16384 ? rows : 16384));
-    if (!a.dy) {
+    if (!a.dy)
         gn_long_row_kernel<IO, V, ACT, false><<<grid, 256, 0, s>>>(a, rows);
-    } else {
+    else
         gn_long_row_kernel<IO, V, ACT, true><<<grid, 256, 0, s>>>(a, rows);
-        if (a.dw || a.db) {
-            const int C = a.G * a.D;
-            const PosGeom q = pos_geom(a.N, a.S, C, V);
-            gn_channel_kernel<IO, V, ACT, true><<<dim3((unsigned)(q.cblk * q.pblk * a.N)), 256, 0, s>>>(a, q);
-            gn_wsum_kernel<<<dim3((C + 15) / 16, 2), 1024, 0, s>>>(a.ws, a.dw, a.db, C, a.N * q.pblk);
-        }
-    }
-    return hipGetLastError();
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !(a.dw || a.db)) return e;
+    const PosGeom q = pos_geom(a.N, a.S, a.G * a.D, V);
+    e = launch_channel<IO, V, ACT, true>(a, q, s);
+    return e != hipSuccess ? e : launch_wsum(a, a.N * q.pblk, s);
 }
 
 template <typename IO, int V, int K, int ACT>
 hipError_t launch_row(const GnArgs &a, hipStream_t s) {
     const RowGeom q = row_geom(a.N, a.S, a.G, a.D, V, K, a.sx.s2 < a.sx.s1, a.dy != nullptr);
-    const dim3 grid((unsigned)(q.gblk * q.rblk));
-    if (!a.dy) {
-        gn_row_kernel<IO, V, K, ACT, false><<<grid, 256, 0, s>>>(a, q);
-    } else {
-        gn_row_kernel<IO, V, K, ACT, true><<<grid, 256, 0, s>>>(a, q);
-        const int C = a.G * a.D;
-        if (a.dw || a.db) gn_wsum_kernel<<<dim3((C + 15) / 16, 2), 1024, 0, s>>>(a.ws, a.dw, a.db, C, q.rblk);
-    }
-    return hipGetLastError();
+    const hipError_t e = in_runs((long long)q.gblk * q.rblk, 256, [&](unsigned grid, int first) {
+        if (!a.dy)
+            gn_row_kernel<IO, V, K, ACT, false><<<grid, 256, 0, s>>>(a, q, first);
+        else
+            gn_row_kernel<IO, V, K, ACT, true><<<grid, 256, 0, s>>>(a, q, first);
+    });
+    if (e != hipSuccess || !(a.dw || a.db)) return e;
+    return launch_wsum(a, q.rblk, s);
 }
 
 template <typename IO, int ACT>

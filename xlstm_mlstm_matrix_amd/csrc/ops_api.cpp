@@ -273,7 +273,8 @@ static mlstm_status_t gn_dims(int N, int S, int G, int D, mlstm_norm_over_t over
     if (N <= 0 || S <= 0 || G <= 0 || D <= 0) return MLSTM_ERR_SHAPE;
     if (io != MLSTM_F32 && io != MLSTM_BF16) return MLSTM_ERR_UNSUPPORTED;
     if (over != MLSTM_NORM_TOKEN && over != MLSTM_NORM_SEQUENCE) return MLSTM_ERR_UNSUPPORTED;
-    // positions, channels and samples x groups are counted in 32 bits, workgroups too
+    // positions, channels and samples x groups are counted in 32 bits, and so are
+    // workgroups of at least 16 channels of a sample, four for each 64
     size_t n;
     if (!mul_ok((size_t)G, (size_t)D, &n) || n > (size_t)INT32_MAX / 2) return MLSTM_ERR_SHAPE;
     if (!mul_ok((size_t)N, (size_t)S, &n) || n > (size_t)INT32_MAX / 2) return MLSTM_ERR_SHAPE;
