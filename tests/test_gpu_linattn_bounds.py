@@ -48,3 +48,50 @@ def test_bfloat16_outputs_are_rounded_once(shape, state):
     for n, x, r, a in zip(("dq", "dk", "dv"), gr, bw(d), bw(m)):
         # only the passes that share a launch with the state's carry it in three parts
         close(x, r, a, N, 3, f"{what} {n}")
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_state_through_many_segments(io):
+    """A state that decays slowly through 512 segments is not pulled one way.
+
+    Each segment rounds an element twice, by at most u of it either way: over 511
+    segments a standard deviation below sqrt(2 * 511 / 3) u = 19 u, in the mean of
+    4096 elements 0.3 u.  What all elements share: the decay's logarithm in base 2
+    (|g| T u <= 1.1 u), the last segment's power (4 u) and the tokens' own weights
+    (40 u of at most a tenth of the state): 10 u.  So the mean is held to 12 u; a
+    rounded factor may add 511 u / 2.
+    """
+    T, d = 65536, 64
+    r = np.random.default_rng(17)
+    # decays whose power of a 128-token segment lies far from a float
+    cand = -r.uniform(2e-6, 1.6e-5, 4000).astype(np.float32)
+    f = np.exp2((cand * np.float32(1.4426950408889634)).astype(np.float64) * 128)
+    off = (f.astype(np.float32) - f) / U
+    for g in cand[[int(off.argmin()), int(off.argmax())]]:
+        k, v = (torch.from_numpy(r.normal(0, s, (1, 1, T, d)).astype(np.float32)) for s in (0.01, 1.0))
+        k, v = ((x.bfloat16() if io == "bf16" else x).cuda() for x in (k, v))
+        S0 = torch.from_numpy(r.uniform(100, 200, (1, 1, d, d)).astype(np.float32)).cuda()
+        decay = torch.tensor([g], device="cuda")
+        _, S = B.linattn_fwd(k, k, v, decay, S0)
+        w = torch.exp(decay.double() * torch.arange(T - 1, -1, -1, device="cuda"))[:, None]
+        ref = S0.double() * torch.exp(decay.double() * T) + (k[0, 0].double() * w).T @ v[0, 0].double()
+        e = (S.double() / ref - 1).mean().item() / U
+        print(f"[linattn] {io} decay {g:.3e}: mean error {e:.2f} u", flush=True)
+        assert abs(e) <= 12
+
+
+@pytest.mark.parametrize("T", [1, 5, 32, 40])
+def test_states_of_short_bfloat16_sequences(T):
+    """A state that is handed out is as float32 sums leave it: u for each sum and
+    40 u for a product's weight, a product of five powers each good to 2 u and
+    rounded four times, of exponents below 3.  Two parts of it instead of three
+    would be off by up to 2^-16 = 256 u.
+    """
+    d = make("bf16", 2, 3, T, 64, 64, seed=T, decay=[-0.05, -0.01, 0.0])
+    g, m = cu(d), mag(d)
+    _, S = B.linattn_fwd(g["q"], g["k"], g["v"], g["g"], g["S0"])
+    _, ref = O.linattn_forward(d["q"], d["k"], d["v"], d["g"], d["S0"])
+    _, A = O.linattn_forward(m["q"], m["k"], m["v"], m["g"], m["S0"])
+    bad = (np.abs(S.double().cpu().numpy() - ref) / ((40 + T) * U * A)).max()
+    print(f"[linattn] state of {T} tokens: {bad:.3f} of the bound", flush=True)
+    assert bad <= 1.0

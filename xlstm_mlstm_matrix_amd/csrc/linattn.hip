@@ -736,7 +736,10 @@ __global__ __launch_bounds__(256) void linattn_scan_kernel(KArgs a) {
     const int bt = (x >> 6) % NCT, at = (x >> 6) / NCT % NAT, wave = x / (64 * NCT * NAT);
     const int row = 32 * (at >> 1) + 8 * g4 + 4 * (at & 1);
     const int col = tile * BV + wave * 16 * NCT + (NCT == 2 ? 8 : 4) * (l16 >> 2) + (l16 & 3) + 4 * bt;
-    const float f = __builtin_amdgcn_exp2f(decay_log2(a.g[h]) * (float)a.seg_len);
+    // e^{g seg_len} in two parts: a rounded factor just below 1, applied once a
+    // segment, would pull the state 1.5e-5 off over 511 of them
+    const double fd = exp2((double)decay_log2(a.g[h]) * (double)a.seg_len);
+    const float f = (float)fd, fl = (float)(fd - (double)f);
     f32x4 run = {0, 0, 0, 0};
     if (job.X0)
 #pragma unroll
@@ -758,7 +761,7 @@ __global__ __launch_bounds__(256) void linattn_scan_kernel(KArgs a) {
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j)
             if (i + j < count) {
-                run = run * f + own[j];
+                run = run * f + (run * fl + own[j]);
                 *(f32x4 *)(s + (size_t)(i + j + 1) * step) = run;
             }
     }
