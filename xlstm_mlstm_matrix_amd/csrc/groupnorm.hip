@@ -17,6 +17,15 @@
 // positions to two numbers for each channel, gn_combine_kernel joins those
 // into the group's statistics (or the backward's two means), and
 // gn_apply_kernel writes the result.  Every sum has a fixed order.
+//
+// A mean is formed in two steps: the sum over n, then that plus the mean of the
+// distances from it (in the pass that sums their squares).  So it is good to its
+// last bit: a constant group has exactly its value as its mean and its bias as its
+// result.  (A sum of n equal floats is rounded: divided by n it can be a step off,
+// which 1 / sqrt(eps) turns into 0.3 for a row of 48 times 12345.678.)  bfloat16
+// groups held in registers, and bfloat16 blocks of positions, take the first step
+// only: sums of up to 2^16 equal values of 8 bits are exact, and the second costs
+// rows of 16 x 128 (SiLU) 5%: 26.7 -> 28 us, and float32 ones 47.3 -> 49 us.
 #include "ops.hpp"
 
 namespace mlstm {
@@ -120,6 +129,13 @@ __device__ __forceinline__ void load_w(const float *p, size_t at, bool ok, float
     }
 }
 
+// Variance from the mean square distance from a point `off` below the mean.
+// off is a few roundings of the mean's first step, so nothing cancels.
+__device__ __forceinline__ float variance(float sq, float off) {
+    const float v = sq - off * off;
+    return v < 0.0f ? 0.0f : v;  // NaN stays
+}
+
 // ---- over tokens, D <= 64 V K: lanes of a row
 //
 // A wavefront is cut into subgroups of `lpr` lanes, each holding one group's D
@@ -134,11 +150,12 @@ struct RowGeom {
 };
 
 template <typename IO, int V, int K, int ACT, bool BWD>
-__global__ __launch_bounds__(256) void gn_row_kernel(GnArgs a, RowGeom q, int first) {
+__global__ __launch_bounds__(256) void gn_row_kernel(GnArgs a, RowGeom q, int block0) {
+    constexpr bool TWO = sizeof(IO) == 4;  // steps of a mean
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lpr = 1 << q.lpr, sub = lane >> q.lpr, ln = lane & (lpr - 1);
     const int rpi = 64 >> (q.lpr + q.gp);  // positions side by side in a wavefront
-    const int block = first + blockIdx.x, gb = block % q.gblk, rb = block / q.gblk;
+    const int block = block0 + blockIdx.x, gb = block % q.gblk, rb = block / q.gblk;
     const int g = (gb << q.gp) + (sub & ((1 << q.gp) - 1)), rsub = sub >> q.gp;
     const int D = a.D, nrow = a.N * a.S;
     const IO *x = (const IO *)a.x + g * a.sx.s2;
@@ -182,16 +199,23 @@ __global__ __launch_bounds__(256) void gn_row_kernel(GnArgs a, RowGeom q, int fi
             for (int k = 0; k < K; ++k)
 #pragma unroll
                 for (int i = 0; i < V; ++i) t += v[k][i];
-            const float mu = lane_sum(t, lpr) / (float)D;  // divided: exact for a constant row
-            t = 0.0f;
+            const float m0 = lane_sum(t, lpr) / (float)D;
+            float t1 = 0.0f, t2 = 0.0f;
 #pragma unroll
             for (int k = 0; k < K; ++k)
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    const float c = v[k][i] - mu;
-                    t += ok[k] ? c * c : 0.0f;
+                    const float c = v[k][i] - m0;
+                    if constexpr (TWO) t1 += ok[k] ? c : 0.0f;
+                    t2 += ok[k] ? c * c : 0.0f;
                 }
-            const float rs = rsqrtf(lane_sum(t, lpr) * inv + a.eps);
+            float mu = m0, var = lane_sum(t2, lpr) * inv;
+            if constexpr (TWO) {
+                const float off = lane_sum(t1, lpr) * inv;
+                mu += off;
+                var = variance(var, off);
+            }
+            const float rs = rsqrtf(var + a.eps);
             if (a.mean && rok && ln == 0) {
                 a.mean[si] = mu;
                 a.rstd[si] = rs;
@@ -257,7 +281,22 @@ __global__ __launch_bounds__(256) void gn_row_kernel(GnArgs a, RowGeom q, int fi
     }
 }
 
-// Sum over a workgroup of up to 1024 threads, in every thread; red [16]
+// Sums over a workgroup of up to 1024 threads, in every thread; red [32] for two
+__device__ __forceinline__ void gn_block_sum2(float &x, float &y, float *red) {
+    x = lane_sum(x, 64);
+    y = lane_sum(y, 64);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) {
+        red[threadIdx.x >> 6] = x;
+        red[16 + (threadIdx.x >> 6)] = y;
+    }
+    __syncthreads();
+    x = y = 0.0f;
+    for (int i = 0; i < (int)blockDim.x >> 6; ++i) {
+        x += red[i];
+        y += red[16 + i];
+    }
+}
 __device__ __forceinline__ float gn_block_sum(float v, float *red) {
     v = lane_sum(v, 64);
     __syncthreads();
@@ -273,7 +312,7 @@ __device__ __forceinline__ float gn_block_sum(float v, float *red) {
 // come from gn_channel_kernel.
 template <typename IO, int V, int ACT, bool BWD>
 __global__ __launch_bounds__(256) void gn_long_row_kernel(GnArgs a, long long rows) {
-    __shared__ float red[16];
+    __shared__ float red[32];
     const float inv = 1.0f / (float)a.D;
     for (long long r = blockIdx.x; r < rows; r += gridDim.x) {
         const int g = (int)(r % a.G), ns = (int)(r / a.G);
@@ -282,7 +321,7 @@ __global__ __launch_bounds__(256) void gn_long_row_kernel(GnArgs a, long long ro
         const IO *dy = BWD ? (const IO *)a.dy + n * a.sdy.s0 + p * a.sdy.s1 + g * a.sdy.s2 : nullptr;
         IO *y = (IO *)a.y + n * a.sy.s0 + p * a.sy.s1 + g * a.sy.s2;
         const float *w = a.w ? a.w + (size_t)g * a.D : nullptr, *b = a.b ? a.b + (size_t)g * a.D : nullptr;
-        float mu, rs, s0 = 0.0f, s1 = 0.0f;
+        float mu, rs, s0 = 0.0f, s1 = 0.0f, s2 = 0.0f;
         float v[V], u[V];
         if constexpr (!BWD) {
             for (int d = threadIdx.x * V; d < a.D; d += 256 * V) {
@@ -290,13 +329,18 @@ __global__ __launch_bounds__(256) void gn_long_row_kernel(GnArgs a, long long ro
 #pragma unroll
                 for (int i = 0; i < V; ++i) s0 += v[i];
             }
-            mu = gn_block_sum(s0, red) / (float)a.D;
+            const float m0 = gn_block_sum(s0, red) / (float)a.D;
             for (int d = threadIdx.x * V; d < a.D; d += 256 * V) {
                 load_v<IO, V>(x + d, v);
 #pragma unroll
-                for (int i = 0; i < V; ++i) s1 += (v[i] - mu) * (v[i] - mu);
+                for (int i = 0; i < V; ++i) {
+                    s1 += v[i] - m0;
+                    s2 += (v[i] - m0) * (v[i] - m0);
+                }
             }
-            rs = rsqrtf(gn_block_sum(s1, red) * inv + a.eps);
+            gn_block_sum2(s1, s2, red);
+            mu = m0 + s1 * inv;
+            rs = rsqrtf(variance(s2 * inv, s1 * inv) + a.eps);
             if (a.mean && threadIdx.x == 0) {
                 a.mean[r] = mu;
                 a.rstd[r] = rs;
@@ -338,12 +382,12 @@ __global__ __launch_bounds__(256) void gn_long_row_kernel(GnArgs a, long long ro
 // ---- over sequences, groups of up to 16384 values: a workgroup holds a
 // group in registers (NE values a thread), one launch instead of three.
 template <typename IO, int V, int NE, int ACT>
-__global__ __launch_bounds__(1024) void gn_group_kernel(GnArgs a, int first) {
+__global__ __launch_bounds__(1024) void gn_group_kernel(GnArgs a, int block0) {
     constexpr int NV = NE / V;
-    __shared__ float red[16];
+    __shared__ float red[32];
     // neighbouring groups, which share cache lines, on one XCD (workgroups go round the 8)
     const int nwg = gridDim.x, xq = nwg >> 3, xr = nwg & 7, xcd = blockIdx.x & 7;
-    const int id = first + xcd * xq + min(xcd, xr) + (blockIdx.x >> 3);
+    const int id = block0 + xcd * xq + min(xcd, xr) + (blockIdx.x >> 3);
     const int g = id % a.G, n = id / a.G;
     const int rv = a.D / V, total = a.S * rv;  // vectors of a position, of the group
     const IO *x = (const IO *)a.x + n * a.sx.s0 + g * a.sx.s2;
@@ -364,16 +408,24 @@ __global__ __launch_bounds__(1024) void gn_group_kernel(GnArgs a, int first) {
 #pragma unroll
         for (int j = 0; j < V; ++j) t += v[i][j];
     const float inv = 1.0f / ((float)a.S * (float)a.D);
-    const float mu = gn_block_sum(t, red) / ((float)a.S * (float)a.D);
-    t = 0.0f;
+    const float m0 = gn_block_sum(t, red) / ((float)a.S * (float)a.D);
+    float t1 = 0.0f, t2 = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const float c = v[i][j] - mu;
-            t += (int)(threadIdx.x + i * blockDim.x) < total ? c * c : 0.0f;
+            const float c = (int)(threadIdx.x + i * blockDim.x) < total ? v[i][j] - m0 : 0.0f;
+            t1 += c;
+            t2 += c * c;
         }
-    const float rs = rsqrtf(gn_block_sum(t, red) * inv + a.eps);
+    if constexpr (sizeof(IO) == 4) {
+        gn_block_sum2(t1, t2, red);
+    } else {
+        t1 = 0.0f;
+        t2 = gn_block_sum(t2, red);
+    }
+    const float off = t1 * inv, mu = m0 + off;
+    const float rs = rsqrtf(variance(t2 * inv, off) + a.eps);
     if (a.mean && threadIdx.x == 0) {
         a.mean[id] = mu;
         a.rstd[id] = rs;
@@ -440,15 +492,36 @@ __device__ __forceinline__ void gn_reduce(float *red, float *t, int tx, int TX, 
         t[i] = red[tx];
     }
 }
+// ... of two sets of values at once; red [512]
+template <int V>
+__device__ __forceinline__ void gn_reduce2(float *red, float *t, float *u, int tx, int TX, int ty, int TY) {
+    float *red1 = red + 256;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        __syncthreads();
+        red[threadIdx.x] = t[i];
+        red1[threadIdx.x] = u[i];
+        __syncthreads();
+        for (int m = TY >> 1; m > 0; m >>= 1) {
+            if (ty < m) {
+                red[threadIdx.x] += red[threadIdx.x + m * TX];
+                red1[threadIdx.x] += red1[threadIdx.x + m * TX];
+            }
+            __syncthreads();
+        }
+        t[i] = red[tx];
+        u[i] = red1[tx];
+    }
+}
 
 // BWD false: mean and centred sum of squares of each channel of the block;
 // true: sum dz and sum dz xh.
 template <typename IO, int V, int ACT, bool BWD>
-__global__ __launch_bounds__(256) void gn_channel_kernel(GnArgs a, PosGeom q, int first) {
-    __shared__ float red[256];
+__global__ __launch_bounds__(256) void gn_channel_kernel(GnArgs a, PosGeom q, int block0) {
+    __shared__ float red[!BWD && sizeof(IO) == 4 ? 512 : 256];
     const int C = a.G * a.D;
     const int tx = threadIdx.x % q.tx, ty = threadIdx.x / q.tx, TY = 256 / q.tx;
-    const int block = first + blockIdx.x, cb = block % q.cblk;
+    const int block = block0 + blockIdx.x, cb = block % q.cblk;
     const int pb = block / q.cblk % q.pblk, o = block / q.cblk / q.pblk;
     const int c = (cb * q.tx + tx) * V;
     const bool ok = c < C;
@@ -500,21 +573,36 @@ __global__ __launch_bounds__(256) void gn_channel_kernel(GnArgs a, PosGeom q, in
     }
     if constexpr (BWD) {
         gn_reduce<V>(red, t[0], tx, q.tx, ty, TY);
+        gn_reduce<V>(red, t[1], tx, q.tx, ty, TY);
     } else {
-        // the rows' means joined, then their centred sums about that
-        float m[V];
+        // the rows' means joined, then their centred sums about that, and how far
+        // the rows' means still lie from it
+        float m[V], off[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) m[i] = cnt * t[0][i];
         gn_reduce<V>(red, m, tx, q.tx, ty, TY);
+        const float n = (float)(p1 - p0);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            m[i] /= (float)(p1 - p0);
+            m[i] /= n;
             const float d = t[0][i] - m[i];
+            off[i] = cnt * d;
             t[1][i] += cnt * d * d;
-            t[0][i] = m[i];
+        }
+        if constexpr (sizeof(IO) == 4) {
+            gn_reduce2<V>(red, t[1], off, tx, q.tx, ty, TY);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                off[i] /= n;
+                t[0][i] = m[i] + off[i];
+                t[1][i] = n * variance(t[1][i] / n, off[i]);
+            }
+        } else {
+            gn_reduce<V>(red, t[1], tx, q.tx, ty, TY);
+#pragma unroll
+            for (int i = 0; i < V; ++i) t[0][i] = m[i];
         }
     }
-    gn_reduce<V>(red, t[1], tx, q.tx, ty, TY);
     if (ty == 0 && ok) {
         float *ws = a.ws + ((size_t)o * q.pblk + pb) * 2 * C + c;
 #pragma unroll
@@ -552,8 +640,8 @@ __device__ __forceinline__ void gn_wsum(const float *ws, float *dw, float *db, i
 }
 
 // dw, db: sums of the partials [rblk][2][C] in ws over rblk; blockIdx.y is 0 for dw.
-__global__ __launch_bounds__(1024) void gn_wsum_kernel(const float *ws, float *dw, float *db, int C, int rblk, int first) {
-    gn_wsum<64>(ws, dw, db, C, rblk, first + blockIdx.x, blockIdx.y);
+__global__ __launch_bounds__(1024) void gn_wsum_kernel(const float *ws, float *dw, float *db, int C, int rblk, int block0) {
+    gn_wsum<64>(ws, dw, db, C, rblk, block0 + blockIdx.x, blockIdx.y);
 }
 
 // One workgroup per (sample, group).  Forward: mean and rstd from the channels'
@@ -561,10 +649,10 @@ __global__ __launch_bounds__(1024) void gn_wsum_kernel(const float *ws, float *d
 // out0, out1 [N][G].  The workgroups past those sum dw and db.
 // Threads: tx channels x 1024 / tx blocks of positions.
 template <bool BWD>
-__global__ __launch_bounds__(1024) void gn_combine_kernel(GnArgs a, PosGeom q, float *out0, float *out1, int first) {
-    __shared__ float red[16];
+__global__ __launch_bounds__(1024) void gn_combine_kernel(GnArgs a, PosGeom q, float *out0, float *out1, int block0) {
+    __shared__ float red[32];
     const int C = a.G * a.D;
-    const int block = first + blockIdx.x;
+    const int block = block0 + blockIdx.x;
     if (BWD && block >= a.N * a.G) {
         const int i = block - a.N * a.G;
         gn_wsum<64>(a.ws, a.dw, a.db, C, a.N * q.pblk, i >> 1, i & 1);
@@ -576,7 +664,7 @@ __global__ __launch_bounds__(1024) void gn_combine_kernel(GnArgs a, PosGeom q, f
     const float *ws = a.ws + (size_t)o * q.pblk * 2 * C + (size_t)g * a.D;
     const float total = (float)a.D * (float)a.S;
     auto rows = [&](int pb) { return (float)(min(a.S, (pb + 1) * q.plen) - pb * q.plen); };
-    float s0 = 0.0f, s1 = 0.0f;
+    float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f;
     for (int d = tx; d < a.D; d += 1 << sh) {
         const float w = BWD && a.w ? a.w[g * a.D + d] : 1.0f;
 #pragma unroll 4
@@ -598,20 +686,27 @@ __global__ __launch_bounds__(1024) void gn_combine_kernel(GnArgs a, PosGeom q, f
                 const float *r = ws + (size_t)pb * 2 * C + d;
                 const float c = r[0] - m0;
                 s1 += r[C] + c * c * rows(pb);
+                s2 += c * rows(pb);
             }
-    }
-    const float m1 = gn_block_sum(s1, red) / total;
-    if (threadIdx.x == 0) {
-        out0[block] = m0;
-        out1[block] = BWD ? m1 : rsqrtf(m1 + a.eps);
+        gn_block_sum2(s1, s2, red);
+        if (threadIdx.x == 0) {
+            out0[block] = m0 + s2 / total;
+            out1[block] = rsqrtf(variance(s1 / total, s2 / total) + a.eps);
+        }
+    } else {
+        const float m1 = gn_block_sum(s1, red) / total;
+        if (threadIdx.x == 0) {
+            out0[block] = m0;
+            out1[block] = m1;
+        }
     }
 }
 
 template <typename IO, int V, int ACT, bool BWD>
-__global__ __launch_bounds__(256) void gn_apply_kernel(GnArgs a, PosGeom q, const float *in0, const float *in1, int first) {
+__global__ __launch_bounds__(256) void gn_apply_kernel(GnArgs a, PosGeom q, const float *in0, const float *in1, int block0) {
     const int C = a.G * a.D;
     const int tx = threadIdx.x % q.tx, ty = threadIdx.x / q.tx, TY = 256 / q.tx;
-    const int block = first + blockIdx.x, cb = block % q.cblk;
+    const int block = block0 + blockIdx.x, cb = block % q.cblk;
     const int pb = block / q.cblk % q.pblk, o = block / q.cblk / q.pblk;
     const int c = (cb * q.tx + tx) * V;
     if (c >= C) return;
