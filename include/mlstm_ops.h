@@ -128,7 +128,7 @@ mlstm_status_t mlstm_linattn_bwd(const void *q, const void *k, const void *v,
 typedef enum {
     MLSTM_ACT_NONE = 0,
     MLSTM_ACT_SILU = 1, /* z / (1 + e^-z) */
-    MLSTM_ACT_GELU = 2  /* z Phi(z), with the error function */
+    MLSTM_ACT_GELU = 2  /* z Phi(z), Phi the normal distribution function */
 } mlstm_act_t;
 
 /* What one mean and variance is taken over. */
@@ -153,6 +153,11 @@ typedef enum {
  * below 2^28 (MLSTM_ERR_SHAPE).
  * D and the strides being multiples of 16 bytes makes it faster, and is not
  * required.  y may not be x.
+ *
+ * Precision.  float32 throughout, results rounded once.  The activations keep
+ * relative precision over their whole range: SiLU's and Phi's relative errors are
+ * below (8 + 1.5 |z|) 2^-24 and (16 + 1.3 z^2) 2^-24.  A group of one float32 value
+ * throughout has exactly that value as its mean.
  */
 mlstm_status_t mlstm_groupnorm_workspace_size(int N, int S, int G, int D, mlstm_norm_over_t over,
                                               mlstm_dtype_t io, int backward, size_t *bytes);
