@@ -11,7 +11,7 @@ namespace mlstm {
 
 namespace {
 
-constexpr long long kCacheBytes = 256ll << 20;  // Infinity Cache
+constexpr long long kStreamBytes = 320ll << 20;  // a quarter more than the Infinity Cache
 
 // 16 bytes of state, past the caches' replacement order when STREAM
 template <bool STREAM>
@@ -88,11 +88,15 @@ template <typename IO>
 hipError_t launch_t(const LinStepArgs &a, hipStream_t s) {
     const long long cells = (long long)a.B * a.H;
     const int quads = a.dv / 4;
-    // A state that the cache cannot hold is streamed past it (2 GB read and
-    // written: 386 us, 411 without; 1 GB of 128 x 128: 188 against 206); one that
-    // it holds is not (64 heads of 256 x 512: 12.7 us, streamed 38.7), nor are rows
-    // too short for it (1 GB of 64 x 64: 186 us, streamed 202).
-    if (cells * a.dk * a.dv * 8 > kCacheBytes) {
+    // States that the cache cannot hold from one step to the next are streamed past
+    // it.  What counts are the bytes touched, once in place and twice from one tensor
+    // into another.  In place, 256 x 512: 144 MB 46.8 us (streamed 72.1), 256 MB 94
+    // (97), 320 MB 129 (141), 384 MB 152 (152), 512 MB 209 (195), 2 GB 411 (386);
+    // 128 x 128: 224 MB 70 (85), 320 MB 124 (119), 512 MB 208 (189).  Into another
+    // tensor, states of 144 MB 53 (65), 160 MB 59 (66), 192 MB 80 (74).  Rows too
+    // short for it are not streamed (1 GB of 64 x 64: 186 us, streamed 202).
+    const bool once = !a.S_in || a.S_in == a.S_out;
+    if (cells * a.dk * a.dv * (once ? 4 : 8) > kStreamBytes) {
         if (quads >= 64) return launch_ct<IO, 64, true>(a, s);
         if (quads >= 32) return launch_ct<IO, 32, true>(a, s);
     }
