@@ -114,7 +114,10 @@ mlstm_status_t mlstm_linattn_step(const void *q, const void *k, const void *v,
  *  strides    7: of q, k, v, d_o, dq, dk, dv over (b, h, t), or NULL.  An input
  *             that repeats rows over b or h gets one gradient row for each
  *             (b, h): the caller sums them.
- * Everything else as for mlstm_linattn_fwd.
+ * Everything else as for mlstm_linattn_fwd, the precision too.  Without dS0 what
+ * is carried keeps 16 bits of each decayed product: a bfloat16 dv may differ in
+ * its last bit from that of a call with dS0, and so may dq and dk where d_qk and
+ * d_v are padded to the same width (64, 128, 256 or 512).
  */
 mlstm_status_t mlstm_linattn_bwd_workspace_size(int B, int H, int T, int d_qk, int d_v,
                                                 mlstm_dtype_t io, size_t *bytes);

@@ -524,7 +524,7 @@ def linattn_fwd(q, k, v, log_decay, S0=None, *, lengths=None, scale: float = 1.0
     [B,H,d_qk,d_v] float32; optional lengths [B] int32 of a padded batch: rows
     behind a sequence's length are not read, come out as zeros, and do not
     touch its state.  Returns o [B,H,T,d_v], or (o, S_T) with
-    ``return_state``.  Output buffers may be passed in (S_T may be S0; o may
+    ``return_state`` (a bfloat16 o may differ in its last bit without).  Output buffers may be passed in (S_T may be S0; o may
     be strided)."""
     import torch
     dev = _hip_device(q, "q")
@@ -594,7 +594,8 @@ def linattn_bwd(q, k, v, log_decay, do, S0=None, dS_T=None, *, lengths=None, sca
 
     Returns (dq, dk, dv) in the I/O dtype, each rounded once from float32 (zeros
     behind a sequence's length), and with ``state_grad`` also dS0 float32 (of
-    the zero state when S0 is None).  log_decay is a constant and gets none.
+    the zero state when S0 is None).  bfloat16 gradients may differ in their last
+    bit with and without ``state_grad``.  log_decay is a constant and gets none.
     Buffers for dq, dk and dv may be passed in, strided like the inputs."""
     import torch
     dev = _hip_device(q, "q")

@@ -31,17 +31,17 @@
 // 2^-16 where the output's own rounding is off by 2^-8.  One part of X adds to
 // the output as much as its rounding does (2.2e-3 root mean square instead of
 // 1.7e-3), and far more where the products cancel; it is 20% faster (64 heads of
-// 256 x 512 340 us instead of 422, 256 heads of 128 x 128 238 instead of 280).
+// 256 x 512 340 us instead of 418, 256 heads of 128 x 128 238 instead of 277).
 // w_j v_j enters the state in three parts (8 + 8 + 8 bits of its 24) where the
 // state is handed out: two parts would leave its float32 values 3e-6 off, three
 // leave what float32 sums do.  Where nobody sees the state but the read-out,
 // whose copy has 16 bits, two parts do.  X itself, every decay and every sum are
 // float32.  float32 I/O runs on the float32 MFMA without further rounding.
 //
-// Measured (bfloat16, 4096 tokens, state handed out): 256 heads of 128 x 128 280
-// us, 3.8 TB/s, where a large copy has 4.8; 64 heads of 256 x 512 422 us, 1.9
-// TB/s.  There 256 workgroups leave a SIMD one wavefront, whose vector
-// instructions, 192 of them MFMA a chunk, overlap little.
+// Measured (bfloat16, 4096 tokens, state handed out): 256 heads of 128 x 128 277
+// us, 3.9 TB/s, where a large copy has 4.8; 64 heads of 256 x 512 418 us, 2.0
+// TB/s.  There 256 workgroups leave a SIMD one wavefront, and its 879 vector
+// instructions a chunk, 192 of them MFMA, overlap little.
 #include "ops.hpp"
 
 namespace mlstm {
@@ -461,8 +461,8 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
     constexpr int NST = SO ? 0 : 2 * (ES == 4 ? NCT : 1);
     // w v among the read-out's products, where the registers allow it
     constexpr bool EARLY = !SO && C::EARLY;
-    // Copies in front of the read-out; among its steps for 512 rows only (4%
-    // faster there, up to 7% slower for fewer rows).
+    // Copies in front of the read-out; among its steps for 512 rows only (backward
+    // of 32 heads of 256 x 512 689 us instead of 715, no difference for fewer rows).
     constexpr bool SPREAD = !SO && NKS > 8;
     // Order of a chunk's work: each step's LDS reads are issued a step ahead of
     // the products that use them, and the elementwise work (w v, P, the
@@ -787,10 +787,10 @@ struct Plan {
 // often as 64 do; segments cost a second reading of K and V and the states'
 // way through memory; so: 128 if that gives a workgroup each, else 64 if that
 // does, else 128 and segments for two each (of at least four chunks).  Measured
-// (bfloat16, 4096 tokens): backward of 64 heads of 128 x 128 206 us with 64
-// columns, 220 with 128 and segments; of 32 heads of 256 x 512 580 against 676.
+// (bfloat16, 4096 tokens): backward of 64 heads of 128 x 128 238 us with 64
+// columns, 241 with 128 and segments; of 32 heads of 256 x 512 689 against 758.
 // Segments for two workgroups a unit against one: forward of 128 heads of
-// 64 x 64 86 us against 110, of 64 heads of 128 x 128 95 against 98.
+// 64 x 64 88 us against 113, of 64 heads of 128 x 128 101 against 106.
 Plan make_plan(int B, int H, int T, int dk, int dv, int io_bf16, int backward) {
     Plan p{};
     const int dims[3][2] = {{backward ? dv : dk, backward ? dk : dv}, {dk, dv}, {dv, dk}};
