@@ -30,7 +30,7 @@
 // read-out's copy of X goes in two parts (8 + 8 bits), and so does P, each off by
 // 2^-16 where the output's own rounding is off by 2^-8.  One part of X adds to
 // the output as much as its rounding does (2.2e-3 root mean square instead of
-// 1.7e-3), and far more where the products cancel; it is 20% faster (64 heads of
+// 1.7e-3), and far more where the products cancel; it is up to 19% faster (64 heads of
 // 256 x 512 340 us instead of 418, 256 heads of 128 x 128 238 instead of 277).
 // w_j v_j enters the state in three parts (8 + 8 + 8 bits of its 24) where the
 // state is handed out: two parts would leave its float32 values 3e-6 off, three
