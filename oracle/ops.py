@@ -1,6 +1,7 @@
-"""float64 oracle of linear attention with a decay for each head and of group
-norm with an activation, written token by token and row by row from the
-formulas (numpy; shares nothing with the HIP kernels).
+"""float64 oracle of linear attention with a decay for each head, of the gated
+delta rule, of group norm with an activation and of the norm and rotation of
+queries and keys, written token by token and row by row from the formulas (numpy;
+shares nothing with the HIP kernels).
 
 Linear attention, g = log decay of a head, s = scale:
 
@@ -55,6 +56,113 @@ def linattn_backward(q, k, v, g, do, S0=None, dS_T=None, lengths=None, scale=1.0
             gv[b, :, t] = np.einsum("hkv,hk->hv", D[b], k[b, :, t])
             D[b] = gam * D[b]
     return gq, gk, gv, D
+
+
+def _tokens(lengths, b, T):
+    return T if lengths is None else min(max(int(lengths[b]), 0), T)
+
+
+def deltarule_forward(q, k, v, g, beta, S0=None, lengths=None, scale=1.0):
+    """The gated delta rule: S_t = e^{g_t} (I - beta_t k_t k_t^T) S_{t-1} + beta_t k_t v_t^T,
+    o_t = s q_t^T S_t.  (o [B,H,T,dv], S_T [B,H,dk,dv]); q, k [B,Hk,T,dk]."""
+    q, k, v, g, beta = _np(q), _np(k), _np(v), _np(g), _np(beta)
+    B, H, T, dv = v.shape
+    q, k = (np.repeat(x, H // x.shape[1], 1) for x in (q, k))
+    dk = k.shape[-1]
+    o = np.zeros((B, H, T, dv))
+    S = np.zeros((B, H, dk, dv)) if S0 is None else _np(S0).copy()
+    eye = np.eye(dk)
+    for b in range(B):
+        for t in range(_tokens(lengths, b, T)):
+            kt, bt = k[b, :, t], beta[b, :, t, None, None]
+            S[b] = np.exp(g[b, :, t, None, None]) * ((eye - bt * kt[:, :, None] * kt[:, None, :]) @ S[b]) \
+                + bt * kt[:, :, None] * v[b, :, t, None, :]
+            o[b, :, t] = scale * (q[b, :, t, None, :] @ S[b])[:, 0]
+    return o, S
+
+
+def deltarule_backward(q, k, v, g, beta, do, S0=None, dS_T=None, lengths=None, scale=1.0):
+    """(dq, dk, dv, dg, dbeta, dS0) by the reverse mode of deltarule_forward, each
+    token's from the states before and behind it (all kept)."""
+    q, k, v, g, beta, do = _np(q), _np(k), _np(v), _np(g), _np(beta), _np(do)
+    B, H, T, dv = v.shape
+    Hk, dk = k.shape[1], k.shape[-1]
+    q, k = (np.repeat(x, H // Hk, 1) for x in (q, k))
+    gq, gk, gv = np.zeros_like(q), np.zeros_like(k), np.zeros_like(v)
+    gg, gb = np.zeros((B, H, T)), np.zeros((B, H, T))
+    D0 = np.zeros((B, H, dk, dv)) if dS_T is None else _np(dS_T).copy()
+    eye = np.eye(dk)
+    for b in range(B):
+        n = _tokens(lengths, b, T)
+        S = [np.zeros((H, dk, dv)) if S0 is None else _np(S0)[b]]
+        step = []
+        for t in range(n):
+            kt, bt = k[b, :, t], beta[b, :, t, None, None]
+            step.append(eye - bt * kt[:, :, None] * kt[:, None, :])
+            S.append(np.exp(g[b, :, t, None, None]) * (step[t] @ S[t]) + bt * kt[:, :, None] * v[b, :, t, None, :])
+        D = D0[b]
+        for t in range(n - 1, -1, -1):
+            kt, bt, vt = k[b, :, t], beta[b, :, t, None], v[b, :, t]
+            gam = np.exp(g[b, :, t, None, None])
+            gq[b, :, t] = scale * (S[t + 1] @ do[b, :, t, :, None])[..., 0]
+            D = D + scale * q[b, :, t, :, None] * do[b, :, t, None, :]
+            Dk, Sk = (D.transpose(0, 2, 1) @ kt[..., None])[..., 0], (S[t].transpose(0, 2, 1) @ kt[..., None])[..., 0]
+            # L = <D, e^g (S - beta k (k^T S)) + beta k v^T> of this token
+            gb[b, :, t] = (Dk * vt).sum(-1) - gam[:, 0, 0] * (Dk * Sk).sum(-1)
+            gv[b, :, t] = bt * Dk
+            gk[b, :, t] = bt * (D @ vt[..., None])[..., 0] \
+                - gam[:, 0] * bt * ((D @ Sk[..., None])[..., 0] + (S[t] @ Dk[..., None])[..., 0])
+            gg[b, :, t] = gam[:, 0, 0] * (D * (step[t] @ S[t])).sum((-1, -2))
+            D = gam * (step[t] @ D)
+        D0[b] = D
+    shared = lambda x: x.reshape(B, Hk, H // Hk, T, dk).sum(2)
+    return shared(gq), shared(gk), gv, gg, gb, D0
+
+
+def _qk_turn(x, angle, amp, layout, sign):
+    """Rows [B, heads, T, d] with the pairs of their first channels turned by sign * angle [B, T, n]."""
+    n = angle.shape[-1]
+    y = x.copy()
+    c, s = amp * np.cos(angle)[:, None], sign * amp * np.sin(angle)[:, None]
+    for i in range(n):
+        a, b = (i, i + n) if layout == "half" else (2 * i, 2 * i + 1)
+        y[..., a] = x[..., a] * c[..., i] - x[..., b] * s[..., i]
+        y[..., b] = x[..., b] * c[..., i] + x[..., a] * s[..., i]
+    return y
+
+
+def _qk_angle(x, inv_freq, positions):
+    B, T = x.shape[0], x.shape[2]
+    f = np.zeros(0) if inv_freq is None else _np(inv_freq)
+    p = np.broadcast_to(np.arange(T, dtype=np.float64), (B, T)) if positions is None else _np(positions)
+    return p[..., None] * f
+
+
+def _qk_scale(x, norm, eps):
+    if norm == "none":
+        return np.ones(x.shape[:-1] + (1,))
+    sq = (x * x).sum(-1, keepdims=True)
+    return 1.0 / np.sqrt((sq / x.shape[-1] if norm == "rms" else sq) + eps)
+
+
+def qknorm_forward(x, w=None, norm="rms", eps=1e-6, inv_freq=None, positions=None, layout="half", amp=1.0):
+    """Norm and rotation of the rows x [B,H,T,d]."""
+    x = _np(x)
+    z = x * _qk_scale(x, norm, eps) * (1.0 if w is None else _np(w))
+    return _qk_turn(z, _qk_angle(x, inv_freq, positions), amp, layout, 1.0)
+
+
+def qknorm_backward(x, dy, w=None, norm="rms", eps=1e-6, inv_freq=None, positions=None, layout="half", amp=1.0):
+    """(dx, dw)."""
+    x, dy = _np(x), _np(dy)
+    u = _qk_turn(dy, _qk_angle(x, inv_freq, positions), amp, layout, -1.0)
+    r = _qk_scale(x, norm, eps)
+    dw = (u * x * r).sum((0, 1, 2))
+    u = u * (1.0 if w is None else _np(w))
+    if norm == "none":
+        return u, dw
+    n = x.shape[-1] if norm == "rms" else 1
+    return r * u - r ** 3 * x * (u * x).sum(-1, keepdims=True) / n, dw
 
 
 _erf = np.vectorize(math.erf, otypes=[np.float64])

@@ -45,7 +45,8 @@ SIGNATURES = {
     "mlstm_slstm_fwd": (_i, [_vp] * 11 + [_i] * 5 + [_vp]),
 }
 # the same for include/mlstm_ops.h
-_f, _szp = ctypes.c_float, ctypes.POINTER(_sz)
+_f, _d, _szp = ctypes.c_float, ctypes.c_double, ctypes.POINTER(_sz)
+_floats = ctypes.POINTER(_f)
 OPS_SIGNATURES = {
     "mlstm_linattn_fwd_workspace_size": (_i, [_i] * 6 + [_szp]),
     "mlstm_linattn_fwd": (_i, [_vp] * 9 + [_f] + [_i] * 6 + [_vp, _sz, _vp]),
@@ -55,9 +56,21 @@ OPS_SIGNATURES = {
     "mlstm_groupnorm_workspace_size": (_i, [_i] * 7 + [_szp]),
     "mlstm_groupnorm_fwd": (_i, [_vp] * 7 + [_i] * 6 + [_f, _i, _vp, _sz, _vp]),
     "mlstm_groupnorm_bwd": (_i, [_vp] * 10 + [_i] * 7 + [_vp, _sz, _vp]),
+    "mlstm_deltarule_fwd_workspace_size": (_i, [_i] * 7 + [_szp]),
+    "mlstm_deltarule_fwd": (_i, [_vp] * 10 + [_f] + [_i] * 7 + [_vp, _sz, _vp]),
+    "mlstm_deltarule_step": (_i, [_vp] * 9 + [_f] + [_i] * 6 + [_vp]),
+    "mlstm_deltarule_bwd_workspace_size": (_i, [_i] * 7 + [_szp]),
+    "mlstm_deltarule_bwd": (_i, [_vp] * 16 + [_f] + [_i] * 7 + [_vp, _sz, _vp]),
+    "mlstm_qknorm_fwd": (_i, [_vp] * 9 + [_i] * 7 + [_f, _i, _f, _i, _vp]),
+    "mlstm_qknorm_bwd_workspace_size": (_i, [_i] * 5 + [_szp]),
+    "mlstm_qknorm_bwd": (_i, [_vp] * 13 + [_i] * 7 + [_f, _i, _f, _i, _vp, _sz, _vp]),
+    "mlstm_rope_frequencies": (_i, [_i, _d, _i, _d, _i, _d, _d, _floats, _floats]),
 }
 ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2}
 NORM_OVER = {"token": 0, "sequence": 1}
+QK_NORMS = {"none": 0, "rms": 1, "l2": 2}
+ROTARY_LAYOUTS = {"half": 0, "pairs": 1}
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "ramp": 3}
 
 
 class MlstmError(RuntimeError):
@@ -420,7 +433,7 @@ def step_noalloc(q, k, v, i_pre, f_pre, o_pre, C=None, n=None, m=None, *, h=None
 # ---- operators of include/mlstm_ops.h
 
 _NO_GUARD = contextlib.nullcontext()
-_LONGS = {n: ctypes.c_longlong * n for n in (6, 9, 12, 21)}
+_LONGS = {n: ctypes.c_longlong * n for n in (6, 9, 12, 18, 21, 33)}
 
 
 def _guard(device):
@@ -478,6 +491,34 @@ def _strides(*ts):
     for t in ts:
         flat += t.stride()[:-1] if t.dim() == 4 else (*t.stride()[:-1], 0)
     return _LONGS[len(flat)](*flat)
+
+
+def _gate_strides(gates, *ts):
+    """The same where the tensors at the places ``gates`` have a single value for each
+    (b, h, t) or (b, h): all their strides count."""
+    for t in ts:
+        if not t.is_contiguous():
+            break
+    else:
+        return None
+    flat = []
+    for i, t in enumerate(ts):
+        st = t.stride() if i in gates else t.stride()[:-1]
+        flat += st if len(st) == 3 else (*st, 0)
+    return _LONGS[len(flat)](*flat)
+
+
+def _strided(t, name, shape, dtype, device):
+    """Check a tensor of any strides."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
 
 
 def _hip_device(t, name):
@@ -625,6 +666,137 @@ def linattn_bwd(q, k, v, log_decay, do, S0=None, dS_T=None, *, lengths=None, sca
     return (dq, dk, dv, dS0) if state_grad else (dq, dk, dv)
 
 
+@functools.lru_cache(maxsize=4096)
+def deltarule_workspace_size(B, Hk, H, T, d_qk, d_v, io: int, backward: bool = False) -> int:
+    """Bytes of workspace of deltarule_fwd, or of deltarule_bwd."""
+    n = ctypes.c_size_t(0)
+    f = lib().mlstm_deltarule_bwd_workspace_size if backward else lib().mlstm_deltarule_fwd_workspace_size
+    _check(f(B, Hk, H, T, d_qk, d_v, io, ctypes.byref(n)))
+    return n.value
+
+
+def deltarule_fwd(q, k, v, log_decay, beta, S0=None, *, lengths=None, scale: float = 1.0,
+                  return_state: bool = True, o=None, S_T=None, workspace=None):
+    """The gated delta rule over whole sequences:
+    S_t = e^{g_t} (I - beta_t k_t k_t^T) S_{t-1} + beta_t k_t v_t^T, o_t = scale * q_t^T S_t.
+
+    q, k [B,Hk,T,d_qk], v [B,H,T,d_v] (float32 or bfloat16, one dtype; strided as
+    in linattn_fwd); H is a multiple of Hk, and H / Hk heads of v in a row share
+    one of q and k.  log_decay (g <= 0, -inf allowed) and beta [B,H,T] float32,
+    any strides; optional S0 [B,H,d_qk,d_v] float32; optional lengths [B] int32 of
+    a padded batch, as in linattn_fwd.  The recurrence is stable for 0 <= beta |k|^2
+    <= 2 (keys of unit length: qknorm_fwd).  Returns o [B,H,T,d_v], or (o, S_T)
+    with ``return_state`` (a bfloat16 o may differ in its last bit without).
+    Output buffers may be passed in (S_T may be S0; o may be strided)."""
+    import torch
+    dev = _hip_device(q, "q")
+    io = _io(q)
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k, v must be [B, H, T, d]")
+    B, Hk, T, dk = q.shape
+    H, dv = v.shape[1], v.shape[-1]
+    _view(q, "q", (B, Hk, T, dk), q.dtype, dev)
+    _view(k, "k", (B, Hk, T, dk), q.dtype, dev)
+    _view(v, "v", (B, H, T, dv), q.dtype, dev)
+    _strided(log_decay, "log_decay", (B, H, T), torch.float32, dev)
+    _strided(beta, "beta", (B, H, T), torch.float32, dev)
+    _dense(S0, "S0", (B, H, dk, dv), torch.float32, dev)
+    _dense(lengths, "lengths", (B,), torch.int32, dev)
+    with _guard(dev):
+        if o is None:
+            o = torch.empty((B, H, T, dv), dtype=q.dtype, device=dev)
+        if return_state and S_T is None:
+            S_T = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
+        _view(o, "o", (B, H, T, dv), q.dtype, dev)
+        _dense(S_T, "S_T", (B, H, dk, dv), torch.float32, dev)
+        wp, wn, _keep = _workspace(workspace, deltarule_workspace_size(B, Hk, H, T, dk, dv, io), dev)
+        _check(lib().mlstm_deltarule_fwd(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(beta), _ptr(S0), _ptr(lengths), _ptr(o),
+            _ptr(S_T), _gate_strides((3, 4), q, k, v, log_decay, beta, o), scale, B, Hk, H, T, dk, dv, io,
+            wp, wn, _raw_stream(dev)))
+    return (o, S_T) if return_state else o
+
+
+def deltarule_step(q, k, v, log_decay, beta, S=None, *, scale: float = 1.0, o=None, S_out=None,
+                   inplace: bool = True):
+    """One token of the gated delta rule for B*H heads.
+
+    q, k [B,Hk,d_qk], v [B,H,d_v], log_decay, beta [B,H] (strided as in
+    deltarule_fwd), state S [B,H,d_qk,d_v] float32 or None for the zero state.
+    With ``inplace`` (default), a state and no ``S_out``, the state tensor is
+    updated in place.  Returns (o, S_out)."""
+    import torch
+    dev = _hip_device(q, "q")
+    io = _io(q)
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k, v must be [B, H, d]")
+    B, Hk, dk = q.shape
+    H, dv = v.shape[1], v.shape[-1]
+    _view(q, "q", (B, Hk, dk), q.dtype, dev)
+    _view(k, "k", (B, Hk, dk), q.dtype, dev)
+    _view(v, "v", (B, H, dv), q.dtype, dev)
+    _strided(log_decay, "log_decay", (B, H), torch.float32, dev)
+    _strided(beta, "beta", (B, H), torch.float32, dev)
+    _dense(S, "S", (B, H, dk, dv), torch.float32, dev)
+    with _guard(dev):
+        if o is None:
+            o = torch.empty((B, H, dv), dtype=q.dtype, device=dev)
+        if S_out is None:
+            S_out = S if inplace and S is not None else \
+                torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
+        _view(o, "o", (B, H, dv), q.dtype, dev)
+        _dense(S_out, "S_out", (B, H, dk, dv), torch.float32, dev)
+        _check(lib().mlstm_deltarule_step(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(beta), _ptr(S), _ptr(o), _ptr(S_out),
+            _gate_strides((3, 4), q, k, v, log_decay, beta, o), scale, B, Hk, H, dk, dv, io, _raw_stream(dev)))
+    return o, S_out
+
+
+def deltarule_bwd(q, k, v, log_decay, beta, do, S0=None, dS_T=None, *, lengths=None, scale: float = 1.0,
+                  state_grad: bool = False, dq=None, dk=None, dv=None, dlog_decay=None, dbeta=None,
+                  workspace=None):
+    """Gradients of a loss L for the inputs of deltarule_fwd, given dL/do [B,H,T,d_v]
+    and, where the final state was used, dL/dS_T.
+
+    Returns (dq, dk, dv, dlog_decay, dbeta): the first three in the I/O dtype, each
+    rounded once (dq and dk [B,Hk,T,d_qk], summed over the heads that share them),
+    the other two float32 [B,H,T]; zeros behind a sequence's length.  With
+    ``state_grad`` also dS0 float32 (of the zero state when S0 is None).  Buffers
+    for the first five may be passed in, strided like the inputs."""
+    import torch
+    dev = _hip_device(q, "q")
+    io = _io(q)
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k, v must be [B, H, T, d]")
+    B, Hk, T, d_qk = q.shape
+    H, d_v = v.shape[1], v.shape[-1]
+    nk, nv, ng, ns = (B, Hk, T, d_qk), (B, H, T, d_v), (B, H, T), (B, H, d_qk, d_v)
+    for name, t, shape in (("q", q, nk), ("k", k, nk), ("v", v, nv), ("do", do, nv)):
+        _view(t, name, shape, q.dtype, dev)
+    _strided(log_decay, "log_decay", ng, torch.float32, dev)
+    _strided(beta, "beta", ng, torch.float32, dev)
+    _dense(S0, "S0", ns, torch.float32, dev)
+    _dense(dS_T, "dS_T", ns, torch.float32, dev)
+    _dense(lengths, "lengths", (B,), torch.int32, dev)
+    with _guard(dev):
+        new = lambda t, shape, dt: torch.empty(shape, dtype=dt, device=dev) if t is None else t
+        dq, dk, dv = new(dq, nk, q.dtype), new(dk, nk, q.dtype), new(dv, nv, q.dtype)
+        dlog_decay, dbeta = new(dlog_decay, ng, torch.float32), new(dbeta, ng, torch.float32)
+        for name, t, shape in (("dq", dq, nk), ("dk", dk, nk), ("dv", dv, nv)):
+            _view(t, name, shape, q.dtype, dev)
+        _strided(dlog_decay, "dlog_decay", ng, torch.float32, dev)
+        _strided(dbeta, "dbeta", ng, torch.float32, dev)
+        dS0 = torch.empty(ns, dtype=torch.float32, device=dev) if state_grad else None
+        wp, wn, _keep = _workspace(workspace, deltarule_workspace_size(B, Hk, H, T, d_qk, d_v, io, True), dev)
+        _check(lib().mlstm_deltarule_bwd(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(beta), _ptr(S0), _ptr(lengths), _ptr(do),
+            _ptr(dS_T), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dlog_decay), _ptr(dbeta), _ptr(dS0),
+            _gate_strides((3, 4, 9, 10), q, k, v, log_decay, beta, do, dq, dk, dv, dlog_decay, dbeta), scale,
+            B, Hk, H, T, d_qk, d_v, io, wp, wn, _raw_stream(dev)))
+    out = (dq, dk, dv, dlog_decay, dbeta)
+    return out + (dS0,) if state_grad else out
+
+
 def _choice(table, key, name):
     if key not in table:
         raise ValueError(f"{name} must be one of {sorted(table)}, got {key!r}")
@@ -712,3 +884,118 @@ def groupnorm_bwd(x, dy, mean, rstd, weight=None, bias=None, *, act: str = "none
             _ptr(x), _ptr(dy), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(bias), _ptr(dx), _ptr(dw), _ptr(db),
             _strides(x, dy, dx), N, S, G, D, ov, ac, io, wp, wn, _raw_stream(dev)))
     return dx, dw, db
+
+
+def rope_frequencies(n_freq: int, base: float = 10000.0, *, scaling: str = "plain", factor: float = 1.0,
+                     context: int = 4096, fast: float = 32.0, slow: float = 1.0, device=None):
+    """The table of rotations a position (radians, float32 [n_freq]) that qknorm_fwd
+    takes as inv_freq, and the amplitude that goes with it: base^(-i / n_freq),
+    scaled for contexts ``factor`` times the trained one.
+
+    scaling "plain"; "linear" (every frequency divided by the factor); "base" (a
+    larger base: the slowest divided by the factor, the fastest kept); "ramp" (those
+    of ``fast`` turns or more over the trained ``context`` kept, those of ``slow`` turns or
+    fewer divided, a ramp between; amplitude 0.1 ln(factor) + 1)."""
+    import torch
+    table, amp = (_f * max(int(n_freq), 1))(), _f()
+    _check(lib().mlstm_rope_frequencies(n_freq, base, _choice(ROPE_SCALINGS, scaling, "scaling"), factor, context,
+                                        fast, slow, table, ctypes.byref(amp)))
+    return torch.tensor(list(table), dtype=torch.float32, device=device), amp.value
+
+
+def _qk_checks(q, k, others, inv_freq, positions, weights, dev):
+    """Shapes of a qknorm call: (B, H, Hk, T, d, n_freq)."""
+    import torch
+    B, H, T, d = q.shape
+    Hk = 0 if k is None else k.shape[1]
+    for name, t, h in (("q", q, H), ("k", k, Hk)) + others:
+        if k is not None or h != Hk:
+            _view(t, name, (B, h, T, d), q.dtype, dev)
+        elif t is not None:
+            raise ValueError(f"{name} without k")
+    for name, w in weights:
+        _dense(w, name, (d,), torch.float32, dev)
+    n = 0
+    if inv_freq is not None:
+        if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+            raise TypeError("inv_freq must be a torch tensor of one dimension")
+        n = inv_freq.shape[0]
+        _dense(inv_freq, "inv_freq", (n,), torch.float32, dev)
+    _dense(positions, "positions", (B, T), torch.int32, dev)
+    return B, H, Hk, T, d, n
+
+
+def qknorm_fwd(q, k=None, q_weight=None, k_weight=None, *, norm: str = "rms", eps: float = 1e-6, inv_freq=None,
+               positions=None, layout: str = "half", amplitude: float = 1.0, yq=None, yk=None):
+    """Norm of each head's queries and keys, and their rotation by the token's
+    position, in one pass.
+
+    q [B,H,T,d], k [B,Hk,T,d] or None (float32 or bfloat16; any strides, the last
+    dimension contiguous, d <= 512).  Each row is divided by its root mean square
+    (``norm="rms"``), its length ("l2") or nothing ("none"), and scaled by q_weight, k_weight
+    [d] float32 or None.  With inv_freq [n] float32 (rope_frequencies) the first 2 n
+    channels are then rotated by positions[b,t] * inv_freq (int32 [B,T]; 0 ... T-1 when
+    None) in n pairs: channels i and i + n (``layout="half"``) or 2 i and 2 i + 1
+    ("pairs"), times ``amplitude``.  Returns (yq, yk), yq alone without k; buffers may be
+    passed in, strided, and yq may be q itself and yk k."""
+    import torch
+    dev = _hip_device(q, "q")
+    io = _io(q)
+    nm, ly = _choice(QK_NORMS, norm, "norm"), _choice(ROTARY_LAYOUTS, layout, "layout")
+    if q.dim() != 4 or (k is not None and (not isinstance(k, torch.Tensor) or k.dim() != 4)):
+        raise ValueError("q and k must be [B, H, T, d]")
+    with _guard(dev):
+        if yq is None:
+            yq = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        if yk is None and k is not None:
+            yk = torch.empty(k.shape, dtype=q.dtype, device=dev)
+        B, H, Hk, T, d, n = _qk_checks(q, k, (("yq", yq, q.shape[1]), ("yk", yk, 0 if k is None else k.shape[1])),
+                                       inv_freq, positions, (("q_weight", q_weight), ("k_weight", k_weight)), dev)
+        kk, yy = (q, yq) if k is None else (k, yk)
+        _check(lib().mlstm_qknorm_fwd(
+            _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), _ptr(positions), _ptr(yq), _ptr(yk),
+            _strides(q, kk, yq, yy), B, H, Hk, T, d, n, ly, amplitude, nm, eps, io, _raw_stream(dev)))
+    return yq if k is None else (yq, yk)
+
+
+@functools.lru_cache(maxsize=4096)
+def qknorm_bwd_workspace_size(B, H, Hk, T, d) -> int:
+    """Bytes of workspace of qknorm_bwd with weight gradients (Hk = 0: queries alone)."""
+    n = ctypes.c_size_t(0)
+    _check(lib().mlstm_qknorm_bwd_workspace_size(B, H, Hk, T, d, ctypes.byref(n)))
+    return n.value
+
+
+def qknorm_bwd(q, k, dyq, dyk, q_weight=None, k_weight=None, *, norm: str = "rms", eps: float = 1e-6,
+               inv_freq=None, positions=None, layout: str = "half", amplitude: float = 1.0,
+               weight_grad: bool = True, dq=None, dk=None, workspace=None):
+    """Gradients of qknorm_fwd, given its q and k (before the norm) and dyq and dyk.
+
+    Returns (dq, dk, dq_weight, dk_weight), the first two in the I/O dtype, the others
+    [d] float32 (None without ``weight_grad``; k, dyk None: dk and dk_weight are None).
+    Buffers dq and dk may be passed in, strided; they may be dyq and dyk themselves."""
+    import torch
+    dev = _hip_device(q, "q")
+    io = _io(q)
+    nm, ly = _choice(QK_NORMS, norm, "norm"), _choice(ROTARY_LAYOUTS, layout, "layout")
+    if q.dim() != 4 or (k is not None and (not isinstance(k, torch.Tensor) or k.dim() != 4)):
+        raise ValueError("q and k must be [B, H, T, d]")
+    with _guard(dev):
+        if dq is None:
+            dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        if dk is None and k is not None:
+            dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
+        h = 0 if k is None else k.shape[1]
+        B, H, Hk, T, d, n = _qk_checks(q, k, (("dyq", dyq, q.shape[1]), ("dyk", dyk, h), ("dq", dq, q.shape[1]),
+                                              ("dk", dk, h)), inv_freq, positions,
+                                       (("q_weight", q_weight), ("k_weight", k_weight)), dev)
+        dwq = torch.empty(d, dtype=torch.float32, device=dev) if weight_grad else None
+        dwk = torch.empty(d, dtype=torch.float32, device=dev) if weight_grad and k is not None else None
+        wp, wn, _keep = _workspace(workspace, qknorm_bwd_workspace_size(B, H, Hk, T, d) if weight_grad else 0, dev)
+        other = (q, dyq, dq) if k is None else (k, dyk, dk)
+        _check(lib().mlstm_qknorm_bwd(
+            _ptr(q), _ptr(k), _ptr(dyq), _ptr(dyk), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq),
+            _ptr(positions), _ptr(dq), _ptr(dk), _ptr(dwq), _ptr(dwk),
+            _strides(q, other[0], dyq, other[1], dq, other[2]), B, H, Hk, T, d, n, ly, amplitude, nm, eps, io,
+            wp, wn, _raw_stream(dev)))
+    return dq, dk, dwq, dwk

@@ -21,7 +21,8 @@ LIB = os.path.join(PKG, "libmlstm.so")
 OBJDIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["api.cpp", "step.hip", "prefill.hip", "backward.hip", "layer.hip", "slstm.hip",
-           "ops_api.cpp", "linattn.hip", "linattn_step.hip", "groupnorm.hip"]
+           "ops_api.cpp", "linattn.hip", "linattn_step.hip", "groupnorm.hip",
+           "deltarule.hip", "deltarule_step.hip", "qknorm.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 FLAGS = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Werror", "-Wno-unused-command-line-argument",

@@ -1,5 +1,6 @@
 // ops.hpp -- internal types of the operators of include/mlstm_ops.h (linear
-// attention with a decay for each head, group norm with an activation).
+// attention with a decay for each head, the gated delta rule, group norm with an
+// activation, norm and rotation of queries and keys).
 #pragma once
 
 #include "common.hpp"
@@ -51,6 +52,58 @@ struct LinStepArgs {
     int B, H, dk, dv;
 };
 hipError_t launch_linattn_step(const LinStepArgs &a, int io_bf16, hipStream_t s);
+
+// The gated delta rule; the members of the second half are the backward's.
+struct DeltaArgs {
+    const void *q, *k, *v;      // [B, Hk, T, dk] x2, [B, H, T, dv]
+    const float *g, *beta;      // [B, H, T]
+    const float *S0;
+    const int *lengths;
+    void *o;
+    float *S_T;
+    Strides sq, sk, sv, sg, sb, so;
+    float scale;
+    int B, Hk, H, T, dk, dv;
+    float *ws;
+    const void *d_o;
+    const float *dS_T;
+    void *dq, *dkk, *dvv;
+    float *dg, *db, *dS0;
+    Strides sdo, sdq, sdk, sdv, sdg, sdb;
+};
+// 0 when the workspace would not fit the limit
+size_t deltarule_workspace_floats(int B, int Hk, int H, int T, int dk, int dv, int io_bf16, int backward);
+hipError_t launch_deltarule_fwd(const DeltaArgs &a, int io_bf16, hipStream_t s);
+hipError_t launch_deltarule_bwd(const DeltaArgs &a, int io_bf16, hipStream_t s);
+
+struct DeltaStepArgs {
+    const void *q, *k, *v;
+    const float *g, *beta, *S_in;
+    void *o;
+    float *S_out;
+    Strides sq, sk, sv, sg, sb, so;  // over (b, h)
+    float scale;
+    int B, Hk, H, dk, dv;
+};
+hipError_t launch_deltarule_step(const DeltaStepArgs &a, int io_bf16, hipStream_t s);
+
+// Norm and rotation of queries (tensor 0) and keys (tensor 1; H[1] = 0 without).
+struct QkArgs {
+    const void *x[2], *dy[2];   // dy: backward
+    void *y[2];                 // y, or dx in the backward
+    const float *w[2];
+    float *dw[2];
+    Strides sx[2], sdy[2], sy[2];
+    const float *freq;
+    const int *pos;
+    int B, T, H[2], d, nf;
+    int pairs;                  // neighbouring channels make a pair
+    int norm;                   // mlstm_qknorm_t
+    float amp, eps;
+    float *ws;
+};
+size_t qknorm_workspace_floats(int B, int H, int Hk, int T, int d);
+hipError_t launch_qknorm(const QkArgs &a, int io_bf16, hipStream_t s);
 
 struct GnArgs {
     const void *x, *dy;         // [N, S, G, D]; dy NULL in the forward

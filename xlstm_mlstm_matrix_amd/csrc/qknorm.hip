@@ -1,0 +1,302 @@
+// qknorm.hip -- norm of each head's queries and keys and their rotation by the
+// token's position, forward and backward.
+//
+// A row x of d channels: r = 1 / sqrt(mean x^2 + eps) (or of the sum, or 1),
+// z = w x r, and channels a, b of each pair turned by the angle position * freq:
+// y = A (z_a c - z_b s, z_b c + z_a s).  Backward, with u the row dy turned back:
+// dw = sum over rows of u x r, dx = r (u w) - x r^3 (sum u w x) / n.
+//
+// Each row is read once and written once, nothing else is large: the pass is
+// bound by HBM.  A row belongs to a few lanes of a wavefront; a lane holds both
+// channels of its pairs, so that rotating costs no exchange, and the row's sums are
+// the only thing that crosses lanes.  The heads of a token are walked by the
+// same lanes, which keep the token's sines and cosines in registers.
+#include "ops.hpp"
+
+namespace mlstm {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxBlocks = 1024;  // of a backward: rows of partial weight gradients
+
+struct QkPlan {
+    int lpr;        // lanes of a row, a power of two
+    int units, rot_units;
+    int per;        // heads that a group of lanes walks for one token
+    int nblk_heads; // groups of heads
+    long long items;
+    int blocks;
+};
+
+template <typename IO, int V>
+__device__ __forceinline__ void load_row(const IO *p, bool ok, float *x) {
+    if constexpr (V == 1) {
+        x[0] = ok ? to_f(*p) : 0.0f;
+    } else {
+        typedef IO vec __attribute__((ext_vector_type(V)));
+        vec v = {};
+        if (ok) v = *(const vec *)p;
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[j] = to_f((IO)v[j]);
+    }
+}
+template <typename IO, int V>
+__device__ __forceinline__ void store_row(IO *p, bool ok, const float *x) {
+    if (!ok) return;
+    if constexpr (V == 1) {
+        *p = from_f<IO>(x[0]);
+    } else {
+        typedef IO vec __attribute__((ext_vector_type(V)));
+        vec v;
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = from_f<IO>(x[j]);
+        *(vec *)p = v;
+    }
+}
+
+// Cosine and sine of position * freq.  The angle is a double product, good to
+// 2^-52 of itself, and only its distance from a whole turn goes on in float32.
+__device__ __forceinline__ void turn(int pos, float freq, float amp, float &c, float &s) {
+    const double t = (double)pos * (double)freq * 0.15915494309189533577;  // 1 / (2 pi)
+    const float half = (float)(2.0 * (t - rint(t)));
+    sincospif(half, &s, &c);
+    c *= amp;
+    s *= amp;
+}
+
+// V channels of a vector, UPL units (two vectors) of a row for each lane.
+template <typename IO, int V, int UPL, bool PAIRS, bool BWD>
+__global__ __launch_bounds__(kThreads) void qk_kernel(QkArgs a, QkPlan p) {
+    constexpr int W = 2 * V;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int sub = lane & (p.lpr - 1);
+    const int d = a.d, nf = a.nf;
+    int off[UPL][2];
+    bool ok[UPL][2], rot[UPL];
+#pragma unroll
+    for (int i = 0; i < UPL; ++i) {
+        const int u = sub + i * p.lpr;
+        rot[i] = u < p.rot_units;
+        if (rot[i]) {
+            off[i][0] = PAIRS ? u * W : u * V;
+            off[i][1] = PAIRS ? u * W + V : nf + u * V;
+        } else {
+            off[i][0] = 2 * nf + (u - p.rot_units) * W;
+            off[i][1] = off[i][0] + V;
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) ok[i][k] = u < p.units && off[i][k] < d;
+    }
+    // the pair (ia(j), ib(j)) of a unit's W channels
+    const auto ia = [](int j) { return PAIRS ? 2 * j : j; };
+    const auto ib = [](int j) { return PAIRS ? 2 * j + 1 : V + j; };
+    float dw[2][UPL][W];
+    if constexpr (BWD) {
+#pragma unroll
+        for (int i = 0; i < UPL; ++i)
+#pragma unroll
+            for (int j = 0; j < W; ++j) dw[0][i][j] = dw[1][i][j] = 0.0f;
+    }
+    const float count = a.norm == 1 ? (float)d : 1.0f;
+    const int groups = kThreads / p.lpr;  // of lanes in a workgroup
+    for (long long item = (long long)blockIdx.x * groups + threadIdx.x / p.lpr; item < p.items;
+         item += (long long)gridDim.x * groups) {
+        const int n = (int)(item / p.nblk_heads), hb = (int)(item % p.nblk_heads);
+        const int b = n / a.T, t = n % a.T;
+        float c[UPL][V], s[UPL][V];
+#pragma unroll
+        for (int i = 0; i < UPL; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) c[i][j] = 1.0f, s[i][j] = 0.0f;
+        if (nf > 0) {
+            const int pos = a.pos ? a.pos[n] : t;
+#pragma unroll
+            for (int i = 0; i < UPL; ++i)
+                if (rot[i])
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        turn(pos, a.freq[(sub + i * p.lpr) * V + j], a.amp, c[i][j], s[i][j]);
+        }
+        const int h0 = hb * p.per, h1 = min(h0 + p.per, a.H[0] + a.H[1]);
+#pragma unroll
+        for (int ti = 0; ti < 2; ++ti) {
+            const int first = ti == 0 ? h0 : max(h0 - a.H[0], 0);
+            const int last = ti == 0 ? min(h1, a.H[0]) : h1 - a.H[0];
+            if (first >= last) continue;
+            float w[UPL][W];
+#pragma unroll
+            for (int i = 0; i < UPL; ++i)
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    const int k = j / V;
+                    w[i][j] = a.w[ti] && ok[i][k] ? a.w[ti][off[i][k] + j % V] : 1.0f;
+                }
+            const IO *xr = (const IO *)a.x[ti] + b * a.sx[ti].s0 + t * a.sx[ti].s2;
+            const IO *gr = BWD ? (const IO *)a.dy[ti] + b * a.sdy[ti].s0 + t * a.sdy[ti].s2 : nullptr;
+            IO *yr = (IO *)a.y[ti] + b * a.sy[ti].s0 + t * a.sy[ti].s2;
+            for (int h = first; h < last; ++h) {
+                float x[UPL][W], g[UPL][W];
+                float ss = 0.0f, dot = 0.0f;
+#pragma unroll
+                for (int i = 0; i < UPL; ++i)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        load_row<IO, V>(xr + h * a.sx[ti].s1 + off[i][k], ok[i][k], x[i] + k * V);
+                        if constexpr (BWD) load_row<IO, V>(gr + h * a.sdy[ti].s1 + off[i][k], ok[i][k], g[i] + k * V);
+                    }
+                if constexpr (BWD) {
+#pragma unroll
+                    for (int i = 0; i < UPL; ++i)
+#pragma unroll
+                        for (int j = 0; j < V; ++j) {
+                            const float ya = g[i][ia(j)], yb = g[i][ib(j)];
+                            g[i][ia(j)] = c[i][j] * ya + s[i][j] * yb;
+                            g[i][ib(j)] = c[i][j] * yb - s[i][j] * ya;
+                        }
+                }
+#pragma unroll
+                for (int i = 0; i < UPL; ++i)
+#pragma unroll
+                    for (int j = 0; j < W; ++j) {
+                        ss += x[i][j] * x[i][j];
+                        if constexpr (BWD) dot += g[i][j] * w[i][j] * x[i][j];
+                    }
+                float r = 1.0f;
+                if (a.norm != 0) {
+                    for (int m = p.lpr >> 1; m > 0; m >>= 1) {
+                        ss += __shfl_xor(ss, m);
+                        if constexpr (BWD) dot += __shfl_xor(dot, m);
+                    }
+                    r = 1.0f / sqrtf(ss / count + a.eps);
+                }
+                const float back = BWD && a.norm != 0 ? r * r * r * (dot / count) : 0.0f;
+#pragma unroll
+                for (int i = 0; i < UPL; ++i) {
+                    if constexpr (BWD) {
+#pragma unroll
+                        for (int j = 0; j < W; ++j) {
+                            dw[ti][i][j] += g[i][j] * (x[i][j] * r);
+                            x[i][j] = r * (g[i][j] * w[i][j]) - x[i][j] * back;
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < W; ++j) x[i][j] = x[i][j] * r * w[i][j];
+#pragma unroll
+                        for (int j = 0; j < V; ++j) {
+                            const float za = x[i][ia(j)], zb = x[i][ib(j)];
+                            x[i][ia(j)] = za * c[i][j] - zb * s[i][j];
+                            x[i][ib(j)] = zb * c[i][j] + za * s[i][j];
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        store_row<IO, V>(yr + h * a.sy[ti].s1 + off[i][k], ok[i][k], x[i] + k * V);
+                }
+            }
+        }
+    }
+    if constexpr (BWD) {
+        if (!a.dw[0] && !a.dw[1]) return;
+        // rows of the workgroup together: its wavefronts in turn, in a fixed order
+        __shared__ float sum[4][512];
+#pragma unroll
+        for (int ti = 0; ti < 2; ++ti) {
+            if (!a.dw[ti]) continue;
+#pragma unroll
+            for (int i = 0; i < UPL; ++i)
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    float x = dw[ti][i][j];
+                    for (int m = p.lpr; m < 64; m <<= 1) x += __shfl_xor(x, m);
+                    if (lane < p.lpr && ok[i][j / V]) sum[wave][off[i][j / V] + j % V] = x;
+                }
+            __syncthreads();
+            for (int ch = threadIdx.x; ch < d; ch += kThreads)
+                a.ws[((size_t)ti * gridDim.x + blockIdx.x) * d + ch] =
+                    (sum[0][ch] + sum[1][ch]) + (sum[2][ch] + sum[3][ch]);
+            __syncthreads();
+        }
+    }
+}
+
+// partial weight gradients [tensor][block][d] -> dw: 16 channels a workgroup, 16
+// threads a channel
+__global__ __launch_bounds__(kThreads) void qk_weight_kernel(QkArgs a, int blocks) {
+    __shared__ float sum[16][17];
+    const int ti = blockIdx.y, ch = blockIdx.x * 16 + (threadIdx.x & 15), part = threadIdx.x >> 4;
+    if (!a.dw[ti]) return;
+    float x = 0.0f;
+    if (ch < a.d)
+        for (int r = part; r < blocks; r += 16) x += a.ws[((size_t)ti * blocks + r) * a.d + ch];
+    sum[part][threadIdx.x & 15] = x;
+    __syncthreads();
+    if (part == 0 && ch < a.d) {
+#pragma unroll
+        for (int m = 1; m < 16; ++m) x += sum[m][threadIdx.x & 15];
+        a.dw[ti][ch] = x;
+    }
+}
+
+int pow2_at_least(int x) {
+    int p = 1;
+    while (p < x) p <<= 1;
+    return p;
+}
+
+template <typename IO, int V, int UPL, bool BWD>
+hipError_t launch_v(const QkArgs &a, hipStream_t s) {
+    QkPlan p{};
+    p.rot_units = a.nf / V;
+    p.units = p.rot_units + (a.d - 2 * a.nf + 2 * V - 1) / (2 * V);
+    p.lpr = pow2_at_least((p.units + UPL - 1) / UPL);
+    const int heads = a.H[0] + a.H[1];
+    const long long tokens = (long long)a.B * a.T;
+    // all heads of a token to one group of lanes where the tokens fill the card
+    // (8 wavefronts a SIMD), else as many groups as that takes
+    const long long groups = 8ll * 1024 * 64 / p.lpr;
+    const long long split = tokens >= groups ? 1 : (groups + tokens - 1) / tokens;
+    p.per = (int)(split >= heads ? 1 : (heads + split - 1) / split);
+    p.nblk_heads = (heads + p.per - 1) / p.per;
+    p.items = tokens * p.nblk_heads;
+    const long long blocks = (p.items * p.lpr + kThreads - 1) / kThreads;
+    p.blocks = (int)(BWD && blocks > kMaxBlocks ? kMaxBlocks : blocks);
+    if (a.pairs)
+        qk_kernel<IO, V, UPL, true, BWD><<<dim3((unsigned)p.blocks), kThreads, 0, s>>>(a, p);
+    else
+        qk_kernel<IO, V, UPL, false, BWD><<<dim3((unsigned)p.blocks), kThreads, 0, s>>>(a, p);
+    if (BWD && (a.dw[0] || a.dw[1]))
+        qk_weight_kernel<<<dim3((unsigned)((a.d + 15) / 16), 2), kThreads, 0, s>>>(a, p.blocks);
+    return hipGetLastError();
+}
+
+template <typename IO, bool BWD>
+hipError_t launch_io(const QkArgs &a, hipStream_t s) {
+    constexpr int V = 16 / (int)sizeof(IO);
+    // whole vectors: pairs and the rest begin and end on 16 bytes, and so do all rows
+    bool vec = a.d % V == 0 && a.nf % V == 0;
+    for (int i = 0; i < 2; ++i) {
+        if (a.H[i] == 0) continue;
+        const void *ptr[3] = {a.x[i], a.y[i], BWD ? a.dy[i] : nullptr};
+        const Strides *st[3] = {&a.sx[i], &a.sy[i], &a.sdy[i]};
+        for (int j = 0; j < (BWD ? 3 : 2); ++j)
+            vec = vec && (uintptr_t)ptr[j] % 16 == 0 && st[j]->s0 % V == 0 && st[j]->s1 % V == 0 && st[j]->s2 % V == 0;
+    }
+    if (vec) return launch_v<IO, V, 1, BWD>(a, s);
+    return launch_v<IO, 1, 4, BWD>(a, s);
+}
+
+}  // namespace
+
+size_t qknorm_workspace_floats(int B, int H, int Hk, int T, int d) {
+    // a workgroup holds at least one (token, head) item
+    const long long rows = (long long)B * T * (H + Hk);
+    return (size_t)2 * (size_t)(rows < kMaxBlocks ? rows : kMaxBlocks) * d;
+}
+
+hipError_t launch_qknorm(const QkArgs &a, int io_bf16, hipStream_t s) {
+    if (a.dy[0]) return io_bf16 ? launch_io<bf16, true>(a, s) : launch_io<float, true>(a, s);
+    return io_bf16 ? launch_io<bf16, false>(a, s) : launch_io<float, false>(a, s);
+}
+
+}  // namespace mlstm
