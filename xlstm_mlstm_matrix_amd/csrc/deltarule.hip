@@ -35,16 +35,27 @@ namespace mlstm {
 
 namespace {
 
+// ---- the three walks over a sequence's chunks
+
+enum Walk {
+    FORWARD,  // o and the final state
+    STATES,   // the backward's first: X of every token, the state at every block's start
+    BACK      // dU and the state's gradient, from the last chunk to the first
+};
+
 // ---- records: what a chunk knows without the state
 
 // Operand fragments: tile t holds rows 16 t + l16, slot e of lane group g4 is
-// token 16 (e / 4) + 4 g4 + e % 4.  Then float vectors over the tokens: e^{G_i},
-// e^{G_L - G_i}, beta_i.
-template <typename IO>
+// token 16 (e / 4) + 4 g4 + e % 4.  An inverse (FORWARD: beta T', STATES: T', BACK: T^T with
+// T = (I + beta N)^-1), scores (FORWARD: P, BACK: P^T), then float vectors over the
+// tokens: e^{G_i}, e^{G_L - G_i}, beta_i.
+template <typename IO, Walk W>
 struct Rec {
     typedef typename Types<IO>::Frag Frag;
-    static constexpr int TP = sizeof(IO) == 2 ? 3 : 1, PP = sizeof(IO) == 2 ? 2 : 1;  // parts of T' and P
-    static constexpr int FRAG = 64 * (int)sizeof(Frag);                              // bytes of a tile's part
+    static constexpr bool BF = sizeof(IO) == 2;
+    static constexpr int TP = !BF ? 1 : W == STATES ? 2 : 3;                    // parts of the inverse
+    static constexpr int PP = W == STATES ? 0 : !BF ? 1 : W == FORWARD ? 2 : 3;  // parts of the scores
+    static constexpr int FRAG = 64 * (int)sizeof(Frag);                         // bytes of a tile's part
     static constexpr int P = 2 * TP * FRAG, VEC = P + 2 * PP * FRAG, EG = 0, REST = 1, BETA = 2;
     static constexpr int BYTES = (VEC + 3 * L * 4 + 1023) / 1024 * 1024;
 };
@@ -94,22 +105,25 @@ constexpr int kPrepWaves = 4, kLd = 36;  // wavefronts of a workgroup, row of a 
 // One wavefront a chunk.  The inverse goes by blocks of 16 x 16: those on the diagonal
 // row by row (a lane a column), which no cancellation hurts where keys are alike,
 // then T'_21 = -T'_22 (N beta)_21 T'_11 on the float32 MFMA.
-template <typename IO>
-__global__ __launch_bounds__(64 * kPrepWaves) void prep_kernel(DeltaArgs a, char *rec, long long total) {
-    using R = Rec<IO>;
+template <typename IO, bool BWD>
+__global__ __launch_bounds__(64 * kPrepWaves) void prep_kernel(DeltaArgs a, char *rec, char *rec_back, long long total) {
+    using R = Rec<IO, BWD ? STATES : FORWARD>;
+    using RB = Rec<IO, BACK>;
     using Frag = typename Types<IO>::Frag;
-    __shared__ __attribute__((aligned(16))) float mats[kPrepWaves][2][L * kLd];
+    __shared__ __attribute__((aligned(16))) float mats[kPrepWaves][BWD ? 3 : 2][L * kLd];
     __shared__ __attribute__((aligned(16))) float vecs[kPrepWaves][3][L];
     const int lane = threadIdx.x & 63, l16 = lane & 15, g4 = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    float *A = mats[wave][0], *X = mats[wave][1], *hi = vecs[wave][0], *lo = vecs[wave][1], *be = vecs[wave][2];
+    // N, T', T; the scores go where T' will be
+    float *A = mats[wave][0], *X = mats[wave][1], *Xb = mats[wave][BWD ? 2 : 1];
+    float *hi = vecs[wave][0], *lo = vecs[wave][1], *be = vecs[wave][2];
     const long long ci = (long long)blockIdx.x * kPrepWaves + wave;
     const long long nch = chunks(a.T);
     const long long cell = ci < total ? ci / nch : 0, c = ci < total ? ci % nch : 0;
     const int b = (int)(cell / a.H), h = (int)(cell % a.H), hk = h / (a.H / a.Hk);
     const long long s = c * L;
     const int nc = ci < total ? (int)max(0ll, min((long long)L, tokens(a, b) - s)) : 0;
-    char *out = rec + ci * R::BYTES;
+    char *out = rec + ci * R::BYTES, *outb = BWD ? rec_back + ci * RB::BYTES : nullptr;
 
     // ---- gates: lane = token (twice over)
     const int tok = lane & 31;
@@ -131,12 +145,12 @@ __global__ __launch_bounds__(64 * kPrepWaves) void prep_kernel(DeltaArgs a, char
             hi[tok] = (float)top;
             lo[tok] = (float)(G - top);
             be[tok] = beta;
-            if (nc > 0) {
-                float *v = (float *)(out + R::VEC);
-                v[R::EG * L + tok] = __builtin_amdgcn_exp2f((float)G);
-                v[R::REST * L + tok] = __builtin_amdgcn_exp2f((float)(GL - G));
-                v[R::BETA * L + tok] = beta;
-            }
+        }
+        float *v = (float *)(lane < L ? out + R::VEC : outb + RB::VEC);
+        if (nc > 0 && (lane < L || BWD)) {
+            v[R::EG * L + tok] = __builtin_amdgcn_exp2f((float)G);
+            v[R::REST * L + tok] = __builtin_amdgcn_exp2f((float)(GL - G));
+            v[R::BETA * L + tok] = beta;
         }
     }
     // ---- scores: lane column j = l16 (+ 16), rows i = 4 g4 + r (+ 16)
@@ -175,73 +189,109 @@ __global__ __launch_bounds__(64 * kPrepWaves) void prep_kernel(DeltaArgs a, char
 #pragma unroll
     for (int r = 0; r < 4; ++r) A[(4 * g4 + r) * kLd + 16 + l16] = X[(4 * g4 + r) * kLd + 16 + l16] = 0.0f;
     __syncthreads();
-    // two rows' slots of a matrix in LDS
+    // the slots of row 16 t + l16 of a matrix in LDS, or of its transpose
     const auto slots = [&](const float *m, int t, float *x) {
         const f32x4 u = *(const f32x4 *)(m + (16 * t + l16) * kLd + 4 * g4);
         const f32x4 v = *(const f32x4 *)(m + (16 * t + l16) * kLd + 16 + 4 * g4);
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] = u[e], x[4 + e] = v[e];
     };
+    const auto columns = [&](const float *m, int t, float *x) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = m[(16 * (e >> 2) + 4 * g4 + (e & 3)) * kLd + 16 * t + l16];
+    };
+    const auto put = [&](char *to, int t, const float *x, auto parts_c) {
+        constexpr int PARTS = decltype(parts_c)::value;
+        Frag f[PARTS];
+        split8<PARTS>(x, f);
+        if (nc > 0)
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p) *(Frag *)(to + (t * PARTS + p) * R::FRAG + lane * sizeof(Frag)) = f[p];
+    };
+    using TPc = std::integral_constant<int, R::TP>;
+    using PPc = std::integral_constant<int, BWD ? RB::PP : R::PP>;
+    using TBc = std::integral_constant<int, RB::TP>;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         float x[8];
-        Frag f[R::PP];
-        slots(X, t, x);
-        split8<R::PP>(x, f);
-        if (nc > 0)
-#pragma unroll
-            for (int p = 0; p < R::PP; ++p) *(Frag *)(out + R::P + (t * R::PP + p) * R::FRAG + lane * sizeof(Frag)) = f[p];
+        if constexpr (BWD)
+            columns(X, t, x);
+        else
+            slots(X, t, x);
+        put(BWD ? outb + RB::P : out + R::P, t, x, PPc{});
     }
     __syncthreads();
-    // ---- the inverse
-    if (lane < L) {
-        const int o = 16 * (lane >> 4);  // block on the diagonal; column l16 of it
+    // ---- the inverses: of I + N beta by the first half of the wavefront, of I + beta N
+    // by the second
+    if (lane < L || BWD) {
+        const int o = lane & 16;  // block on the diagonal; column l16 of it
+        const bool second = lane >= L;
+        float *to = second ? Xb : X;
         float x[16], y[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
+            const float bi = be[o + i];
             float sum = 0.0f;
 #pragma unroll
             for (int m = 0; m < i; ++m) sum += A[(o + i) * kLd + o + m] * y[m];
-            x[i] = (i == l16 ? 1.0f : 0.0f) - sum;
-            y[i] = x[i] * be[o + i];
-            X[(o + i) * kLd + o + l16] = x[i];
+            x[i] = (i == l16 ? 1.0f : 0.0f) - (second ? sum * bi : sum);
+            y[i] = second ? x[i] : x[i] * bi;
+            to[(o + i) * kLd + o + l16] = x[i];
         }
     }
     __syncthreads();
-    {
+#pragma unroll
+    for (int w = 0; w < (BWD ? 2 : 1); ++w) {
+        float *M = w ? Xb : X;
+        const float bi = be[16 + l16];
         f32x4 Y = {}, Z = {};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            Y = __builtin_amdgcn_mfma_f32_16x16x4f32(A[(16 + l16) * kLd + 4 * g4 + e] * be[4 * g4 + e],
-                                                     X[(4 * g4 + e) * kLd + l16], Y, 0, 0, 0);
+            Y = __builtin_amdgcn_mfma_f32_16x16x4f32(A[(16 + l16) * kLd + 4 * g4 + e] * (w ? bi : be[4 * g4 + e]),
+                                                     M[(4 * g4 + e) * kLd + l16], Y, 0, 0, 0);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            Z = __builtin_amdgcn_mfma_f32_16x16x4f32(X[(16 + l16) * kLd + 16 + 4 * g4 + e], Y[e], Z, 0, 0, 0);
+            Z = __builtin_amdgcn_mfma_f32_16x16x4f32(M[(16 + l16) * kLd + 16 + 4 * g4 + e], Y[e], Z, 0, 0, 0);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            X[(16 + 4 * g4 + r) * kLd + l16] = -Z[r];
-            X[(4 * g4 + r) * kLd + 16 + l16] = 0.0f;
+            M[(16 + 4 * g4 + r) * kLd + l16] = -Z[r];
+            M[(4 * g4 + r) * kLd + 16 + l16] = 0.0f;
         }
     }
     __syncthreads();
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         float x[8];
-        Frag f[R::TP];
         slots(X, t, x);
-        const float bi = be[16 * t + l16];
+        if constexpr (!BWD) {
+            const float bi = be[16 * t + l16];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= bi;
-        split8<R::TP>(x, f);
-        if (nc > 0)
-#pragma unroll
-            for (int p = 0; p < R::TP; ++p) *(Frag *)(out + (t * R::TP + p) * R::FRAG + lane * sizeof(Frag)) = f[p];
+            for (int e = 0; e < 8; ++e) x[e] *= bi;
+        }
+        put(out, t, x, TPc{});
+        if constexpr (BWD) {
+            columns(Xb, t, x);
+            put(outb, t, x, TBc{});
+        }
     }
 }
 
 // ---- the walk over the chunks
 
-template <typename IO, int DKP_, int NCT_, int NW_>
+// Tokens between the states that the backward keeps, each a block of its last kernel.
+template <typename IO>
+constexpr int kBlock = sizeof(IO) == 2 ? 64 : 32;
+
+// What the walks of the backward write: X or dU of every token, float32
+// [cell][T][dv], and the state (its gradient) at each block's start (end) as operand
+// fragments [cell][block][32 columns][16 rows][part]: slot e of lane group g4 is column
+// 8 g4 + e, lane l16 of tile 2 kk + u row 32 kk + 8 (l16 / 4) + 4 u + l16 % 4.
+struct WalkOut {
+    float *rows;
+    char *states;
+};
+
+template <typename IO, int DKP_, int NCT_, int NW_, Walk W>
 struct Cfg {
     static constexpr int DKP = DKP_, NCT = NCT_, NW = NW_, NTH = 64 * NW_;
     static constexpr int BV = 16 * NCT * NW;               // value columns of a workgroup
@@ -250,8 +300,9 @@ struct Cfg {
     static constexpr int QG = DKP / EPG, VG = 16 * NCT / EPG, WG = BV / EPG;  // granules of a row
     // float32: V in one buffer a wavefront, whose columns are its own
     static constexpr bool VOWN = sizeof(IO) == 4;
-    static constexpr int TROW = 2 * DKP + (VOWN ? 0 : BV);  // elements of a tile for each token
-    static constexpr int REC = Rec<IO>::BYTES / (int)sizeof(IO);  // elements of a record
+    static constexpr int KOFF = W == STATES ? 0 : DKP;      // Q (none in STATES), K, V
+    static constexpr int TROW = KOFF + DKP + (VOWN ? 0 : BV);  // elements of a tile for each token
+    static constexpr int REC = Rec<IO, W>::BYTES / (int)sizeof(IO);  // elements of a record
     static constexpr size_t TILE = ((size_t)L * TROW + REC) * sizeof(IO), VTILE = VOWN ? (size_t)L * BV * sizeof(IO) : 0;
     static constexpr int NBUF = 2 * TILE + VTILE <= kLds ? 2 : 1;
     static constexpr int PER_CU = 2 * (NBUF * TILE + VTILE) <= kLds && NW == 4 ? 2 : 1;  // workgroups of a compute unit
@@ -269,11 +320,15 @@ __device__ __forceinline__ f32x4 mfma_parts(const Frag *x, const Frag *y, f32x4 
     return acc;
 }
 
-// SP: parts of what leads to the state
-template <typename IO, int DKP, int NCT, int NW, int SP>
-__global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) void delta_kernel(DeltaArgs a, const char *rec) {
-    using C = Cfg<IO, DKP, NCT, NW>;
-    using R = Rec<IO>;
+// SP: parts of what leads to the state.  BACK is called with do, dS_T and dS0 in the
+// places of v, S0 and S_T:
+//   dU = T^T (P^T do + e^{G_L - G} o (K D)),  dV = beta o dU,
+//   D <- e^{G_L} D + Q^T (scale e^G o do) - K^T (e^G o dV).
+template <typename IO, int DKP, int NCT, int NW, int SP, Walk W>
+__global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW, W>::PER_CU * NW / 4)) void delta_kernel(DeltaArgs a, const char *rec,
+                                                                                                WalkOut to) {
+    using C = Cfg<IO, DKP, NCT, NW, W>;
+    using R = Rec<IO, W>;
     using Frag = typename Types<IO>::Frag;
     constexpr int NAT = C::NAT, NKS = C::NKS, QG = C::QG, VG = C::VG, BV = C::BV, NBUF = C::NBUF;
     constexpr int OP = Types<IO>::XPARTS;  // parts of what leads to the output
@@ -295,13 +350,13 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
     const IO *qg = (const IO *)a.q + b * a.sq.s0 + hk * a.sq.s1;
     const IO *kg = (const IO *)a.k + b * a.sk.s0 + hk * a.sk.s1;
     const IO *vg = (const IO *)a.v + b * a.sv.s0 + h * a.sv.s1 + col0;
-    IO *og = (IO *)a.o + b * a.so.s0 + h * a.so.s1 + col0;
+    IO *og = W == FORWARD ? (IO *)a.o + b * a.so.s0 + h * a.so.s1 + col0 : nullptr;
     const char *rg = rec + (long long)bh * chunks(a.T) * R::BYTES;
 
     // ---- state.  Lane (l16, g4) of tile (at, bt) holds rows krow(at) + r of column vcol + 4 bt
-    const int vq = NCT == 2 ? 8 : 4;
-    const int vc0 = wave * 16 * NCT;
-    const int vcol = vc0 + vq * (l16 >> 2) + (l16 & 3);
+    // A wavefront of 16 columns has every other quad of 32 that it shares with its neighbour.
+    const int vc0 = NCT == 2 ? wave * 32 : 32 * (wave >> 1) + 4 * (wave & 1);
+    const int vcol = vc0 + 8 * (l16 >> 2) + (l16 & 3);
     auto krow = [&](int at) { return 32 * (at >> 1) + 8 * g4 + 4 * (at & 1); };
     f32x4 X[NAT][NCT];
     const size_t cell = (size_t)bh * dk * dv;
@@ -329,7 +384,9 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
     // ---- chunks.  Rows past a chunk's tokens are out of their descriptor's range:
     // they read as zero and are not written.
     const int nch = (n + L - 1) / L;
-    auto count = [&](int c) -> int { return max(0, min(L, n - c * L)); };
+    const int ncb = (dv + 31) >> 5;  // blocks of 32 columns
+    const long long nblk = (chunks(a.T) * L + kBlock<IO> - 1) / kBlock<IO>;
+    auto count = [&](int c) -> int { return c < 0 ? 0 : max(0, min(L, n - c * L)); };
     auto copy_offsets = [&](unsigned *off, int ld, int ncol, auto gpr_c) {
         constexpr int GPR = decltype(gpr_c)::value, RPI = C::NTH / GPR;
         static_assert(L * GPR % C::NTH == 0, "whole instructions");
@@ -354,20 +411,20 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
     using WGc = std::integral_constant<int, C::WG>;
     constexpr int QPER = 16 * QG > C::NTH ? 16 * QG / C::NTH : 1, WPER = 16 * C::WG > C::NTH ? 16 * C::WG / C::NTH : 1;
     unsigned qoff[QPER], koff[QPER], voff[WPER], ownoff = kOut;
-    copy_offsets(qoff, ldq, dk, QGc{});
+    if constexpr (W != STATES) copy_offsets(qoff, ldq, dk, QGc{});
     copy_offsets(koff, ldk, dk, QGc{});
     constexpr int VI = L * VG / 64;  // own tile: 64 / VG rows an instruction
     if constexpr (C::VOWN) {
-        const int col = vc0 + lane % VG * C::EPG;
+        const int col = NCT == 2 ? vc0 + lane % VG * 4 : vc0 + lane % VG * 8;
         ownoff = col0 + col < dv ? (unsigned)((lane / VG * ldv + col) * ES) : kOut;
     } else {
         copy_offsets(voff, ldv, dv - col0, WGc{});
     }
     constexpr int NREC = R::BYTES / 1024;
     auto load = [&](IO *t, int c) {
-        copy(t, qg, ldq, qoff, QGc{}, c);
-        copy(t + L * DKP, kg, ldk, koff, QGc{}, c);
-        if constexpr (!C::VOWN) copy(t + 2 * L * DKP, vg, ldv, voff, WGc{}, c);
+        if constexpr (W != STATES) copy(t, qg, ldq, qoff, QGc{}, c);
+        copy(t + L * C::KOFF, kg, ldk, koff, QGc{}, c);
+        if constexpr (!C::VOWN) copy(t + L * (C::KOFF + DKP), vg, ldv, voff, WGc{}, c);
         const int bytes = count(c) > 0 ? R::BYTES : 0;
         const auto rs = __builtin_amdgcn_make_buffer_rsrc((void *)(rg + (long long)c * R::BYTES), 0,
                                                           __builtin_amdgcn_readfirstlane(bytes), kBuf);
@@ -393,31 +450,37 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
     Cols<QG> cols;
     rows.init((const IO *)nullptr, l16, g4);
     cols.init((const IO *)nullptr, l16, g4);
-    // this lane's outputs: tokens l16 and 16 + l16, columns vc0 + vq g4 + (0 .. 4 NCT - 1)
-    const int ocol = vc0 + vq * g4;
+    // this lane's outputs: tokens l16 and 16 + l16, columns vc0 + 8 g4 + (0 .. 4 NCT - 1)
+    const int ocol = vc0 + 8 * g4;
     const bool ook = col0 + ocol < dv;
-    constexpr int NST = 2 * (ES == 4 ? NCT : 1);  // stores of a chunk, issued after the next one's copies
-    auto body = [&](IO *cur, IO *next, int c) {
+    // memory operations of a chunk issued after the next one's copies, 15 of them at most
+    constexpr int NST = W == FORWARD ? 2 * (ES == 4 ? NCT : 1) : 8 * NCT < 15 ? 8 * NCT : 15;
+    constexpr int STEP = W == BACK ? -1 : 1, PER = kBlock<IO> / L;  // chunks of a block
+    auto body = [&](IO *cur, IO *next, int c, bool first) {
         if (NBUF == 1) {
             __syncthreads();
             load(cur, c);
             wait_vm<0>();
-        } else if (c == 0) {
+        } else if (first) {
             wait_vm<0>();
         } else {
             wait_vm<NST>();  // this wavefront's copies have landed
         }
         __syncthreads();
-        if (NBUF == 2) load(next, c + 1);
+        if (NBUF == 2) load(next, c + STEP);
         const int nc = count(c);
-        const IO *Qs = cur, *Ks = Qs + L * DKP;
+        const IO *Qs = cur, *Ks = Qs + L * C::KOFF;
         const char *rc = (const char *)(cur + L * C::TROW);
         const float *vec = (const float *)(rc + R::VEC);
         Frag vf[NCT];
 #pragma unroll
         for (int bt = 0; bt < NCT; ++bt)
-            vf[bt] = C::VOWN ? v_frag<16 * NCT>((const IO *)own, 4 * bt, vq, l16, g4)
-                             : v_frag<BV>(cur + 2 * L * DKP, vc0 + 4 * bt, vq, l16, g4);
+            vf[bt] = C::VOWN ? v_frag<16 * NCT>((const IO *)own, 4 * bt, 4 * NCT, l16, g4)
+                             : v_frag<BV>(cur + L * (C::KOFF + DKP), vc0 + 4 * bt, 8, l16, g4);
+        // the state is kept: X[dk][dv] of the accumulators, transposed by the unit matrix
+        const bool keep = W == STATES ? c % PER == 0 : W == BACK ? c % PER == PER - 1 || c == nch - 1 : false;
+        char *kept = W == FORWARD ? nullptr
+                                  : to.states + ((((size_t)bh * nblk + c / PER) * ncb + ((col0 + vc0) >> 5)) * NAT) * OP * R::FRAG;
         // K S (lane: column, tokens 16 t + 4 g4 + r) and S^T Q^T (lane: token, columns)
         f32x4 KS[2][NCT], O[2][NCT];
 #pragma unroll
@@ -429,7 +492,7 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
             Frag q[2], k[2], xf[NCT][SP];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                q[t] = rows.get(Qs, t, kk);
+                if constexpr (W == FORWARD) q[t] = rows.get(Qs, t, kk);
                 k[t] = rows.get(Ks, t, kk);
             }
 #pragma unroll
@@ -446,17 +509,45 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         KS[t][bt] = mfma(k[t], xf[bt][p], KS[t][bt]);
-                        if (p < OP) O[t][bt] = mfma(xf[bt][p], q[t], O[t][bt]);
+                        if (W == FORWARD && p < OP) O[t][bt] = mfma(xf[bt][p], q[t], O[t][bt]);
                     }
+            if (W != FORWARD && keep && col0 + (vc0 & ~31) < dv)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    Frag unit = {};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) unit[e] = (IO)(8 * g4 + e == 8 * (l16 >> 2) + 4 * u + (l16 & 3) ? 1.0f : 0.0f);
+#pragma unroll
+                    for (int p = 0; p < OP; ++p) {
+                        char *at = kept + ((2 * kk + u) * OP + p) * R::FRAG + lane * sizeof(Frag);
+                        f32x4 y[NCT];
+#pragma unroll
+                        for (int bt = 0; bt < NCT; ++bt) y[bt] = mfma(xf[bt][p], unit, f32x4{0, 0, 0, 0});
+                        if constexpr (ES == 4) {
+#pragma unroll
+                            for (int bt = 0; bt < NCT; ++bt) *(f32x4 *)(at + (NCT == 2 ? 16 * bt : 16 * (wave & 1))) = y[bt];
+                        } else {
+                            const f32x4 a0 = y[0], a1 = y[NCT - 1];
+                            const float z[8] = {a0[0], a0[1], a0[2], a0[3], a1[0], a1[1], a1[2], a1[3]};
+                            bf16x8 f;
+                            pack(z, f);
+                            const u32x4 w4 = __builtin_bit_cast(u32x4, f);
+                            if constexpr (NCT == 2)
+                                *(u32x4 *)at = w4;
+                            else
+                                *(u32x2 *)(at + 8 * (wave & 1)) = u32x2{w4[0], w4[1]};
+                        }
+                    }
+                }
         }
         if constexpr (C::VOWN) {
             // V's next rows over this chunk's, whose reads have returned
 #pragma unroll
             for (int bt = 0; bt < NCT; ++bt) asm volatile("" : "+v"(vf[bt]));
             __builtin_amdgcn_sched_barrier(0);
-            load_v(c + 1);
+            load_v(c + STEP);
         }
-        Frag tf[2][R::TP], pf[2][R::PP];
+        Frag tf[2][R::TP], pf[2][R::PP > 0 ? R::PP : 1];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
 #pragma unroll
@@ -464,19 +555,34 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
 #pragma unroll
             for (int p = 0; p < R::PP; ++p) pf[t][p] = *(const Frag *)(rc + R::P + (t * R::PP + p) * R::FRAG + lane * sizeof(Frag));
         }
-        f32x4 eg[2], rest[2];
+        f32x4 eg[2], rest[2], be[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             eg[t] = *(const f32x4 *)(vec + R::EG * L + 16 * t + 4 * g4);
             rest[t] = *(const f32x4 *)(vec + R::REST * L + 16 * t + 4 * g4);
+            be[t] = *(const f32x4 *)(vec + R::BETA * L + 16 * t + 4 * g4);
         }
-        Frag uf[NCT][OP], wf[NCT][SP];
+        const auto own_rows = __builtin_amdgcn_make_buffer_rsrc(
+            (void *)(to.rows + ((size_t)bh * a.T + (size_t)c * L) * dv), 0,
+            __builtin_amdgcn_readfirstlane(W == FORWARD ? 0 : nc * dv * 4), kBuf);
+        Frag uf[NCT][OP], wf[NCT][SP], gf[NCT][SP];
 #pragma unroll
         for (int bt = 0; bt < NCT; ++bt) {
             float x[8];
             Frag rf[SP];
+            if constexpr (W == BACK) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = (float)vf[bt][e] - eg[e >> 2][e & 3] * KS[e >> 2][bt][e & 3];
+                for (int t = 0; t < 2; ++t) {
+                    f32x4 y = KS[t][bt] * rest[t];
+#pragma unroll
+                    for (int p = SP - 1; p >= 0; --p) y = mfma(pf[t][p], vf[bt], y);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) x[4 * t + r] = y[r];
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = (float)vf[bt][e] - eg[e >> 2][e & 3] * KS[e >> 2][bt][e & 3];
+            }
             split8<SP>(x, rf);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
@@ -484,17 +590,41 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
 #pragma unroll
                 for (int r = 0; r < 4; ++r) x[4 * t + r] = u[r];
             }
-            split8<OP>(x, uf[bt]);
+            if constexpr (W == FORWARD) {
+                split8<OP>(x, uf[bt]);
+            } else {
+                const bool ok = col0 + vcol + 4 * bt < dv;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] *= rest[e >> 2][e & 3];
+                for (int e = 0; e < 8; ++e) {
+                    const int i = 16 * (e >> 2) + 4 * g4 + (e & 3);
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[e]), own_rows,
+                                                          ok ? (unsigned)((i * dv + col0 + vcol + 4 * bt) * 4) : kOut, 0, 0);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] *= be[e >> 2][e & 3];
+            }
+            if constexpr (W == BACK) {
+                float y[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    y[e] = (float)vf[bt][e] * (eg[e >> 2][e & 3] * a.scale);
+                    x[e] *= -eg[e >> 2][e & 3];
+                }
+                split8<SP>(y, gf[bt]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] *= rest[e >> 2][e & 3];
+            }
             split8<SP>(x, wf[bt]);
         }
         // output
+        if constexpr (W == FORWARD) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const float fade = vec[R::EG * L + 16 * t + l16] * a.scale;
+            for (int t = 0; t < 2; ++t) {
+                const float fade = vec[R::EG * L + 16 * t + l16] * a.scale;
 #pragma unroll
-            for (int bt = 0; bt < NCT; ++bt) O[t][bt] = mfma_parts<OP>(uf[bt], pf[t], O[t][bt] * fade);
+                for (int bt = 0; bt < NCT; ++bt) O[t][bt] = mfma_parts<OP>(uf[bt], pf[t], O[t][bt] * fade);
+            }
         }
         // state update
         const float decay = vec[R::EG * L + L - 1];
@@ -503,43 +633,51 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const Frag kf = cols.get(Ks, kk, t);
+                Frag qf;
+                if constexpr (W == BACK) qf = cols.get(Qs, kk, t);
 #pragma unroll
                 for (int bt = 0; bt < NCT; ++bt) {
                     f32x4 x = X[2 * kk + t][bt] * decay;
 #pragma unroll
-                    for (int p = SP - 1; p >= 0; --p) x = mfma(kf, wf[bt][p], x);
+                    for (int p = SP - 1; p >= 0; --p) {
+                        x = mfma(kf, wf[bt][p], x);
+                        if constexpr (W == BACK) x = mfma(qf, gf[bt][p], x);
+                    }
                     X[2 * kk + t][bt] = x;
                 }
             }
-        const auto os = __builtin_amdgcn_make_buffer_rsrc((void *)(og + (size_t)c * L * ldo), 0,
-                                                          __builtin_amdgcn_readfirstlane(nc * ldo * ES), kBuf);
+        if constexpr (W == FORWARD) {
+            const auto os = __builtin_amdgcn_make_buffer_rsrc((void *)(og + (size_t)c * L * ldo), 0,
+                                                              __builtin_amdgcn_readfirstlane(nc * ldo * ES), kBuf);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const unsigned at = ook ? (unsigned)(((16 * t + l16) * ldo + ocol) * ES) : kOut;
-            if constexpr (ES == 4) {
+            for (int t = 0; t < 2; ++t) {
+                const unsigned at = ook ? (unsigned)(((16 * t + l16) * ldo + ocol) * ES) : kOut;
+                if constexpr (ES == 4) {
 #pragma unroll
-                for (int i = 0; i < NCT; ++i)
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[t][i]), os, at + 16 * i, 0, 0);
-            } else {
-                const f32x4 a0 = O[t][0], a1 = O[t][NCT - 1];
-                const float y[8] = {a0[0], a0[1], a0[2], a0[3], a1[0], a1[1], a1[2], a1[3]};
-                bf16x8 o8;
-                pack(y, o8);
-                const u32x4 u = __builtin_bit_cast(u32x4, o8);
-                if constexpr (NCT == 2)
-                    __builtin_amdgcn_raw_buffer_store_b128(u, os, at, 0, 0);
-                else
-                    __builtin_amdgcn_raw_buffer_store_b64(u32x2{u[0], u[1]}, os, at, 0, 0);
+                    for (int i = 0; i < NCT; ++i)
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[t][i]), os, at + 16 * i, 0, 0);
+                } else {
+                    const f32x4 a0 = O[t][0], a1 = O[t][NCT - 1];
+                    const float y[8] = {a0[0], a0[1], a0[2], a0[3], a1[0], a1[1], a1[2], a1[3]};
+                    bf16x8 o8;
+                    pack(y, o8);
+                    const u32x4 u = __builtin_bit_cast(u32x4, o8);
+                    if constexpr (NCT == 2)
+                        __builtin_amdgcn_raw_buffer_store_b128(u, os, at, 0, 0);
+                    else
+                        __builtin_amdgcn_raw_buffer_store_b64(u32x2{u[0], u[1]}, os, at, 0, 0);
+                }
             }
         }
     };
+    const int first = W == BACK ? nch - 1 : 0;
     if (nch > 0) {
-        if (NBUF == 2) load(tile0, 0);
-        if constexpr (C::VOWN) load_v(0);
+        if (NBUF == 2) load(tile0, first);
+        if constexpr (C::VOWN) load_v(first);
     }
-    for (int c = 0; c < nch; c += 2) {
-        body(tile0, tile1, c);
-        if (c + 1 < nch) body(NBUF == 2 ? tile1 : tile0, tile0, c + 1);
+    for (int i = 0; i < nch; i += 2) {
+        body(tile0, tile1, first + STEP * i, i == 0);
+        if (i + 1 < nch) body(NBUF == 2 ? tile1 : tile0, tile0, first + STEP * (i + 1), false);
     }
     wait_vm<0>();  // no copy may still be on its way into LDS when the workgroup ends
 
@@ -556,6 +694,7 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
                                                           off == kOut ? kOut : off + r * dv * 4, 0, 0);
             }
     }
+    if constexpr (W != FORWARD) return;
     // rows behind the sequence's length
     constexpr int QPR = BV / 4;  // quads of a row
     const long long quads = (long long)(a.T - n) * QPR;
@@ -571,267 +710,525 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW>::PER_CU * NW / 4)) 
     }
 }
 
-// ---- gradients, token by token
+// ---- the gradients of a block, all blocks at once
 
-constexpr int kBV = 64;  // value columns of a workgroup
-
-__device__ __forceinline__ float decay(const DeltaArgs &a, int b, int h, long long t) {
-    return __builtin_amdgcn_exp2f(decay_log2(a.g[b * a.sg.s0 + h * a.sg.s1 + t * a.sg.s2]));
-}
-__device__ __forceinline__ float strength(const DeltaArgs &a, int b, int h, long long t) {
-    return a.beta[b * a.sb.s0 + h * a.sb.s1 + t * a.sb.s2];
-}
-
-struct Ws {
-    float *x, *du, *gq, *gk, *st, *dG;
+// From the state S at a block's start, its gradient D at the block's end, and X and dU
+// of its tokens (U = beta o X, dV = beta o dU; G now runs from the block's start):
+//   E1_ij = scale M_ij (do_i . U_j)  (j <= i),  E2_ij = M_ij (dV_i . U_j)  (j < i),
+//   dQ = scale e^G o (do S^T) + E1 K,
+//   dK = e^{G_L - G} o (U D^T) - e^G o (dV S^T) + E1^T Q - E2 K - E2^T K,
+//   dbeta_i = dU_i . X_i,
+//   dg_i = sum_{j >= i} (q.dq + k.dk - 2 beta dbeta)_j + <D, S_L>,
+//   <D, S_L> = e^{G_L} <D, S> + sum_j k_j . (e^{G_L - G} o (U D^T))_j.
+// The last sum is the decays' share of everything behind a token: it is exact, and
+// starts anew at each block, so that its roundings do not add up over a sequence.
+//
+// A workgroup has a block of kBlock tokens of one head of q and k and walks the
+// heads of v that share it.  A wavefront owns 16 RTW columns of d_qk for all tokens:
+// S and D come to it as operands straight from memory; do, X and dU are split once, by the
+// wavefront of their 16 tokens, and shared through LDS.  Everything is computed
+// transposed (lane: token, rows: d_qk), so that rows leave in whole vectors.
+struct GradIn {
+    const float *x, *du;
+    const char *s, *d;
 };
-Ws make_ws(const DeltaArgs &a) {
-    const size_t n = (size_t)a.B * a.H * a.T, c = (size_t)a.B * a.H;
-    Ws w;
-    w.x = a.ws;
-    w.du = w.x + n * a.dv;
-    w.gq = w.du + n * a.dv;
-    w.gk = w.gq + n * a.dk;
-    w.st = w.gk + n * a.dk;
-    w.dG = w.st + c * a.dk * a.dv;
-    return w;
+
+template <typename IO, int DKP_, int NW_>
+struct GCfg {
+    static constexpr int DKP = DKP_, NW = NW_, NTH = 64 * NW_;
+    static constexpr int SC = kBlock<IO>, NT = SC / 16, NAT = DKP / 16, RTW = NAT / NW;  // tokens and their tiles; tiles of d_qk
+    static constexpr int NG = NW / NT, CB = NG > 2 ? NG : 2;  // wavefronts of 16 tokens, 32-column blocks of a stage
+    static constexpr int OP = Types<IO>::XPARTS, NM = 1 + 2 * OP;
+    static constexpr int EPG = Types<IO>::EPG, QG = DKP / EPG, EG = SC / EPG;  // granules of a row of K, of E
+    static constexpr int OPS = CB * NT * NM * 512, ES = 2 * OP * SC * SC;      // elements of a stage, of E1 and E2
+    static constexpr int POOL = OPS > ES ? OPS : ES;
+    static_assert(NG >= 1 && EG >= 8 && RTW >= 1, "layout");
+};
+
+// slots of row `row` of a swizzled [SC][SC] matrix in the 32 columns of block jb
+template <int EGR>
+__device__ __forceinline__ bf16x8 e_row(const bf16 *m, int row, int jb, int g4) {
+    const int s = swz<EGR>(row & 15);
+    const bf16 *p = m + row * EGR * 8;
+    const int c0 = 32 * jb + 4 * g4, c1 = c0 + 16;
+    const bf16x4 x = *(const bf16x4 *)(p + (((c0 >> 3) ^ s) << 3) + (c0 & 7));
+    const bf16x4 y = *(const bf16x4 *)(p + (((c1 >> 3) ^ s) << 3) + (c1 & 7));
+    return bf16x8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+}
+template <int EGR>
+__device__ __forceinline__ f32x8 e_row(const float *m, int row, int jb, int g4) {
+    const int s = swz<EGR>(row & 15);
+    const float *p = m + row * EGR * 4;
+    const int c0 = 32 * jb + 4 * g4, c1 = c0 + 16;
+    const f32x4 x = *(const f32x4 *)(p + (((c0 >> 2) ^ s) << 2)), y = *(const f32x4 *)(p + (((c1 >> 2) ^ s) << 2));
+    return f32x8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+}
+// column c0 + l16 of the 32 rows of block ib, tokens as slots
+template <int EGR>
+__device__ __forceinline__ bf16x8 e_col(const bf16 *m, int ib, int c0, int l16, int g4) {
+    return v_frag<EGR * 8>(m + ib * 32 * EGR * 8, c0, 4, l16, g4);
+}
+template <int EGR>
+__device__ __forceinline__ f32x8 e_col(const float *m, int ib, int c0, int l16, int g4) {
+    f32x8 f;
+    const int c = c0 + l16;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int r = 32 * ib + 16 * (e >> 2) + 4 * g4 + (e & 3);
+        f[e] = m[r * EGR * 4 + (((c >> 2) ^ swz<EGR>(r & 15)) << 2) + (c & 3)];
+    }
+    return f;
 }
 
-// 64 columns of a head: 4 wavefronts hold 64 rows each.
-template <typename IO, bool REV>
-__global__ __launch_bounds__(256) void column_kernel(DeltaArgs a, Ws w) {
-    __shared__ float ks[256], qs[256], red[2][4][kBV];
-    const int ntile = (a.dv + kBV - 1) / kBV;
-    const int tile = blockIdx.x % ntile, bh = blockIdx.x / ntile, b = bh / a.H, h = bh % a.H, hk = h / (a.H / a.Hk);
-    const int tid = threadIdx.x, c = tid & 63, rg = tid >> 6, col = tile * kBV + c;
-    const bool ok = col < a.dv;
-    const int n = tokens(a, b);
-    float S[64];
-    const float *S0 = REV ? a.dS_T : a.S0;
+// four consecutive elements of a row
+template <typename IO>
+__device__ __forceinline__ void store4(IO *p, const float *x) {
+    typedef IO vec __attribute__((ext_vector_type(4)));
+    vec v;
 #pragma unroll
-    for (int i = 0; i < 64; ++i) {
-        const int r = rg * 64 + i;
-        S[i] = S0 && ok && r < a.dk ? S0[((size_t)bh * a.dk + r) * a.dv + col] : 0.0f;
-    }
-    for (int s = 0; s < n; ++s) {
-        const long long t = REV ? n - 1 - s : s;
-        const IO *q = (const IO *)a.q + b * a.sq.s0 + hk * a.sq.s1 + t * a.sq.s2;
-        const IO *k = (const IO *)a.k + b * a.sk.s0 + hk * a.sk.s1 + t * a.sk.s2;
-        __syncthreads();
-        ks[tid] = tid < a.dk ? to_f(k[tid]) : 0.0f;
-        qs[tid] = tid < a.dk ? to_f(q[tid]) : 0.0f;
-        const float gam = decay(a, b, h, t), beta = strength(a, b, h, t);
-        const size_t row = ((size_t)bh * a.T + t) * a.dv + col;
-        __syncthreads();
-        float acc = 0.0f;
-        if constexpr (REV) {
-            const float go = ok ? a.scale * to_f(((const IO *)a.d_o)[b * a.sdo.s0 + h * a.sdo.s1 + t * a.sdo.s2 + col]) : 0.0f;
-#pragma unroll
-            for (int i = 0; i < 64; ++i) {
-                S[i] += qs[rg * 64 + i] * go;
-                acc += ks[rg * 64 + i] * S[i];
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 64; ++i) {
-                S[i] *= gam;
-                acc += ks[rg * 64 + i] * S[i];
+    for (int e = 0; e < 4; ++e) v[e] = from_f<IO>(x[e]);
+    *(vec *)p = v;
+}
+
+template <typename IO, int DKP, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void grad_kernel(DeltaArgs a, GradIn in) {
+    using C = GCfg<IO, DKP, NW>;
+    using Frag = typename Types<IO>::Frag;
+    constexpr int SC = C::SC, NT = C::NT, NAT = C::NAT, RTW = C::RTW, NG = C::NG, CB = C::CB, OP = C::OP, NM = C::NM;
+    constexpr int QG = C::QG, EPG = C::EPG, FRAG = 64 * (int)sizeof(Frag);
+    __shared__ __attribute__((aligned(16))) IO kt[SC * DKP], qt[SC * DKP];
+    __shared__ __attribute__((aligned(16))) IO pool[C::POOL];
+    __shared__ __attribute__((aligned(16))) float hi[SC], lo[SC], be[SC], eg[SC], rest[SC], db[SC];
+    __shared__ float part[2][NW][SC], dots[NW];
+
+    const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g4 = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const long long nblk = (chunks(a.T) * L + SC - 1) / SC;
+    const int blk = (int)(blockIdx.x % nblk), bk = (int)(blockIdx.x / nblk), b = bk / a.Hk, hk = bk % a.Hk;
+    const int per = a.H / a.Hk, dk = a.dk, dv = a.dv, ncb = (dv + 31) >> 5;
+    const long long s0 = (long long)blk * SC;
+    const int n = (int)min((long long)SC, tokens(a, b) - s0);     // of the block's tokens, may be <= 0
+    const int rows = (int)min((long long)SC, a.T - s0);           // that the tensors have
+    IO *dqg = (IO *)a.dq + b * a.sdq.s0 + hk * a.sdq.s1 + s0 * a.sdq.s2;
+    IO *dkg = (IO *)a.dkk + b * a.sdk.s0 + hk * a.sdk.s1 + s0 * a.sdk.s2;
+    const float zero4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (n <= 0) {  // behind the sequence
+        for (int i = tid; i < rows * (dk / 4); i += C::NTH) {
+            const int t = i / (dk / 4), c = i % (dk / 4) * 4;
+            store4(dqg + t * a.sdq.s2 + c, zero4);
+            store4(dkg + t * a.sdk.s2 + c, zero4);
+        }
+        for (int h = hk * per; h < (hk + 1) * per; ++h) {
+            IO *dvg = (IO *)a.dvv + b * a.sdv.s0 + h * a.sdv.s1 + s0 * a.sdv.s2;
+            for (int i = tid; i < rows * (dv / 4); i += C::NTH) store4(dvg + i / (dv / 4) * a.sdv.s2 + i % (dv / 4) * 4, zero4);
+            if (tid < rows) {
+                a.dg[b * a.sdg.s0 + h * a.sdg.s1 + (s0 + tid) * a.sdg.s2] = 0.0f;
+                a.db[b * a.sdb.s0 + h * a.sdb.s1 + (s0 + tid) * a.sdb.s2] = 0.0f;
             }
         }
-        red[0][rg][c] = acc;
+        return;
+    }
+    // ---- K and Q
+    {
+        const IO *kp = (const IO *)a.k + b * a.sk.s0 + hk * a.sk.s1 + s0 * a.sk.s2;
+        const IO *qp = (const IO *)a.q + b * a.sq.s0 + hk * a.sq.s1 + s0 * a.sq.s2;
+        for (int i = tid; i < SC * QG; i += C::NTH) {
+            const int r = i / QG, g = i % QG, c = g * EPG, at = (r * QG + (g ^ swz<QG>(r & 15))) * EPG;
+            u32x4 x = {0, 0, 0, 0}, y = x;
+            if (r < n && c < dk) {
+                x = *(const u32x4 *)(kp + r * a.sk.s2 + c);
+                y = *(const u32x4 *)(qp + r * a.sq.s2 + c);
+            }
+            *(u32x4 *)(kt + at) = x;
+            *(u32x4 *)(qt + at) = y;
+        }
+    }
+    Cols<QG> cols;
+    cols.init((const IO *)nullptr, l16, g4);
+    f32x4 tq[RTW][NT], tk[RTW][NT];
+#pragma unroll
+    for (int i = 0; i < RTW; ++i)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) tq[i][t] = tk[i][t] = f32x4{0, 0, 0, 0};
+    const int rt = wave % NT, gq = wave / NT;  // this wavefront's 16 tokens where it splits and scores
+    const bool mine1 = gq == 0, mine2 = gq == (NG > 1 ? 1 : 0);
+
+    for (int h = hk * per; h < (hk + 1) * per; ++h) {
+        const size_t cell = (size_t)b * a.H + h;
         __syncthreads();
-        acc = (red[0][0][c] + red[0][1][c]) + (red[0][2][c] + red[0][3][c]);
-        if constexpr (REV) {
-            const float dv = beta * acc;
-            if (ok && rg == 0) {
-                w.du[row] = acc;
-                ((IO *)a.dvv)[b * a.sdv.s0 + h * a.sdv.s1 + t * a.sdv.s2 + col] = from_f<IO>(dv);
+        if (tid < 64) {
+            // gates of the block's tokens
+            double G = 0.0;
+            float beta = 0.0f;
+            if (lane < n) {
+                G = gate_log2(a.g[b * a.sg.s0 + h * a.sg.s1 + (s0 + lane) * a.sg.s2]);
+                beta = a.beta[b * a.sb.s0 + h * a.sb.s1 + (s0 + lane) * a.sb.s2];
             }
 #pragma unroll
-            for (int i = 0; i < 64; ++i) S[i] = gam * (S[i] - ks[rg * 64 + i] * dv);
-        } else {
-            const float v = ok ? to_f(((const IO *)a.v)[b * a.sv.s0 + h * a.sv.s1 + t * a.sv.s2 + col]) : 0.0f;
-            const float x = v - acc;
-            float y = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 64; ++i) {
-                S[i] += ks[rg * 64 + i] * (beta * x);
-                y += qs[rg * 64 + i] * S[i];
+            for (int m = 1; m < 64; m <<= 1) {
+                const double x = __shfl_up(G, m);
+                if (lane >= m) G += x;
             }
-            red[1][rg][c] = y;
-            if (w.x && ok && rg == 0) w.x[row] = x;
+            const double GL = __shfl(G, 63), top = rint(G * 64.0) / 64.0;
+            if (lane < SC) {
+                hi[lane] = (float)top;
+                lo[lane] = (float)(G - top);
+                be[lane] = beta;
+                eg[lane] = __builtin_amdgcn_exp2f((float)G);
+                rest[lane] = __builtin_amdgcn_exp2f((float)(GL - G));
+            }
+        }
+        __syncthreads();
+        f32x4 aq[RTW][NT], ak1[RTW][NT], ak2[RTW][NT], e1[NT], e2[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            e1[t] = e2[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < RTW; ++i) aq[i][t] = ak1[i][t] = ak2[i][t] = f32x4{0, 0, 0, 0};
+        }
+        const int tok = 16 * rt + l16;
+        const float *xr = in.x + (cell * a.T + s0 + tok) * dv, *ur = in.du + (cell * a.T + s0 + tok) * dv;
+        const IO *gr = (const IO *)a.d_o + b * a.sdo.s0 + h * a.sdo.s1 + (s0 + tok) * a.sdo.s2;
+        IO *vr = (IO *)a.dvv + b * a.sdv.s0 + h * a.sdv.s1 + (s0 + tok) * a.sdv.s2;
+        const char *sp = in.s + (cell * nblk + blk) * ncb * NAT * OP * FRAG + lane * sizeof(Frag);
+        const char *dp = in.d + (cell * nblk + blk) * ncb * NAT * OP * FRAG + lane * sizeof(Frag);
+        float dot = 0.0f;
+        for (int base = 0; base < ncb; base += CB) {
+            if (base > 0) __syncthreads();
+            // operands of CB blocks of columns: do, parts of X, parts of dU; dv on the way
+#pragma unroll
+            for (int j = 0; j < CB / NG; ++j) {
+                const int cbl = gq + j * NG, c0 = 32 * (base + cbl) + 8 * g4;
+                if (base + cbl < ncb) {
+                    const bool ok = tok < n && c0 < dv;
+                    const Frag go = row8(gr + c0, ok);
+                    const f32x8 x = row8(xr + c0, ok), u = row8(ur + c0, ok);
+                    float y[8], z[8], w[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        y[e] = x[e];
+                        z[e] = u[e];
+                        w[e] = u[e] * be[tok];
+                    }
+                    Frag *to = (Frag *)pool + (size_t)(cbl * NT + rt) * NM * 64 + lane;
+                    Frag fx[OP], fu[OP];
+                    split8<OP>(y, fx);
+                    split8<OP>(z, fu);
+                    to[0] = go;
+#pragma unroll
+                    for (int p = 0; p < OP; ++p) {
+                        to[(1 + p) * 64] = fx[p];
+                        to[(1 + OP + p) * 64] = fu[p];
+                    }
+                    if (tok < rows && c0 < dv) {
+                        store4(vr + c0, w);
+                        store4(vr + c0 + 4, w + 4);
+                    }
+                }
+            }
             __syncthreads();
-            y = (red[1][0][c] + red[1][1][c]) + (red[1][2][c] + red[1][3][c]);
-            if (a.o && ok && rg == 0)
-                ((IO *)a.o)[b * a.so.s0 + h * a.so.s1 + t * a.so.s2 + col] = from_f<IO>(a.scale * y);
-        }
-    }
-    IO *out = REV ? (IO *)a.dvv : (IO *)a.o;
-    const Strides so = REV ? a.sdv : a.so;
-    for (long long t = n + rg; t < a.T; t += 4)
-        if (out && ok) out[b * so.s0 + h * so.s1 + t * so.s2 + col] = from_f<IO>(0.0f);
-    float *Sn = REV ? a.dS0 : a.S_T;
-    if (!Sn) return;
 #pragma unroll
-    for (int i = 0; i < 64; ++i) {
-        const int r = rg * 64 + i;
-        if (ok && r < a.dk) Sn[((size_t)bh * a.dk + r) * a.dv + col] = S[i];
-    }
-}
-
-__device__ __forceinline__ float wave_sum(float x) {
+            for (int cbl = 0; cbl < CB; ++cbl) {
+                if (base + cbl >= ncb) break;
+                const Frag *op = (const Frag *)pool + (size_t)cbl * NT * NM * 64 + lane;
+                Frag sf[RTW][OP], df[RTW][OP];
 #pragma unroll
-    for (int m = 32; m > 0; m >>= 1) x += __shfl_xor(x, m);
-    return x;
-}
-
-// One row of the memory a wavefront, given every token's x and du.
-template <typename IO, bool REV>
-__global__ __launch_bounds__(64) void row_kernel(DeltaArgs a, Ws w) {
-    const int r = blockIdx.x % a.dk, bh = blockIdx.x / a.dk, b = bh / a.H, h = bh % a.H, hk = h / (a.H / a.Hk);
-    const int lane = threadIdx.x, n = tokens(a, b);
-    float S[8];
-    const float *S0 = REV ? a.dS_T : a.S0;
+                for (int i = 0; i < RTW; ++i)
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        S[i] = S0 && lane + 64 * i < a.dv ? S0[((size_t)bh * a.dk + r) * a.dv + lane + 64 * i] : 0.0f;
-    for (int s = 0; s < n; ++s) {
-        const long long t = REV ? n - 1 - s : s;
-        const float gam = decay(a, b, h, t), beta = strength(a, b, h, t);
-        const float k = to_f(((const IO *)a.k)[b * a.sk.s0 + hk * a.sk.s1 + t * a.sk.s2 + r]);
-        const float q = to_f(((const IO *)a.q)[b * a.sq.s0 + hk * a.sq.s1 + t * a.sq.s2 + r]);
-        const IO *go = (const IO *)a.d_o + b * a.sdo.s0 + h * a.sdo.s1 + t * a.sdo.s2;
-        const size_t row = (size_t)bh * a.T + t;
-        float y = 0.0f, z = 0.0f;
+                    for (int p = 0; p < OP; ++p) {
+                        const size_t off = ((size_t)((base + cbl) * NAT + wave * RTW + i) * OP + p) * FRAG;
+                        sf[i][p] = *(const Frag *)(sp + off);
+                        df[i][p] = *(const Frag *)(dp + off);
+                    }
+                // scores of this wavefront's tokens i (lanes) with all tokens j <= i (rows)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int c = lane + 64 * i;
-            const bool ok = c < a.dv;
-            const float x = ok ? w.x[row * a.dv + c] : 0.0f, dv = ok ? beta * w.du[row * a.dv + c] : 0.0f;
-            const float o = ok ? to_f(go[c]) : 0.0f;
-            if constexpr (REV) {
-                S[i] += a.scale * q * o;
-                y += S[i] * (beta * x);
-                S[i] = gam * (S[i] - k * dv);
-            } else {
-                S[i] *= gam;
-                y -= S[i] * dv;
-                S[i] += k * (beta * x);
-                z += a.scale * S[i] * o;
+                for (int t = 0; t < NT; ++t)
+                    if (t <= rt) {
+                        Frag fx[OP];
+#pragma unroll
+                        for (int p = 0; p < OP; ++p) fx[p] = op[(t * NM + 1 + p) * 64];
+                        if (mine1) {
+                            const Frag go = op[rt * NM * 64];
+#pragma unroll
+                            for (int p = OP - 1; p >= 0; --p) e1[t] = mfma(fx[p], go, e1[t]);
+                        }
+                        if (mine2) {
+                            Frag fu[OP];
+#pragma unroll
+                            for (int p = 0; p < OP; ++p) fu[p] = op[(rt * NM + 1 + OP + p) * 64];
+                            e2[t] = mfma_parts<OP>(fx, fu, e2[t]);
+                        }
+                    }
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const Frag go = op[t * NM * 64];
+                    Frag fx[OP], fu[OP];
+#pragma unroll
+                    for (int p = 0; p < OP; ++p) {
+                        fx[p] = op[(t * NM + 1 + p) * 64];
+                        fu[p] = op[(t * NM + 1 + OP + p) * 64];
+                    }
+#pragma unroll
+                    for (int i = 0; i < RTW; ++i) {
+#pragma unroll
+                        for (int p = OP - 1; p >= 0; --p) aq[i][t] = mfma(sf[i][p], go, aq[i][t]);
+                        ak1[i][t] = mfma_parts<OP>(df[i], fx, ak1[i][t]);
+                        ak2[i][t] = mfma_parts<OP>(sf[i], fu, ak2[i][t]);
+                    }
+                }
+                // <D, S>
+#pragma unroll
+                for (int i = 0; i < RTW; ++i)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float x = (float)sf[i][0][e], y = (float)df[i][0][e];
+                        if constexpr (OP == 2) {
+                            x += (float)sf[i][1][e];
+                            y += (float)df[i][1][e];
+                        }
+                        dot += x * y;
+                    }
             }
         }
-        y = wave_sum(y);
-        if constexpr (!REV) z = wave_sum(z);
-        if (lane == 0) {
-            if constexpr (REV) {
-                w.gk[row * a.dk + r] += y;
-            } else {
-                w.gk[row * a.dk + r] = y;
-                w.gq[row * a.dk + r] = z;
+        __syncthreads();
+        // ---- E1 and -E2, decayed, to LDS over the operands; dbeta on E2's diagonal
+        IO *E1 = pool, *E2 = pool + OP * SC * SC;
+        {
+            const int i = tok;
+            const float hii = hi[i], loi = lo[i], bi = be[i];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                float x[4], y[4];
+                const f32x4 hj = *(const f32x4 *)(hi + 16 * t + 4 * g4), lj = *(const f32x4 *)(lo + 16 * t + 4 * g4);
+                const f32x4 bj = *(const f32x4 *)(be + 16 * t + 4 * g4);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int j = 16 * t + 4 * g4 + r;
+                    const float M = j <= i ? __builtin_amdgcn_exp2f((hii - hj[r]) + (loi - lj[r])) * bj[r] : 0.0f;
+                    x[r] = e1[t][r] * (M * a.scale);
+                    y[r] = j < i ? -e2[t][r] * (M * bi) : 0.0f;
+                    if (mine2 && j == i) db[i] = e2[t][r];
+                }
+                const int c = 16 * t + 4 * g4, at = i * SC + (((c / EPG) ^ swz<C::EG>(l16)) * EPG) + c % EPG;
+#pragma unroll
+                for (int p = 0; p < OP; ++p) {
+                    float v[4], w[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const IO m = from_f<IO>(x[r]), o = from_f<IO>(y[r]);
+                        v[r] = to_f(m);
+                        w[r] = to_f(o);
+                        x[r] -= v[r];
+                        y[r] -= w[r];
+                    }
+                    if (mine1) store4(E1 + p * SC * SC + at, v);
+                    if (mine2) store4(E2 + p * SC * SC + at, w);
+                }
+            }
+        }
+        __syncthreads();
+        // ---- the products with the state, scaled; then those within the block
+        float kd[NT], dG[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int i = 16 * t + l16;
+            const float ei = eg[i], bi = be[i], ri = rest[i];
+            kd[t] = dG[t] = 0.0f;
+#pragma unroll
+            for (int x = 0; x < RTW; ++x) {
+                const int id = wave * RTW + x, c = 32 * (id >> 1) + 8 * g4 + 4 * (id & 1);
+                const IO *kr = kt + (i * QG + ((c / EPG) ^ swz<QG>(l16))) * EPG + c % EPG;
+                ak1[x][t] *= bi * ri;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) kd[t] += to_f(kr[r]) * ak1[x][t][r];
+                ak1[x][t] -= ak2[x][t] * (bi * ei);
+                aq[x][t] *= a.scale * ei;
+            }
+        }
+#pragma unroll
+        for (int ib = 0; ib < SC / 32; ++ib) {
+            Frag kf[RTW], qf[RTW];
+#pragma unroll
+            for (int x = 0; x < RTW; ++x) {
+                const int id = wave * RTW + x;
+                kf[x] = cols.get(kt + ib * 32 * DKP, id >> 1, id & 1);
+                qf[x] = cols.get(qt + ib * 32 * DKP, id >> 1, id & 1);
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int p = OP - 1; p >= 0; --p) {
+                    const IO *m1 = E1 + p * SC * SC, *m2 = E2 + p * SC * SC;
+                    if (ib <= t / 2) {
+                        const Frag r1 = e_row<C::EG>(m1, 16 * t + l16, ib, g4), r2 = e_row<C::EG>(m2, 16 * t + l16, ib, g4);
+#pragma unroll
+                        for (int x = 0; x < RTW; ++x) {
+                            aq[x][t] = mfma(kf[x], r1, aq[x][t]);
+                            ak1[x][t] = mfma(kf[x], r2, ak1[x][t]);
+                        }
+                    }
+                    if (ib >= t / 2) {
+                        const Frag c1 = e_col<C::EG>(m1, ib, 16 * t, l16, g4), c2 = e_col<C::EG>(m2, ib, 16 * t, l16, g4);
+#pragma unroll
+                        for (int x = 0; x < RTW; ++x) {
+                            ak1[x][t] = mfma(qf[x], c1, ak1[x][t]);
+                            ak1[x][t] = mfma(kf[x], c2, ak1[x][t]);
+                        }
+                    }
+                }
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int i = 16 * t + l16;
+#pragma unroll
+            for (int x = 0; x < RTW; ++x) {
+                const int id = wave * RTW + x, c = 32 * (id >> 1) + 8 * g4 + 4 * (id & 1);
+                const int at = (i * QG + ((c / EPG) ^ swz<QG>(l16))) * EPG + c % EPG;
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    dG[t] += to_f(qt[at + r]) * aq[x][t][r] + to_f(kt[at + r]) * ak1[x][t][r];
+                tq[x][t] += aq[x][t];
+                tk[x][t] += ak1[x][t];
+            }
+            kd[t] += __shfl_xor(kd[t], 16);
+            dG[t] += __shfl_xor(dG[t], 16);
+            kd[t] += __shfl_xor(kd[t], 32);
+            dG[t] += __shfl_xor(dG[t], 32);
+            if (g4 == 0) {
+                part[0][wave][i] = dG[t];
+                part[1][wave][i] = kd[t];
+            }
+        }
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) dot += __shfl_xor(dot, m);
+        if (lane == 0) dots[wave] = dot;
+        __syncthreads();
+        if (tid < 64) {
+            // dlog_decay: sums from each token to the block's end, and what is behind it
+            float x = 0.0f, y = 0.0f, tail = 0.0f;
+            const bool ok = lane < n;
+            if (ok) {
+#pragma unroll
+                for (int w = 0; w < NW; ++w) {
+                    x += part[0][w][lane];
+                    y += part[1][w][lane];
+                }
+                x -= 2.0f * be[lane] * db[lane];
+            }
+#pragma unroll
+            for (int w = 0; w < NW; ++w) tail += dots[w];
+#pragma unroll
+            for (int m = 1; m < 64; m <<= 1) {
+                const float z = __shfl_down(x, m);
+                if (lane + m < 64) x += z;
+                y += __shfl_xor(y, m);
+            }
+            x += eg[SC - 1] * tail + y;
+            if (lane < rows) {
+                const float g = ok ? a.g[b * a.sg.s0 + h * a.sg.s1 + (s0 + lane) * a.sg.s2] : 0.0f;
+                const bool gone = __builtin_amdgcn_exp2f(gate_log2(g)) == 0.0f;
+                a.dg[b * a.sdg.s0 + h * a.sdg.s1 + (s0 + lane) * a.sdg.s2] = ok && !gone ? x : 0.0f;
+                a.db[b * a.sdb.s0 + h * a.sdb.s1 + (s0 + lane) * a.sdb.s2] = ok ? db[lane] : 0.0f;
             }
         }
     }
-    if constexpr (!REV)
+    // ---- rows of dq and dk
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (lane + 64 * i < a.dv) w.st[((size_t)bh * a.dk + r) * a.dv + lane + 64 * i] = S[i];
-}
-
-// dbeta and the decay's share of each token, one wavefront a token
-template <typename IO>
-__global__ __launch_bounds__(64) void token_kernel(DeltaArgs a, Ws w) {
-    const long long row = blockIdx.x;
-    const int bh = (int)(row / a.T), b = bh / a.H, h = bh % a.H, hk = h / (a.H / a.Hk);
-    const long long t = row % a.T;
-    const int lane = threadIdx.x;
-    float db = 0.0f, dG = 0.0f;
-    if (t < tokens(a, b)) {
-        const IO *q = (const IO *)a.q + b * a.sq.s0 + hk * a.sq.s1 + t * a.sq.s2;
-        const IO *k = (const IO *)a.k + b * a.sk.s0 + hk * a.sk.s1 + t * a.sk.s2;
-        for (int c = lane; c < a.dv; c += 64) db += w.x[row * a.dv + c] * w.du[row * a.dv + c];
-        for (int c = lane; c < a.dk; c += 64)
-            dG += to_f(q[c]) * w.gq[row * a.dk + c] + to_f(k[c]) * w.gk[row * a.dk + c];
-        db = wave_sum(db);
-        dG = wave_sum(dG) - 2.0f * strength(a, b, h, t) * db;
-    }
-    if (lane == 0) {
-        a.db[b * a.sdb.s0 + h * a.sdb.s1 + t * a.sdb.s2] = db;
-        w.dG[row] = dG;
-    }
-}
-
-__global__ __launch_bounds__(64) void decay_kernel(DeltaArgs a, Ws w) {
-    const int bh = blockIdx.x, b = bh / a.H, h = bh % a.H, n = tokens(a, b);
-    const size_t size = (size_t)a.dk * a.dv;
-    double sum = 0.0;
-    if (a.dS_T)
-        for (size_t i = threadIdx.x; i < size; i += 64) sum += (double)a.dS_T[bh * size + i] * w.st[bh * size + i];
+    for (int t = 0; t < NT; ++t) {
+        const int i = 16 * t + l16;
 #pragma unroll
-    for (int m = 32; m > 0; m >>= 1) sum += __shfl_xor(sum, m);
-    if (threadIdx.x != 0) return;
-    for (long long t = a.T - 1; t >= 0; --t) {
-        if (t < n) sum += w.dG[(size_t)bh * a.T + t];
-        a.dg[b * a.sdg.s0 + h * a.sdg.s1 + t * a.sdg.s2] = t < n && decay(a, b, h, t) != 0.0f ? (float)sum : 0.0f;
-    }
-}
-
-// dq and dk: the heads of a group summed
-template <typename IO>
-__global__ __launch_bounds__(64) void group_kernel(DeltaArgs a, Ws w) {
-    const long long row = blockIdx.x;
-    const int bk = (int)(row / a.T), b = bk / a.Hk, hk = bk % a.Hk, r = a.H / a.Hk;
-    const long long t = row % a.T;
-    const bool live = t < tokens(a, b);
-    for (int c = threadIdx.x; c < a.dk; c += 64) {
-        float q = 0.0f, k = 0.0f;
-        for (int i = 0; i < r && live; ++i) {
-            const size_t at = (((size_t)b * a.H + hk * r + i) * a.T + t) * a.dk + c;
-            q += w.gq[at];
-            k += w.gk[at];
+        for (int x = 0; x < RTW; ++x) {
+            const int id = wave * RTW + x, c = 32 * (id >> 1) + 8 * g4 + 4 * (id & 1);
+            if (i < rows && c < dk) {
+                const f32x4 q = tq[x][t], k = tk[x][t];
+                const float u[4] = {q[0], q[1], q[2], q[3]}, v[4] = {k[0], k[1], k[2], k[3]};
+                store4(dqg + i * a.sdq.s2 + c, u);
+                store4(dkg + i * a.sdk.s2 + c, v);
+            }
         }
-        ((IO *)a.dq)[b * a.sdq.s0 + hk * a.sdq.s1 + t * a.sdq.s2 + c] = from_f<IO>(q);
-        ((IO *)a.dkk)[b * a.sdk.s0 + hk * a.sdk.s1 + t * a.sdk.s2 + c] = from_f<IO>(k);
     }
 }
 
+// ---- launches
 
-template <typename IO, int DKP, int NCT, int NW>
-hipError_t launch_shape(const DeltaArgs &a, const char *rec, hipStream_t s) {
+template <typename IO, int DKP, int NCT, int NW, Walk W>
+hipError_t launch_shape(const DeltaArgs &a, const char *rec, WalkOut to, hipStream_t s) {
     const dim3 grid((unsigned)(a.B * a.H * ((a.dv + 16 * NCT * NW - 1) / (16 * NCT * NW))));
     if constexpr (sizeof(IO) == 4)
-        delta_kernel<IO, DKP, NCT, NW, 1><<<grid, 64 * NW, 0, s>>>(a, rec);
+        delta_kernel<IO, DKP, NCT, NW, 1, W><<<grid, 64 * NW, 0, s>>>(a, rec, to);
+    else if constexpr (W == STATES)
+        delta_kernel<IO, DKP, NCT, NW, 2, W><<<grid, 64 * NW, 0, s>>>(a, rec, to);
     else if (a.S_T)
-        delta_kernel<IO, DKP, NCT, NW, 3><<<grid, 64 * NW, 0, s>>>(a, rec);
+        delta_kernel<IO, DKP, NCT, NW, 3, W><<<grid, 64 * NW, 0, s>>>(a, rec, to);
     else
-        delta_kernel<IO, DKP, NCT, NW, 2><<<grid, 64 * NW, 0, s>>>(a, rec);
+        delta_kernel<IO, DKP, NCT, NW, 2, W><<<grid, 64 * NW, 0, s>>>(a, rec, to);
     return hipGetLastError();
+}
+
+template <typename IO, Walk W>
+hipError_t launch_walk(const DeltaArgs &a, const char *rec, WalkOut to, hipStream_t s) {
+    constexpr bool BF = sizeof(IO) == 2;
+    const bool wide = (long long)a.B * a.H * ((a.dv + 127) / 128) >= 256;
+    if (a.dk <= 64)
+        return wide ? launch_shape<IO, 64, 2, 4, W>(a, rec, to, s) : launch_shape<IO, 64, 1, 4, W>(a, rec, to, s);
+    if (a.dk <= 128)
+        return wide ? launch_shape<IO, 128, 2, 4, W>(a, rec, to, s) : launch_shape<IO, 128, 1, 4, W>(a, rec, to, s);
+    return wide ? launch_shape<IO, 256, BF ? 2 : 1, BF ? 4 : 8, W>(a, rec, to, s) : launch_shape<IO, 256, 1, 4, W>(a, rec, to, s);
 }
 
 template <typename IO>
 hipError_t launch_fwd_t(const DeltaArgs &a, hipStream_t s) {
-    constexpr bool BF = sizeof(IO) == 2;
     char *rec = (char *)a.ws;
-    const long long cells = (long long)a.B * a.H, total = cells * chunks(a.T);
-    prep_kernel<IO><<<dim3((unsigned)((total + kPrepWaves - 1) / kPrepWaves)), 64 * kPrepWaves, 0, s>>>(a, rec, total);
-    const bool wide = cells * ((a.dv + 127) / 128) >= 256;
-    if (a.dk <= 64)
-        return wide ? launch_shape<IO, 64, 2, 4>(a, rec, s) : launch_shape<IO, 64, 1, 4>(a, rec, s);
-    if (a.dk <= 128)
-        return wide ? launch_shape<IO, 128, 2, 4>(a, rec, s) : launch_shape<IO, 128, 1, 4>(a, rec, s);
-    return wide ? launch_shape<IO, 256, BF ? 2 : 1, BF ? 4 : 8>(a, rec, s) : launch_shape<IO, 256, 1, 4>(a, rec, s);
+    const long long total = (long long)a.B * a.H * chunks(a.T);
+    prep_kernel<IO, false><<<dim3((unsigned)((total + kPrepWaves - 1) / kPrepWaves)), 64 * kPrepWaves, 0, s>>>(a, rec, nullptr, total);
+    return launch_walk<IO, FORWARD>(a, rec, WalkOut{}, s);
+}
+
+// Workspace of the backward, bytes from its start; every part is a multiple of 16.
+struct BwdWs {
+    size_t rec, rec_back, x, du, s, d, total;
+};
+template <typename IO>
+BwdWs bwd_ws(size_t cells, int T, int dk, int dv) {
+    const size_t nch = (size_t)chunks(T), nblk = (nch * L + kBlock<IO> - 1) / kBlock<IO>;
+    const int dkp = dk <= 64 ? 64 : dk <= 128 ? 128 : 256;
+    const size_t states = cells * nblk * ((dv + 31) / 32) * (dkp / 16) * Types<IO>::XPARTS * 64 * sizeof(typename Types<IO>::Frag);
+    BwdWs w;
+    w.rec = 0;
+    w.rec_back = w.rec + cells * nch * Rec<IO, STATES>::BYTES;
+    w.x = w.rec_back + cells * nch * Rec<IO, BACK>::BYTES;
+    w.du = w.x + cells * T * dv * 4;
+    w.s = w.du + cells * T * dv * 4;
+    w.d = w.s + states;
+    w.total = w.d + states;
+    return w;
 }
 
 template <typename IO>
 hipError_t launch_bwd_t(const DeltaArgs &a, hipStream_t s) {
-    const Ws w = make_ws(a);
-    const unsigned cols = (unsigned)(a.B * a.H * ((a.dv + kBV - 1) / kBV)), cells = (unsigned)(a.B * a.H);
-    column_kernel<IO, false><<<dim3(cols), 256, 0, s>>>(a, w);
-    column_kernel<IO, true><<<dim3(cols), 256, 0, s>>>(a, w);
-    row_kernel<IO, false><<<dim3(cells * a.dk), 64, 0, s>>>(a, w);
-    row_kernel<IO, true><<<dim3(cells * a.dk), 64, 0, s>>>(a, w);
-    token_kernel<IO><<<dim3(cells * a.T), 64, 0, s>>>(a, w);
-    decay_kernel<<<dim3(cells), 64, 0, s>>>(a, w);
-    group_kernel<IO><<<dim3((unsigned)(a.B * a.Hk) * a.T), 64, 0, s>>>(a, w);
+    char *ws = (char *)a.ws;
+    const size_t cells = (size_t)a.B * a.H;
+    const BwdWs w = bwd_ws<IO>(cells, a.T, a.dk, a.dv);
+    const long long total = (long long)cells * chunks(a.T);
+    prep_kernel<IO, true><<<dim3((unsigned)((total + kPrepWaves - 1) / kPrepWaves)), 64 * kPrepWaves, 0, s>>>(a, ws + w.rec, ws + w.rec_back, total);
+    hipError_t e = launch_walk<IO, STATES>(a, ws + w.rec, WalkOut{(float *)(ws + w.x), ws + w.s}, s);
+    if (e != hipSuccess) return e;
+    DeltaArgs back = a;
+    back.v = a.d_o;
+    back.sv = a.sdo;
+    back.S0 = a.dS_T;
+    back.S_T = a.dS0;
+    e = launch_walk<IO, BACK>(back, ws + w.rec_back, WalkOut{(float *)(ws + w.du), ws + w.d}, s);
+    if (e != hipSuccess) return e;
+    const GradIn in{(const float *)(ws + w.x), (const float *)(ws + w.du), ws + w.s, ws + w.d};
+    const long long nblk = (chunks(a.T) * L + kBlock<IO> - 1) / kBlock<IO>;
+    const dim3 grid((unsigned)((long long)a.B * a.Hk * nblk));
+    if (a.dk <= 64)
+        grad_kernel<IO, 64, 4><<<grid, 256, 0, s>>>(a, in);
+    else if (a.dk <= 128)
+        grad_kernel<IO, 128, 4><<<grid, 256, 0, s>>>(a, in);
+    else
+        grad_kernel<IO, 256, 8><<<grid, 512, 0, s>>>(a, in);
     return hipGetLastError();
 }
 
@@ -840,8 +1237,8 @@ hipError_t launch_bwd_t(const DeltaArgs &a, hipStream_t s) {
 size_t deltarule_workspace_floats(int B, int Hk, int H, int T, int dk, int dv, int io_bf16, int backward) {
     (void)Hk;
     const size_t n = (size_t)B * H;
-    if (!backward) return n * chunks(T) * (io_bf16 ? Rec<bf16>::BYTES : Rec<float>::BYTES) / 4;
-    return n * T * (2 * (size_t)dv + 2 * (size_t)dk + 1) + n * dk * dv;
+    if (!backward) return n * chunks(T) * (io_bf16 ? Rec<bf16, FORWARD>::BYTES : Rec<float, FORWARD>::BYTES) / 4;
+    return (io_bf16 ? bwd_ws<bf16>(n, T, dk, dv).total : bwd_ws<float>(n, T, dk, dv).total) / 4;
 }
 
 hipError_t launch_deltarule_fwd(const DeltaArgs &a, int io_bf16, hipStream_t s) {
