@@ -53,7 +53,7 @@ template <typename IO, Walk W>
 struct Rec {
     typedef typename Types<IO>::Frag Frag;
     static constexpr bool BF = sizeof(IO) == 2;
-    static constexpr int TP = !BF ? 1 : W == STATES ? 2 : 3;                    // parts of the inverse
+    static constexpr int TP = BF ? 3 : 1;                                       // parts of the inverse
     static constexpr int PP = W == STATES ? 0 : !BF ? 1 : W == FORWARD ? 2 : 3;  // parts of the scores
     static constexpr int FRAG = 64 * (int)sizeof(Frag);                         // bytes of a tile's part
     static constexpr int P = 2 * TP * FRAG, VEC = P + 2 * PP * FRAG, EG = 0, REST = 1, BETA = 2;
@@ -73,10 +73,35 @@ __device__ __forceinline__ float gate_log2(float g) {
     return x < -1024.0f ? -1024.0f : x;
 }
 
+// 8 floats as a sum of PARTS bfloat16 operands.  All but the last part are cut, not
+// rounded: the upper halves of two floats by one byte permutation, the rest by a mask
+// and a subtraction.  Three parts hold a float's 24 bits, so the third is cut too and the
+// sum is exact; of two the second is rounded, 2^-17.  (A conversion is half as fast as those, and
+// v_dot2c_f32_bf16 in place of the subtraction does not run beside the MFMA.)
 template <int PARTS>
 __device__ __forceinline__ void split8(const float *x, bf16x8 *f) {
+    unsigned y[8];
 #pragma unroll
-    for (int p = 0; p < 4; ++p) split2<PARTS, false>(x[2 * p], x[2 * p + 1], f, p);
+    for (int e = 0; e < 8; ++e) y[e] = __float_as_uint(x[e]);
+#pragma unroll
+    for (int q = 0; q < PARTS; ++q) {
+        u32x4 w;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            unsigned &y0 = y[2 * p], &y1 = y[2 * p + 1];
+            if (q == PARTS - 1 && PARTS < 3) {
+                const bf16x2 h = __builtin_convertvector((f32x2{__uint_as_float(y0), __uint_as_float(y1)}), bf16x2);
+                w[p] = __builtin_bit_cast(unsigned, h);
+            } else {
+                w[p] = __builtin_amdgcn_perm(y1, y0, 0x07060302u);
+            }
+            if (q + 1 < PARTS) {
+                y0 = __float_as_uint(__uint_as_float(y0) - __uint_as_float(y0 & 0xffff0000u));
+                y1 = __float_as_uint(__uint_as_float(y1) - __uint_as_float(y1 & 0xffff0000u));
+            }
+        }
+        f[q] = __builtin_bit_cast(bf16x8, w);
+    }
 }
 template <int PARTS>
 __device__ __forceinline__ void split8(const float *x, f32x8 *f) {
@@ -283,9 +308,9 @@ template <typename IO>
 constexpr int kBlock = sizeof(IO) == 2 ? 64 : 32;
 
 // What the walks of the backward write: X or dU of every token, float32
-// [cell][T][dv], and the state (its gradient) at each block's start (end) as operand
-// fragments [cell][block][32 columns][16 rows][part]: slot e of lane group g4 is column
-// 8 g4 + e, lane l16 of tile 2 kk + u row 32 kk + 8 (l16 / 4) + 4 u + l16 % 4.
+// [cell][T][dv], and the state (its gradient) at each block's start (end), float32 in the
+// order of operands [cell][block][32 columns][16 rows][lane][8]: slot e of lane group
+// g4 is column 8 g4 + e, lane l16 of tile 2 kk + u row 32 kk + 8 (l16 / 4) + 4 u + l16 % 4.
 struct WalkOut {
     float *rows;
     char *states;
@@ -305,7 +330,7 @@ struct Cfg {
     static constexpr int REC = Rec<IO, W>::BYTES / (int)sizeof(IO);  // elements of a record
     static constexpr size_t TILE = ((size_t)L * TROW + REC) * sizeof(IO), VTILE = VOWN ? (size_t)L * BV * sizeof(IO) : 0;
     static constexpr int NBUF = 2 * TILE + VTILE <= kLds ? 2 : 1;
-    static constexpr int PER_CU = 2 * (NBUF * TILE + VTILE) <= kLds && NW == 4 ? 2 : 1;  // workgroups of a compute unit
+    static constexpr int PER_CU = 2 * (NBUF * TILE + VTILE) <= kLds && NW == 4 && DKP * NCT < 512 ? 2 : 1;  // workgroups of a compute unit
     static_assert(QG >= 8, "swizzle");
     static_assert(TILE + VTILE <= kLds, "LDS");
 };
@@ -467,40 +492,73 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW, W>::PER_CU * NW / 4
             wait_vm<NST>();  // this wavefront's copies have landed
         }
         __syncthreads();
-        if (NBUF == 2) load(next, c + STEP);
         const int nc = count(c);
         const IO *Qs = cur, *Ks = Qs + L * C::KOFF;
         const char *rc = (const char *)(cur + L * C::TROW);
         const float *vec = (const float *)(rc + R::VEC);
-        Frag vf[NCT];
+        // Each step's LDS reads are issued a step ahead of the products that use them, and
+        // so are the parts of S; sched_barrier keeps the steps apart.  V is read before the
+        // next copies begin: the compiler waits for those ahead of this read.
+        Frag vf[NCT], q[2][2], k[2][2], xf[2][NCT][SP];
+        auto parts = [&](int kk) {
+#pragma unroll
+            for (int bt = 0; bt < NCT; ++bt) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = X[2 * kk + (e >> 2)][bt][e & 3];
+                split8<SP>(x, xf[kk & 1][bt]);
+            }
+        };
 #pragma unroll
         for (int bt = 0; bt < NCT; ++bt)
             vf[bt] = C::VOWN ? v_frag<16 * NCT>((const IO *)own, 4 * bt, 4 * NCT, l16, g4)
                              : v_frag<BV>(cur + L * (C::KOFF + DKP), vc0 + 4 * bt, 8, l16, g4);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            if constexpr (W == FORWARD) q[0][t] = rows.get(Qs, t, 0);
+            k[0][t] = rows.get(Ks, t, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (NBUF == 2) load(next, c + STEP);
+        parts(0);
+        __builtin_amdgcn_sched_barrier(0);
         // the state is kept: X[dk][dv] of the accumulators, transposed by the unit matrix
         const bool keep = W == STATES ? c % PER == 0 : W == BACK ? c % PER == PER - 1 || c == nch - 1 : false;
         char *kept = W == FORWARD ? nullptr
-                                  : to.states + ((((size_t)bh * nblk + c / PER) * ncb + ((col0 + vc0) >> 5)) * NAT) * OP * R::FRAG;
+                                  : to.states + ((((size_t)bh * nblk + c / PER) * ncb + ((col0 + vc0) >> 5)) * NAT) * 2048;
         // K S (lane: column, tokens 16 t + 4 g4 + r) and S^T Q^T (lane: token, columns)
         f32x4 KS[2][NCT], O[2][NCT];
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int bt = 0; bt < NCT; ++bt) KS[t][bt] = O[t][bt] = f32x4{0, 0, 0, 0};
+        Frag tf[2][R::TP], pf[2][R::PP > 0 ? R::PP : 1], kf[2][2], qf[2][2];
+        f32x4 eg[2], rest[2], be[2];
 #pragma unroll
         for (int kk = 0; kk < NKS; ++kk) {
-            Frag q[2], k[2], xf[NCT][SP];
+            const int u = kk & 1;
+            __builtin_amdgcn_sched_barrier(0);
+            if (kk + 1 < NKS) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if constexpr (W == FORWARD) q[t] = rows.get(Qs, t, kk);
-                k[t] = rows.get(Ks, t, kk);
-            }
+                for (int t = 0; t < 2; ++t) {
+                    if constexpr (W == FORWARD) q[u ^ 1][t] = rows.get(Qs, t, kk + 1);
+                    k[u ^ 1][t] = rows.get(Ks, t, kk + 1);
+                }
+                parts(kk + 1);
+            } else {
+                // the inverse, the scores of BACK, the tokens' factors
 #pragma unroll
-            for (int bt = 0; bt < NCT; ++bt) {
-                float x[8];
+                for (int t = 0; t < 2; ++t) {
+                    eg[t] = *(const f32x4 *)(vec + R::EG * L + 16 * t + 4 * g4);
+                    rest[t] = *(const f32x4 *)(vec + R::REST * L + 16 * t + 4 * g4);
+                    be[t] = *(const f32x4 *)(vec + R::BETA * L + 16 * t + 4 * g4);
+                    if constexpr (W == BACK)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = X[2 * kk + (e >> 2)][bt][e & 3];
-                split8<SP>(x, xf[bt]);
+                        for (int p = 0; p < SP; ++p)
+                            pf[t][p] = *(const Frag *)(rc + R::P + (t * R::PP + p) * R::FRAG + lane * sizeof(Frag));
+#pragma unroll
+                    for (int p = 0; p < SP; ++p) tf[t][p] = *(const Frag *)(rc + (t * R::TP + p) * R::FRAG + lane * sizeof(Frag));
+                }
             }
 #pragma unroll
             for (int p = SP - 1; p >= 0; --p)
@@ -508,35 +566,23 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW, W>::PER_CU * NW / 4
                 for (int bt = 0; bt < NCT; ++bt)
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        KS[t][bt] = mfma(k[t], xf[bt][p], KS[t][bt]);
-                        if (W == FORWARD && p < OP) O[t][bt] = mfma(xf[bt][p], q[t], O[t][bt]);
+                        KS[t][bt] = mfma(k[u][t], xf[u][bt][p], KS[t][bt]);
+                        if (W == FORWARD && p < OP) O[t][bt] = mfma(xf[u][bt][p], q[u][t], O[t][bt]);
                     }
             if (W != FORWARD && keep && col0 + (vc0 & ~31) < dv)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
+                    const int u2 = kk & 1;
                     Frag unit = {};
 #pragma unroll
                     for (int e = 0; e < 8; ++e) unit[e] = (IO)(8 * g4 + e == 8 * (l16 >> 2) + 4 * u + (l16 & 3) ? 1.0f : 0.0f);
+                    char *at = kept + (2 * kk + u) * 2048 + lane * 32;
 #pragma unroll
-                    for (int p = 0; p < OP; ++p) {
-                        char *at = kept + ((2 * kk + u) * OP + p) * R::FRAG + lane * sizeof(Frag);
-                        f32x4 y[NCT];
+                    for (int bt = 0; bt < NCT; ++bt) {
+                        f32x4 y = {0, 0, 0, 0};  // the parts' sum is exact
 #pragma unroll
-                        for (int bt = 0; bt < NCT; ++bt) y[bt] = mfma(xf[bt][p], unit, f32x4{0, 0, 0, 0});
-                        if constexpr (ES == 4) {
-#pragma unroll
-                            for (int bt = 0; bt < NCT; ++bt) *(f32x4 *)(at + (NCT == 2 ? 16 * bt : 16 * (wave & 1))) = y[bt];
-                        } else {
-                            const f32x4 a0 = y[0], a1 = y[NCT - 1];
-                            const float z[8] = {a0[0], a0[1], a0[2], a0[3], a1[0], a1[1], a1[2], a1[3]};
-                            bf16x8 f;
-                            pack(z, f);
-                            const u32x4 w4 = __builtin_bit_cast(u32x4, f);
-                            if constexpr (NCT == 2)
-                                *(u32x4 *)at = w4;
-                            else
-                                *(u32x2 *)(at + 8 * (wave & 1)) = u32x2{w4[0], w4[1]};
-                        }
+                        for (int p = SP - 1; p >= 0; --p) y = mfma(xf[u2][bt][p], unit, y);
+                        *(f32x4 *)(at + (NCT == 2 ? 16 * bt : 16 * (wave & 1))) = y;
                     }
                 }
         }
@@ -547,20 +593,15 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW, W>::PER_CU * NW / 4
             __builtin_amdgcn_sched_barrier(0);
             load_v(c + STEP);
         }
-        Frag tf[2][R::TP], pf[2][R::PP > 0 ? R::PP : 1];
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
+            if constexpr (W == FORWARD)
 #pragma unroll
-            for (int p = 0; p < SP; ++p) tf[t][p] = *(const Frag *)(rc + (t * R::TP + p) * R::FRAG + lane * sizeof(Frag));
-#pragma unroll
-            for (int p = 0; p < R::PP; ++p) pf[t][p] = *(const Frag *)(rc + R::P + (t * R::PP + p) * R::FRAG + lane * sizeof(Frag));
-        }
-        f32x4 eg[2], rest[2], be[2];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            eg[t] = *(const f32x4 *)(vec + R::EG * L + 16 * t + 4 * g4);
-            rest[t] = *(const f32x4 *)(vec + R::REST * L + 16 * t + 4 * g4);
-            be[t] = *(const f32x4 *)(vec + R::BETA * L + 16 * t + 4 * g4);
+                for (int p = 0; p < R::PP; ++p)
+                    pf[t][p] = *(const Frag *)(rc + R::P + (t * R::PP + p) * R::FRAG + lane * sizeof(Frag));
+            kf[0][t] = cols.get(Ks, 0, t);
+            if constexpr (W == BACK) qf[0][t] = cols.get(Qs, 0, t);
         }
         const auto own_rows = __builtin_amdgcn_make_buffer_rsrc(
             (void *)(to.rows + ((size_t)bh * a.T + (size_t)c * L) * dv), 0,
@@ -629,23 +670,30 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW, W>::PER_CU * NW / 4
         // state update
         const float decay = vec[R::EG * L + L - 1];
 #pragma unroll
-        for (int kk = 0; kk < NKS; ++kk)
+        for (int kk = 0; kk < NKS; ++kk) {
+            const int u = kk & 1;
+            __builtin_amdgcn_sched_barrier(0);
+            if (kk + 1 < NKS)
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const Frag kf = cols.get(Ks, kk, t);
-                Frag qf;
-                if constexpr (W == BACK) qf = cols.get(Qs, kk, t);
-#pragma unroll
-                for (int bt = 0; bt < NCT; ++bt) {
-                    f32x4 x = X[2 * kk + t][bt] * decay;
-#pragma unroll
-                    for (int p = SP - 1; p >= 0; --p) {
-                        x = mfma(kf, wf[bt][p], x);
-                        if constexpr (W == BACK) x = mfma(qf, gf[bt][p], x);
-                    }
-                    X[2 * kk + t][bt] = x;
+                for (int t = 0; t < 2; ++t) {
+                    kf[u ^ 1][t] = cols.get(Ks, kk + 1, t);
+                    if constexpr (W == BACK) qf[u ^ 1][t] = cols.get(Qs, kk + 1, t);
                 }
-            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int bt = 0; bt < NCT; ++bt) X[2 * kk + t][bt] *= decay;
+#pragma unroll
+            for (int p = SP - 1; p >= 0; --p)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int bt = 0; bt < NCT; ++bt) {
+                        f32x4 &x = X[2 * kk + t][bt];
+                        x = mfma(kf[u][t], wf[bt][p], x);
+                        if constexpr (W == BACK) x = mfma(qf[u][t], gf[bt][p], x);
+                    }
+        }
         if constexpr (W == FORWARD) {
             const auto os = __builtin_amdgcn_make_buffer_rsrc((void *)(og + (size_t)c * L * ldo), 0,
                                                               __builtin_amdgcn_readfirstlane(nc * ldo * ES), kBuf);
@@ -718,16 +766,22 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW, W>::PER_CU * NW / 4
 //   dQ = scale e^G o (do S^T) + E1 K,
 //   dK = e^{G_L - G} o (U D^T) - e^G o (dV S^T) + E1^T Q - E2 K - E2^T K,
 //   dbeta_i = dU_i . X_i,
-//   dg_i = sum_{j >= i} (q.dq + k.dk - 2 beta dbeta)_j + <D, S_L>,
+//   dg_i = sum_{j >= i} (do.o - dV.v)_j + <D, S_L>,
+//   (do.o)_i = scale e^{G_i} q_i . (S do_i) + sum_j E1_ij (q_i . k_j),
 //   <D, S_L> = e^{G_L} <D, S> + sum_j k_j . (e^{G_L - G} o (U D^T))_j.
 // The last sum is the decays' share of everything behind a token: it is exact, and
 // starts anew at each block, so that its roundings do not add up over a sequence.
 //
+// Roundings (bfloat16 I/O): dq and dk are rounded once at the end, and what makes them
+// has two parts, as in the forward; dbeta and dlog_decay are float32, and so what makes
+// them (X and dU themselves, three parts of S, D and X) has 24 bits.
+//
 // A workgroup has a block of kBlock tokens of one head of q and k and walks the
-// heads of v that share it.  A wavefront owns 16 RTW columns of d_qk for all tokens:
-// S and D come to it as operands straight from memory; do, X and dU are split once, by the
-// wavefront of their 16 tokens, and shared through LDS.  Everything is computed
-// transposed (lane: token, rows: d_qk), so that rows leave in whole vectors.
+// heads of v that share it (SHARED: more than one).  A wavefront owns 16 RTW columns of
+// d_qk for all tokens: S and D come to it in operand order straight from memory; do, X
+// and dU are split once, by the wavefront of their 16 tokens, and shared through LDS.
+// Everything is computed transposed (lane: token, rows: d_qk), so that rows leave in
+// whole vectors.
 struct GradIn {
     const float *x, *du;
     const char *s, *d;
@@ -737,12 +791,12 @@ template <typename IO, int DKP_, int NW_>
 struct GCfg {
     static constexpr int DKP = DKP_, NW = NW_, NTH = 64 * NW_;
     static constexpr int SC = kBlock<IO>, NT = SC / 16, NAT = DKP / 16, RTW = NAT / NW;  // tokens and their tiles; tiles of d_qk
-    static constexpr int NG = NW / NT, CB = NG > 2 ? NG : 2;  // wavefronts of 16 tokens, 32-column blocks of a stage
-    static constexpr int OP = Types<IO>::XPARTS, NM = 1 + 2 * OP;
+    static constexpr int CB = NW / NT;                                         // 32-column blocks of a stage, one a wavefront
+    static constexpr int OP = Types<IO>::XPARTS, SP = sizeof(IO) == 2 ? 3 : 1, NM = 1 + SP + OP;
     static constexpr int EPG = Types<IO>::EPG, QG = DKP / EPG, EG = SC / EPG;  // granules of a row of K, of E
     static constexpr int OPS = CB * NT * NM * 512, ES = 2 * OP * SC * SC;      // elements of a stage, of E1 and E2
     static constexpr int POOL = OPS > ES ? OPS : ES;
-    static_assert(NG >= 1 && EG >= 8 && RTW >= 1, "layout");
+    static_assert(CB >= 1 && EG >= 8 && RTW >= 1, "layout");
 };
 
 // slots of row `row` of a swizzled [SC][SC] matrix in the 32 columns of block jb
@@ -790,18 +844,18 @@ __device__ __forceinline__ void store4(IO *p, const float *x) {
     *(vec *)p = v;
 }
 
-template <typename IO, int DKP, int NW>
-__global__ __launch_bounds__(64 * NW, 2) void grad_kernel(DeltaArgs a, GradIn in) {
+template <typename IO, int DKP, int NW, bool SHARED>
+__global__ __launch_bounds__(64 * NW, SHARED && NW == 4 ? 1 : 2) void grad_kernel(DeltaArgs a, GradIn in) {
     using C = GCfg<IO, DKP, NW>;
     using Frag = typename Types<IO>::Frag;
-    constexpr int SC = C::SC, NT = C::NT, NAT = C::NAT, RTW = C::RTW, NG = C::NG, CB = C::CB, OP = C::OP, NM = C::NM;
-    constexpr int QG = C::QG, EPG = C::EPG, FRAG = 64 * (int)sizeof(Frag);
+    constexpr int SC = C::SC, NT = C::NT, NAT = C::NAT, RTW = C::RTW, CB = C::CB, OP = C::OP, SP = C::SP, NM = C::NM;
+    constexpr int QG = C::QG, EPG = C::EPG;
     __shared__ __attribute__((aligned(16))) IO kt[SC * DKP], qt[SC * DKP];
     __shared__ __attribute__((aligned(16))) IO pool[C::POOL];
-    __shared__ __attribute__((aligned(16))) float hi[SC], lo[SC], be[SC], eg[SC], rest[SC], db[SC];
-    __shared__ float part[2][NW][SC], dots[NW];
+    __shared__ __attribute__((aligned(16))) float hi[SC], lo[SC], be[SC], eg[SC], rest[SC];
+    __shared__ float dbs[CB][SC], dgs[CB][SC], eqk[SC], part[2][NW][SC], dots[NW];
 
-    const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g4 = lane >> 4;
+    const int tid = threadIdx.x, lane0 = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const long long nblk = (chunks(a.T) * L + SC - 1) / SC;
     const int blk = (int)(blockIdx.x % nblk), bk = (int)(blockIdx.x / nblk), b = bk / a.Hk, hk = bk % a.Hk;
@@ -843,18 +897,38 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(DeltaArgs a, GradIn in
             *(u32x4 *)(qt + at) = y;
         }
     }
-    Cols<QG> cols;
-    cols.init((const IO *)nullptr, l16, g4);
-    f32x4 tq[RTW][NT], tk[RTW][NT];
+    f32x4 tq[SHARED ? RTW : 1][SHARED ? NT : 1], tk[SHARED ? RTW : 1][SHARED ? NT : 1];
+    if constexpr (SHARED)
 #pragma unroll
-    for (int i = 0; i < RTW; ++i)
+        for (int i = 0; i < RTW; ++i)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) tq[i][t] = tk[i][t] = f32x4{0, 0, 0, 0};
-    const int rt = wave % NT, gq = wave / NT;  // this wavefront's 16 tokens where it splits and scores
-    const bool mine1 = gq == 0, mine2 = gq == (NG > 1 ? 1 : 0);
+            for (int t = 0; t < NT; ++t) tq[i][t] = tk[i][t] = f32x4{0, 0, 0, 0};
+    // this wavefront's 16 tokens and block of a stage's columns where it splits, and whether
+    // it makes E1 or E2 of those tokens (both if no other has the same tokens)
+    const int rt = wave % NT, gq = wave / NT;
+    const bool mine1 = gq == 0, mine2 = gq == (CB > 1 ? 1 : 0);
+    auto put_rows = [&](int t, int x, f32x4 q, f32x4 k) {
+        const int id = wave * RTW + x, c = 32 * (id >> 1) + 8 * (lane0 >> 4) + 4 * (id & 1), i = 16 * t + (lane0 & 15);
+        if (i < rows && c < dk) {
+            const float u[4] = {q[0], q[1], q[2], q[3]}, v[4] = {k[0], k[1], k[2], k[3]};
+            store4(dqg + i * a.sdq.s2 + c, u);
+            store4(dkg + i * a.sdk.s2 + c, v);
+        }
+    };
 
-    for (int h = hk * per; h < (hk + 1) * per; ++h) {
+    for (int h = hk * per, end = SHARED ? h + per : h + 1; h < end; ++h) {
         const size_t cell = (size_t)b * a.H + h;
+        // `fresh`: the addresses made from it are not kept over the heads
+        const int lane = SHARED ? fresh(lane0) : lane0, l16 = lane & 15, g4 = lane >> 4;
+        Cols<QG> cols;
+        Rows<QG> krows;
+        cols.init((const IO *)nullptr, l16, g4);
+        krows.init((const IO *)nullptr, l16, g4);
+        // element (token 16 t + l16, columns of tile x) of K and Q in LDS
+        auto at_row = [&](int t, int x) {
+            const int id = wave * RTW + x, c = 32 * (id >> 1) + 8 * g4 + 4 * (id & 1);
+            return ((16 * t + l16) * QG + ((c / EPG) ^ swz<QG>(l16))) * EPG + c % EPG;
+        };
         __syncthreads();
         if (tid < 64) {
             // gates of the block's tokens
@@ -887,127 +961,170 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(DeltaArgs a, GradIn in
             for (int i = 0; i < RTW; ++i) aq[i][t] = ak1[i][t] = ak2[i][t] = f32x4{0, 0, 0, 0};
         }
         const int tok = 16 * rt + l16;
-        const float *xr = in.x + (cell * a.T + s0 + tok) * dv, *ur = in.du + (cell * a.T + s0 + tok) * dv;
-        const IO *gr = (const IO *)a.d_o + b * a.sdo.s0 + h * a.sdo.s1 + (s0 + tok) * a.sdo.s2;
-        IO *vr = (IO *)a.dvv + b * a.sdv.s0 + h * a.sdv.s1 + (s0 + tok) * a.sdv.s2;
-        const char *sp = in.s + (cell * nblk + blk) * ncb * NAT * OP * FRAG + lane * sizeof(Frag);
-        const char *dp = in.d + (cell * nblk + blk) * ncb * NAT * OP * FRAG + lane * sizeof(Frag);
-        float dot = 0.0f;
+        // uniform bases, 32-bit offsets of this lane's row (a block spans less than 2^30 bytes)
+        const float *xr = in.x + (cell * a.T + s0) * dv, *ur = in.du + (cell * a.T + s0) * dv;
+        const IO *gr = (const IO *)a.d_o + b * a.sdo.s0 + h * a.sdo.s1 + s0 * a.sdo.s2;
+        const IO *ir = (const IO *)a.v + b * a.sv.s0 + h * a.sv.s1 + s0 * a.sv.s2;
+        IO *vr = (IO *)a.dvv + b * a.sdv.s0 + h * a.sdv.s1 + s0 * a.sdv.s2;
+        const unsigned xo = tok * dv, gof = tok * (int)a.sdo.s2, io = tok * (int)a.sv.s2, vo = tok * (int)a.sdv.s2;
+        const float *sp = (const float *)in.s + (cell * nblk + blk) * ncb * NAT * 512 + wave * RTW * 512;
+        const float *dp = (const float *)in.d + (cell * nblk + blk) * ncb * NAT * 512 + wave * RTW * 512;
+        const float bt = be[tok];
+        float dot = 0.0f, xu = 0.0f, vu = 0.0f;
+        // rows of this wavefront's tokens in the next stage's block of columns
+        Frag go, vi;
+        f32x8 xn, un;
+        auto fetch = [&](int base) {
+            const unsigned c0 = 32 * (base + gq) + 8 * g4;
+            const bool ok = tok < n && (int)c0 < dv;
+            go = row8(gr + (gof + c0), ok);
+            vi = row8(ir + (io + c0), ok);
+            xn = row8(xr + (xo + c0), ok);
+            un = row8(ur + (xo + c0), ok);
+        };
+        fetch(0);
         for (int base = 0; base < ncb; base += CB) {
+            // S and D of this stage's first block are on their way while the rows are split
+            f32x8 sn[RTW], dn[RTW];
+            auto fetch_states = [&](int cb) {
+#pragma unroll
+                for (int i = 0; i < RTW; ++i) {
+                    sn[i] = row8(sp + cb * NAT * 512 + i * 512 + lane * 8, true);
+                    dn[i] = row8(dp + cb * NAT * 512 + i * 512 + lane * 8, true);
+                }
+            };
+            fetch_states(base);
             if (base > 0) __syncthreads();
-            // operands of CB blocks of columns: do, parts of X, parts of dU; dv on the way
+            if (base + gq < ncb) {
+                const unsigned c0 = 32 * (base + gq) + 8 * g4;
+                float y[8], z[8], w[8];
 #pragma unroll
-            for (int j = 0; j < CB / NG; ++j) {
-                const int cbl = gq + j * NG, c0 = 32 * (base + cbl) + 8 * g4;
-                if (base + cbl < ncb) {
-                    const bool ok = tok < n && c0 < dv;
-                    const Frag go = row8(gr + c0, ok);
-                    const f32x8 x = row8(xr + c0, ok), u = row8(ur + c0, ok);
-                    float y[8], z[8], w[8];
+                for (int e = 0; e < 8; ++e) {
+                    y[e] = xn[e];
+                    z[e] = un[e];
+                    w[e] = un[e] * bt;
+                    xu += un[e] * xn[e];
+                    vu += w[e] * (float)vi[e];
+                }
+                Frag *to = (Frag *)pool + (size_t)(gq * NT + rt) * NM * 64 + lane;
+                Frag fx[SP], fu[OP];
+                split8<SP>(y, fx);
+                split8<OP>(z, fu);
+                to[0] = go;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        y[e] = x[e];
-                        z[e] = u[e];
-                        w[e] = u[e] * be[tok];
-                    }
-                    Frag *to = (Frag *)pool + (size_t)(cbl * NT + rt) * NM * 64 + lane;
-                    Frag fx[OP], fu[OP];
-                    split8<OP>(y, fx);
-                    split8<OP>(z, fu);
-                    to[0] = go;
+                for (int p = 0; p < SP; ++p) to[(1 + p) * 64] = fx[p];
 #pragma unroll
-                    for (int p = 0; p < OP; ++p) {
-                        to[(1 + p) * 64] = fx[p];
-                        to[(1 + OP + p) * 64] = fu[p];
-                    }
-                    if (tok < rows && c0 < dv) {
-                        store4(vr + c0, w);
-                        store4(vr + c0 + 4, w + 4);
-                    }
+                for (int p = 0; p < OP; ++p) to[(1 + SP + p) * 64] = fu[p];
+                if (tok < rows && (int)c0 < dv) {
+                    store4(vr + (vo + c0), w);
+                    store4(vr + (vo + c0 + 4), w + 4);
                 }
             }
             __syncthreads();
-#pragma unroll
-            for (int cbl = 0; cbl < CB; ++cbl) {
-                if (base + cbl >= ncb) break;
+            if (base + CB < ncb) fetch(base + CB);
+            for (int cbl = 0; cbl < CB && base + cbl < ncb; ++cbl) {
                 const Frag *op = (const Frag *)pool + (size_t)cbl * NT * NM * 64 + lane;
-                Frag sf[RTW][OP], df[RTW][OP];
+                if (cbl > 0) fetch_states(base + cbl);
+                // first all products with S and the scores, then those with D: the parts of one in
+                // registers at a time
+                Frag f[RTW][SP];
 #pragma unroll
-                for (int i = 0; i < RTW; ++i)
+                for (int i = 0; i < RTW; ++i) {
+                    float x[8];
 #pragma unroll
-                    for (int p = 0; p < OP; ++p) {
-                        const size_t off = ((size_t)((base + cbl) * NAT + wave * RTW + i) * OP + p) * FRAG;
-                        sf[i][p] = *(const Frag *)(sp + off);
-                        df[i][p] = *(const Frag *)(dp + off);
+                    for (int e = 0; e < 8; ++e) {
+                        x[e] = sn[i][e];
+                        dot += sn[i][e] * dn[i][e];
                     }
+                    split8<SP>(x, f[i]);
+                }
                 // scores of this wavefront's tokens i (lanes) with all tokens j <= i (rows)
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
                     if (t <= rt) {
-                        Frag fx[OP];
-#pragma unroll
-                        for (int p = 0; p < OP; ++p) fx[p] = op[(t * NM + 1 + p) * 64];
+                        __builtin_amdgcn_sched_barrier(0);  // keeps the operands of one tile in registers, not of all
                         if (mine1) {
-                            const Frag go = op[rt * NM * 64];
+                            const Frag g = op[rt * NM * 64];
 #pragma unroll
-                            for (int p = OP - 1; p >= 0; --p) e1[t] = mfma(fx[p], go, e1[t]);
+                            for (int p = SP - 1; p >= 0; --p) e1[t] = mfma(op[(t * NM + 1 + p) * 64], g, e1[t]);
                         }
                         if (mine2) {
-                            Frag fu[OP];
+                            Frag fx[OP], fu[OP];
 #pragma unroll
-                            for (int p = 0; p < OP; ++p) fu[p] = op[(rt * NM + 1 + OP + p) * 64];
+                            for (int p = 0; p < OP; ++p) {
+                                fx[p] = op[(t * NM + 1 + p) * 64];
+                                fu[p] = op[(rt * NM + 1 + SP + p) * 64];
+                            }
                             e2[t] = mfma_parts<OP>(fx, fu, e2[t]);
                         }
                     }
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    const Frag go = op[t * NM * 64];
-                    Frag fx[OP], fu[OP];
+                    __builtin_amdgcn_sched_barrier(0);
+                    const Frag g = op[t * NM * 64];
+                    Frag fu[OP];
 #pragma unroll
-                    for (int p = 0; p < OP; ++p) {
-                        fx[p] = op[(t * NM + 1 + p) * 64];
-                        fu[p] = op[(t * NM + 1 + OP + p) * 64];
-                    }
+                    for (int p = 0; p < OP; ++p) fu[p] = op[(t * NM + 1 + SP + p) * 64];
 #pragma unroll
                     for (int i = 0; i < RTW; ++i) {
 #pragma unroll
-                        for (int p = OP - 1; p >= 0; --p) aq[i][t] = mfma(sf[i][p], go, aq[i][t]);
-                        ak1[i][t] = mfma_parts<OP>(df[i], fx, ak1[i][t]);
-                        ak2[i][t] = mfma_parts<OP>(sf[i], fu, ak2[i][t]);
+                        for (int p = SP - 1; p >= 0; --p) aq[i][t] = mfma(f[i][p], g, aq[i][t]);
+                        ak2[i][t] = mfma_parts<OP>(f[i], fu, ak2[i][t]);
                     }
                 }
-                // <D, S>
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int i = 0; i < RTW; ++i)
+                for (int i = 0; i < RTW; ++i) {
+                    float x[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float x = (float)sf[i][0][e], y = (float)df[i][0][e];
-                        if constexpr (OP == 2) {
-                            x += (float)sf[i][1][e];
-                            y += (float)df[i][1][e];
-                        }
-                        dot += x * y;
-                    }
+                    for (int e = 0; e < 8; ++e) x[e] = dn[i][e];
+                    split8<SP>(x, f[i]);
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    Frag fx[SP];
+#pragma unroll
+                    for (int p = 0; p < SP; ++p) fx[p] = op[(t * NM + 1 + p) * 64];
+#pragma unroll
+                    for (int i = 0; i < RTW; ++i) ak1[i][t] = mfma_parts<SP>(f[i], fx, ak1[i][t]);
+                }
             }
         }
+        // the rows' own products: dbeta, and dV.v
+        xu += __shfl_xor(xu, 16);
+        vu += __shfl_xor(vu, 16);
+        xu += __shfl_xor(xu, 32);
+        vu += __shfl_xor(vu, 32);
+        if (g4 == 0) {
+            dbs[gq][tok] = xu;
+            dgs[gq][tok] = -vu;
+        }
         __syncthreads();
-        // ---- E1 and -E2, decayed, to LDS over the operands; dbeta on E2's diagonal
+        // ---- E1 and -E2, decayed, to LDS over the operands; E1's part of do.o on the way
         IO *E1 = pool, *E2 = pool + OP * SC * SC;
         {
             const int i = tok;
-            const float hii = hi[i], loi = lo[i], bi = be[i];
+            const float hii = hi[i], loi = lo[i];
+            float qke = 0.0f;
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 float x[4], y[4];
                 const f32x4 hj = *(const f32x4 *)(hi + 16 * t + 4 * g4), lj = *(const f32x4 *)(lo + 16 * t + 4 * g4);
                 const f32x4 bj = *(const f32x4 *)(be + 16 * t + 4 * g4);
+                f32x4 qk = {0, 0, 0, 0};
+                __builtin_amdgcn_sched_barrier(0);
+                if (mine1 && t <= rt)
+#pragma unroll
+                    for (int kk = 0; kk < DKP / 32; ++kk)
+                        qk = mfma(krows.get(kt + (t >> 1) * 32 * DKP, t & 1, kk), krows.get(qt + (rt >> 1) * 32 * DKP, rt & 1, kk), qk);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int j = 16 * t + 4 * g4 + r;
                     const float M = j <= i ? __builtin_amdgcn_exp2f((hii - hj[r]) + (loi - lj[r])) * bj[r] : 0.0f;
                     x[r] = e1[t][r] * (M * a.scale);
-                    y[r] = j < i ? -e2[t][r] * (M * bi) : 0.0f;
-                    if (mine2 && j == i) db[i] = e2[t][r];
+                    y[r] = j < i ? -e2[t][r] * (M * bt) : 0.0f;
+                    qke += x[r] * qk[r];
                 }
                 const int c = 16 * t + 4 * g4, at = i * SC + (((c / EPG) ^ swz<C::EG>(l16)) * EPG) + c % EPG;
 #pragma unroll
@@ -1025,26 +1142,76 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(DeltaArgs a, GradIn in
                     if (mine2) store4(E2 + p * SC * SC + at, w);
                 }
             }
+            qke += __shfl_xor(qke, 16);
+            qke += __shfl_xor(qke, 32);
+            if (mine1 && g4 == 0) eqk[i] = qke;
         }
-        __syncthreads();
-        // ---- the products with the state, scaled; then those within the block
-        float kd[NT], dG[NT];
+        // ---- the products with the state, scaled; their part of do.o and of <D, S_L>
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const int i = 16 * t + l16;
             const float ei = eg[i], bi = be[i], ri = rest[i];
-            kd[t] = dG[t] = 0.0f;
+            float kd = 0.0f, qo = 0.0f;
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int x = 0; x < RTW; ++x) {
-                const int id = wave * RTW + x, c = 32 * (id >> 1) + 8 * g4 + 4 * (id & 1);
-                const IO *kr = kt + (i * QG + ((c / EPG) ^ swz<QG>(l16))) * EPG + c % EPG;
+                const int at = at_row(t, x);
                 ak1[x][t] *= bi * ri;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) kd[t] += to_f(kr[r]) * ak1[x][t][r];
-                ak1[x][t] -= ak2[x][t] * (bi * ei);
                 aq[x][t] *= a.scale * ei;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    kd += to_f(kt[at + r]) * ak1[x][t][r];
+                    qo += to_f(qt[at + r]) * aq[x][t][r];
+                }
+                ak1[x][t] -= ak2[x][t] * (bi * ei);
+            }
+            kd += __shfl_xor(kd, 16);
+            qo += __shfl_xor(qo, 16);
+            kd += __shfl_xor(kd, 32);
+            qo += __shfl_xor(qo, 32);
+            if (g4 == 0) {
+                part[0][wave][i] = qo;
+                part[1][wave][i] = kd;
             }
         }
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) dot += __shfl_xor(dot, m);
+        if (lane == 0) dots[wave] = dot;
+        __syncthreads();
+        if (tid < 64) {
+            // dlog_decay: sums from each token to the block's end, and what is behind it
+            float x = 0.0f, y = 0.0f, z = 0.0f, tail = 0.0f;
+            const bool ok = lane < n;
+            if (ok) {
+#pragma unroll
+                for (int w = 0; w < NW; ++w) {
+                    x += part[0][w][lane];
+                    y += part[1][w][lane];
+                }
+                x += eqk[lane];
+#pragma unroll
+                for (int w = 0; w < CB; ++w) {
+                    x += dgs[w][lane];
+                    z += dbs[w][lane];
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < NW; ++w) tail += dots[w];
+#pragma unroll
+            for (int m = 1; m < 64; m <<= 1) {
+                const float u = __shfl_down(x, m);
+                if (lane + m < 64) x += u;
+                y += __shfl_xor(y, m);
+            }
+            x += eg[SC - 1] * tail + y;
+            if (lane < rows) {
+                const float g = ok ? a.g[b * a.sg.s0 + h * a.sg.s1 + (s0 + lane) * a.sg.s2] : 0.0f;
+                const bool gone = __builtin_amdgcn_exp2f(gate_log2(g)) == 0.0f;
+                a.dg[b * a.sdg.s0 + h * a.sdg.s1 + (s0 + lane) * a.sdg.s2] = ok && !gone ? x : 0.0f;
+                a.db[b * a.sdb.s0 + h * a.sdb.s1 + (s0 + lane) * a.sdb.s2] = ok ? z : 0.0f;
+            }
+        }
+        // ---- the products within the block
 #pragma unroll
         for (int ib = 0; ib < SC / 32; ++ib) {
             Frag kf[RTW], qf[RTW];
@@ -1059,6 +1226,7 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(DeltaArgs a, GradIn in
 #pragma unroll
                 for (int p = OP - 1; p >= 0; --p) {
                     const IO *m1 = E1 + p * SC * SC, *m2 = E2 + p * SC * SC;
+                    __builtin_amdgcn_sched_barrier(0);
                     if (ib <= t / 2) {
                         const Frag r1 = e_row<C::EG>(m1, 16 * t + l16, ib, g4), r2 = e_row<C::EG>(m2, 16 * t + l16, ib, g4);
 #pragma unroll
@@ -1078,75 +1246,22 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(DeltaArgs a, GradIn in
                 }
         }
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int i = 16 * t + l16;
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int x = 0; x < RTW; ++x) {
-                const int id = wave * RTW + x, c = 32 * (id >> 1) + 8 * g4 + 4 * (id & 1);
-                const int at = (i * QG + ((c / EPG) ^ swz<QG>(l16))) * EPG + c % EPG;
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    dG[t] += to_f(qt[at + r]) * aq[x][t][r] + to_f(kt[at + r]) * ak1[x][t][r];
-                tq[x][t] += aq[x][t];
-                tk[x][t] += ak1[x][t];
-            }
-            kd[t] += __shfl_xor(kd[t], 16);
-            dG[t] += __shfl_xor(dG[t], 16);
-            kd[t] += __shfl_xor(kd[t], 32);
-            dG[t] += __shfl_xor(dG[t], 32);
-            if (g4 == 0) {
-                part[0][wave][i] = dG[t];
-                part[1][wave][i] = kd[t];
-            }
-        }
-#pragma unroll
-        for (int m = 1; m < 64; m <<= 1) dot += __shfl_xor(dot, m);
-        if (lane == 0) dots[wave] = dot;
-        __syncthreads();
-        if (tid < 64) {
-            // dlog_decay: sums from each token to the block's end, and what is behind it
-            float x = 0.0f, y = 0.0f, tail = 0.0f;
-            const bool ok = lane < n;
-            if (ok) {
-#pragma unroll
-                for (int w = 0; w < NW; ++w) {
-                    x += part[0][w][lane];
-                    y += part[1][w][lane];
+                if constexpr (SHARED) {
+                    tq[x][t] += aq[x][t];
+                    tk[x][t] += ak1[x][t];
+                } else {
+                    put_rows(t, x, aq[x][t], ak1[x][t]);
                 }
-                x -= 2.0f * be[lane] * db[lane];
             }
-#pragma unroll
-            for (int w = 0; w < NW; ++w) tail += dots[w];
-#pragma unroll
-            for (int m = 1; m < 64; m <<= 1) {
-                const float z = __shfl_down(x, m);
-                if (lane + m < 64) x += z;
-                y += __shfl_xor(y, m);
-            }
-            x += eg[SC - 1] * tail + y;
-            if (lane < rows) {
-                const float g = ok ? a.g[b * a.sg.s0 + h * a.sg.s1 + (s0 + lane) * a.sg.s2] : 0.0f;
-                const bool gone = __builtin_amdgcn_exp2f(gate_log2(g)) == 0.0f;
-                a.dg[b * a.sdg.s0 + h * a.sdg.s1 + (s0 + lane) * a.sdg.s2] = ok && !gone ? x : 0.0f;
-                a.db[b * a.sdb.s0 + h * a.sdb.s1 + (s0 + lane) * a.sdb.s2] = ok ? db[lane] : 0.0f;
-            }
-        }
     }
-    // ---- rows of dq and dk
+    if constexpr (SHARED)
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const int i = 16 * t + l16;
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int x = 0; x < RTW; ++x) {
-            const int id = wave * RTW + x, c = 32 * (id >> 1) + 8 * g4 + 4 * (id & 1);
-            if (i < rows && c < dk) {
-                const f32x4 q = tq[x][t], k = tk[x][t];
-                const float u[4] = {q[0], q[1], q[2], q[3]}, v[4] = {k[0], k[1], k[2], k[3]};
-                store4(dqg + i * a.sdq.s2 + c, u);
-                store4(dkg + i * a.sdk.s2 + c, v);
-            }
-        }
-    }
+            for (int x = 0; x < RTW; ++x) put_rows(t, x, tq[x][t], tk[x][t]);
 }
 
 // ---- launches
@@ -1156,11 +1271,9 @@ hipError_t launch_shape(const DeltaArgs &a, const char *rec, WalkOut to, hipStre
     const dim3 grid((unsigned)(a.B * a.H * ((a.dv + 16 * NCT * NW - 1) / (16 * NCT * NW))));
     if constexpr (sizeof(IO) == 4)
         delta_kernel<IO, DKP, NCT, NW, 1, W><<<grid, 64 * NW, 0, s>>>(a, rec, to);
-    else if constexpr (W == STATES)
-        delta_kernel<IO, DKP, NCT, NW, 2, W><<<grid, 64 * NW, 0, s>>>(a, rec, to);
-    else if (a.S_T)
+    else if (W != FORWARD || a.S_T)  // all gradients but those in bfloat16 are float32 sums
         delta_kernel<IO, DKP, NCT, NW, 3, W><<<grid, 64 * NW, 0, s>>>(a, rec, to);
-    else
+    else if constexpr (W == FORWARD)
         delta_kernel<IO, DKP, NCT, NW, 2, W><<<grid, 64 * NW, 0, s>>>(a, rec, to);
     return hipGetLastError();
 }
@@ -1173,7 +1286,9 @@ hipError_t launch_walk(const DeltaArgs &a, const char *rec, WalkOut to, hipStrea
         return wide ? launch_shape<IO, 64, 2, 4, W>(a, rec, to, s) : launch_shape<IO, 64, 1, 4, W>(a, rec, to, s);
     if (a.dk <= 128)
         return wide ? launch_shape<IO, 128, 2, 4, W>(a, rec, to, s) : launch_shape<IO, 128, 1, 4, W>(a, rec, to, s);
-    return wide ? launch_shape<IO, 256, BF ? 2 : 1, BF ? 4 : 8, W>(a, rec, to, s) : launch_shape<IO, 256, 1, 4, W>(a, rec, to, s);
+    if constexpr (BF)
+        if (wide) return launch_shape<IO, 256, 2, 4, W>(a, rec, to, s);
+    return launch_shape<IO, 256, 1, 4, W>(a, rec, to, s);
 }
 
 template <typename IO>
@@ -1192,7 +1307,7 @@ template <typename IO>
 BwdWs bwd_ws(size_t cells, int T, int dk, int dv) {
     const size_t nch = (size_t)chunks(T), nblk = (nch * L + kBlock<IO> - 1) / kBlock<IO>;
     const int dkp = dk <= 64 ? 64 : dk <= 128 ? 128 : 256;
-    const size_t states = cells * nblk * ((dv + 31) / 32) * (dkp / 16) * Types<IO>::XPARTS * 64 * sizeof(typename Types<IO>::Frag);
+    const size_t states = cells * nblk * ((dv + 31) / 32) * (dkp / 16) * 2048;
     BwdWs w;
     w.rec = 0;
     w.rec_back = w.rec + cells * nch * Rec<IO, STATES>::BYTES;
@@ -1202,6 +1317,17 @@ BwdWs bwd_ws(size_t cells, int T, int dk, int dv) {
     w.d = w.s + states;
     w.total = w.d + states;
     return w;
+}
+
+template <typename IO, bool SHARED>
+hipError_t launch_grad(const DeltaArgs &a, const GradIn &in, dim3 grid, hipStream_t s) {
+    if (a.dk <= 64)
+        grad_kernel<IO, 64, 4, SHARED><<<grid, 256, 0, s>>>(a, in);
+    else if (a.dk <= 128)
+        grad_kernel<IO, 128, 4, SHARED><<<grid, 256, 0, s>>>(a, in);
+    else
+        grad_kernel<IO, 256, 8, SHARED><<<grid, 512, 0, s>>>(a, in);
+    return hipGetLastError();
 }
 
 template <typename IO>
@@ -1223,13 +1349,7 @@ hipError_t launch_bwd_t(const DeltaArgs &a, hipStream_t s) {
     const GradIn in{(const float *)(ws + w.x), (const float *)(ws + w.du), ws + w.s, ws + w.d};
     const long long nblk = (chunks(a.T) * L + kBlock<IO> - 1) / kBlock<IO>;
     const dim3 grid((unsigned)((long long)a.B * a.Hk * nblk));
-    if (a.dk <= 64)
-        grad_kernel<IO, 64, 4><<<grid, 256, 0, s>>>(a, in);
-    else if (a.dk <= 128)
-        grad_kernel<IO, 128, 4><<<grid, 256, 0, s>>>(a, in);
-    else
-        grad_kernel<IO, 256, 8><<<grid, 512, 0, s>>>(a, in);
-    return hipGetLastError();
+    return a.H == a.Hk ? launch_grad<IO, false>(a, in, grid, s) : launch_grad<IO, true>(a, in, grid, s);
 }
 
 }  // namespace
