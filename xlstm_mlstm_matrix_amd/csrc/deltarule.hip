@@ -316,7 +316,19 @@ struct WalkOut {
     char *states;
 };
 
-template <typename IO, int DKP_, int NCT_, int NW_, Walk W>
+// Segments of a sequence where few heads would leave most of the card idle.  A segment
+// of `len` chunks maps the state before it linearly, S -> M S + b, M [dk x dk] the
+// product of its tokens' e^g (I - beta k k^T).  A first walk (SO, state only) makes b from the zero
+// state and M as dk more columns, those of the unit matrix with v = 0; scan_kernel
+// runs through the segments, and a second walk starts each from its own state.
+// Backwards D -> M^T D + c.
+struct Segs {
+    int count, len;   // count = 1: none
+    float *local;     // [cell][segment][dk][dv + dk]: b and M (the BACK walk: c, [dk][dv])
+    float *state;     // [cell][segment][dk][dv]: the state before (BACK: D behind) a segment
+};
+
+template <typename IO, int DKP_, int NCT_, int NW_, Walk W, bool SO = false>
 struct Cfg {
     static constexpr int DKP = DKP_, NCT = NCT_, NW = NW_, NTH = 64 * NW_;
     static constexpr int BV = 16 * NCT * NW;               // value columns of a workgroup
@@ -325,10 +337,12 @@ struct Cfg {
     static constexpr int QG = DKP / EPG, VG = 16 * NCT / EPG, WG = BV / EPG;  // granules of a row
     // float32: V in one buffer a wavefront, whose columns are its own
     static constexpr bool VOWN = sizeof(IO) == 4;
-    static constexpr int KOFF = W == STATES ? 0 : DKP;      // Q (none in STATES), K, V
+    static constexpr bool HASQ = W == BACK || (W == FORWARD && !SO);
+    static constexpr int KOFF = HASQ ? DKP : 0;             // Q, K, V
     static constexpr int TROW = KOFF + DKP + (VOWN ? 0 : BV);  // elements of a tile for each token
     static constexpr int REC = Rec<IO, W>::BYTES / (int)sizeof(IO);  // elements of a record
-    static constexpr size_t TILE = ((size_t)L * TROW + REC) * sizeof(IO), VTILE = VOWN ? (size_t)L * BV * sizeof(IO) : 0;
+    static constexpr int ELEMS = L * TROW + REC, VELEMS = VOWN ? L * 16 * NCT : 8;
+    static constexpr size_t TILE = (size_t)ELEMS * sizeof(IO), VTILE = VOWN ? (size_t)L * BV * sizeof(IO) : 0;
     static constexpr int NBUF = 2 * TILE + VTILE <= kLds ? 2 : 1;
     static constexpr int PER_CU = 2 * (NBUF * TILE + VTILE) <= kLds && NW == 4 && DKP * NCT < 512 ? 2 : 1;  // workgroups of a compute unit
     static_assert(QG >= 8, "swizzle");
@@ -349,33 +363,34 @@ __device__ __forceinline__ f32x4 mfma_parts(const Frag *x, const Frag *y, f32x4 
 // places of v, S0 and S_T:
 //   dU = T^T (P^T do + e^{G_L - G} o (K D)),  dV = beta o dU,
 //   D <- e^{G_L} D + Q^T (scale e^G o do) - K^T (e^G o dV).
-template <typename IO, int DKP, int NCT, int NW, int SP, Walk W>
-__global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW, W>::PER_CU * NW / 4)) void delta_kernel(DeltaArgs a, const char *rec,
-                                                                                                WalkOut to) {
-    using C = Cfg<IO, DKP, NCT, NW, W>;
+// Workgroup `wg` of `nwg`.  The tiles are two arrays of the kernel, and a loop goes over pairs of
+// chunks: the compiler waits for a copy in flight before any LDS read that may alias it.
+template <typename IO, int DKP, int NCT, int NW, int SP, Walk W, bool SO>
+__device__ __forceinline__ void walk(const DeltaArgs &a, const char *rec, WalkOut to, Segs sg, int wg, int nwg, IO *tile0,
+                                     IO *tile1, IO *vtiles) {
+    using C = Cfg<IO, DKP, NCT, NW, W, SO>;
     using R = Rec<IO, W>;
     using Frag = typename Types<IO>::Frag;
     constexpr int NAT = C::NAT, NKS = C::NKS, QG = C::QG, VG = C::VG, BV = C::BV, NBUF = C::NBUF;
     constexpr int OP = Types<IO>::XPARTS;  // parts of what leads to the output
     constexpr int ES = (int)sizeof(IO);
-    __shared__ __attribute__((aligned(16))) IO tile0[L * C::TROW + C::REC];
-    __shared__ __attribute__((aligned(16))) IO tile1[NBUF == 2 ? L * C::TROW + C::REC : 16];
-    __shared__ __attribute__((aligned(16))) IO vtiles[NW][C::VOWN ? L * 16 * NCT : 8];
+    constexpr bool OUT = W == FORWARD && !SO;  // makes o
 
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g4 = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // the column blocks of a head on one XCD: each XCD has a contiguous run of them
-    const int nwg = gridDim.x, xq = nwg >> 3, xr = nwg & 7, xcd = blockIdx.x & 7;
-    const int logical = xcd * xq + min(xcd, xr) + (blockIdx.x >> 3);
-    const int ntile = (a.dv + BV - 1) / BV;
-    const int tile = logical % ntile, bh = logical / ntile;
+    const int xq = nwg >> 3, xr = nwg & 7, xcd = wg & 7;
+    const int logical = xcd * xq + min(xcd, xr) + (wg >> 3);
+    const int vtile = (a.dv + BV - 1) / BV, ntile = vtile + (SO && W != BACK ? (a.dk + BV - 1) / BV : 0);
+    const int tile = logical % ntile, seg = logical / ntile % sg.count, bh = logical / ntile / sg.count;
     const int b = bh / a.H, h = bh % a.H, hk = h / (a.H / a.Hk);
-    const int dk = a.dk, dv = a.dv, n = tokens(a, b), col0 = tile * BV;
+    const bool unit_cols = SO && tile >= vtile;  // columns of M: those of the unit matrix, v = 0
+    const int dk = a.dk, dv = unit_cols ? dk : a.dv, n = tokens(a, b), col0 = (unit_cols ? tile - vtile : tile) * BV;
     const int ldq = (int)a.sq.s2, ldk = (int)a.sk.s2, ldv = (int)a.sv.s2, ldo = (int)a.so.s2;
     const IO *qg = (const IO *)a.q + b * a.sq.s0 + hk * a.sq.s1;
     const IO *kg = (const IO *)a.k + b * a.sk.s0 + hk * a.sk.s1;
     const IO *vg = (const IO *)a.v + b * a.sv.s0 + h * a.sv.s1 + col0;
-    IO *og = W == FORWARD ? (IO *)a.o + b * a.so.s0 + h * a.so.s1 + col0 : nullptr;
+    IO *og = OUT ? (IO *)a.o + b * a.so.s0 + h * a.so.s1 + col0 : nullptr;
     const char *rg = rec + (long long)bh * chunks(a.T) * R::BYTES;
 
     // ---- state.  Lane (l16, g4) of tile (at, bt) holds rows krow(at) + r of column vcol + 4 bt
@@ -392,8 +407,14 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW, W>::PER_CU * NW / 4
     for (int at = 0; at < NAT; ++at)
 #pragma unroll
         for (int bt = 0; bt < NCT; ++bt) X[at][bt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    if (a.S0) {
-        const auto xs = __builtin_amdgcn_make_buffer_rsrc((void *)(a.S0 + cell), 0, dk * dv * 4, kBuf);
+    const int nch = (n + L - 1) / L, c0 = seg * sg.len, c1 = min(c0 + sg.len, nch);  // this segment's chunks
+    const float *start = W == BACK ? (c1 == nch ? a.S0 : nullptr) : (seg == 0 ? a.S0 : nullptr);
+    if (SO)
+        start = nullptr;
+    else if (sg.count > 1 && c0 < nch)
+        start = (W == BACK ? c1 < nch : seg > 0) ? sg.state + (size_t)seg * dk * dv + (size_t)bh * (sg.count - 1) * dk * dv : start;
+    if (start) {
+        const auto xs = __builtin_amdgcn_make_buffer_rsrc((void *)(start + cell), 0, dk * dv * 4, kBuf);
 #pragma unroll
         for (int at = 0; at < NAT; ++at)
 #pragma unroll
@@ -405,10 +426,17 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW, W>::PER_CU * NW / 4
                         __builtin_amdgcn_raw_buffer_load_b32(xs, off == kOut ? kOut : off + r * dv * 4, 0, 0));
             }
     }
+    if (unit_cols) {
+#pragma unroll
+        for (int at = 0; at < NAT; ++at)
+#pragma unroll
+            for (int bt = 0; bt < NCT; ++bt)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) X[at][bt][r] = krow(at) + r == col0 + vcol + 4 * bt ? 1.0f : 0.0f;
+    }
 
     // ---- chunks.  Rows past a chunk's tokens are out of their descriptor's range:
     // they read as zero and are not written.
-    const int nch = (n + L - 1) / L;
     const int ncb = (dv + 31) >> 5;  // blocks of 32 columns
     const long long nblk = (chunks(a.T) * L + kBlock<IO> - 1) / kBlock<IO>;
     auto count = [&](int c) -> int { return c < 0 ? 0 : max(0, min(L, n - c * L)); };
@@ -436,20 +464,20 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW, W>::PER_CU * NW / 4
     using WGc = std::integral_constant<int, C::WG>;
     constexpr int QPER = 16 * QG > C::NTH ? 16 * QG / C::NTH : 1, WPER = 16 * C::WG > C::NTH ? 16 * C::WG / C::NTH : 1;
     unsigned qoff[QPER], koff[QPER], voff[WPER], ownoff = kOut;
-    if constexpr (W != STATES) copy_offsets(qoff, ldq, dk, QGc{});
+    if constexpr (C::HASQ) copy_offsets(qoff, ldq, dk, QGc{});
     copy_offsets(koff, ldk, dk, QGc{});
     constexpr int VI = L * VG / 64;  // own tile: 64 / VG rows an instruction
     if constexpr (C::VOWN) {
         const int col = NCT == 2 ? vc0 + lane % VG * 4 : vc0 + lane % VG * 8;
-        ownoff = col0 + col < dv ? (unsigned)((lane / VG * ldv + col) * ES) : kOut;
+        ownoff = !unit_cols && col0 + col < dv ? (unsigned)((lane / VG * ldv + col) * ES) : kOut;
     } else {
-        copy_offsets(voff, ldv, dv - col0, WGc{});
+        copy_offsets(voff, ldv, unit_cols ? 0 : dv - col0, WGc{});
     }
     constexpr int NREC = R::BYTES / 1024;
     auto load = [&](IO *t, int c) {
-        if constexpr (W != STATES) copy(t, qg, ldq, qoff, QGc{}, c);
+        if constexpr (C::HASQ) copy(t, qg, ldq, qoff, QGc{}, c);
         copy(t + L * C::KOFF, kg, ldk, koff, QGc{}, c);
-        if constexpr (!C::VOWN) copy(t + L * (C::KOFF + DKP), vg, ldv, voff, WGc{}, c);
+        if constexpr (!C::VOWN) copy(t + L * (C::KOFF + DKP), vg, ldv, voff, WGc{}, c);  // reads nothing for unit columns
         const int bytes = count(c) > 0 ? R::BYTES : 0;
         const auto rs = __builtin_amdgcn_make_buffer_rsrc((void *)(rg + (long long)c * R::BYTES), 0,
                                                           __builtin_amdgcn_readfirstlane(bytes), kBuf);
@@ -460,7 +488,7 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW, W>::PER_CU * NW / 4
                     rs, (lds_ptr *)((char *)(t + L * C::TROW) + (i * NW + wave) * 1024), 16,
                     (unsigned)((i * NW + wave) * 1024 + lane * 16), 0, 0, 0);
     };
-    IO *own = vtiles[wave];
+    IO *own = vtiles + wave * C::VELEMS;
     auto load_v = [&](int c) {
         const int bytes = count(c) * ldv * ES;
         const auto rs = __builtin_amdgcn_make_buffer_rsrc((void *)(vg + (size_t)c * L * ldv), 0,
@@ -479,7 +507,7 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW, W>::PER_CU * NW / 4
     const int ocol = vc0 + 8 * g4;
     const bool ook = col0 + ocol < dv;
     // memory operations of a chunk issued after the next one's copies, 15 of them at most
-    constexpr int NST = W == FORWARD ? 2 * (ES == 4 ? NCT : 1) : 8 * NCT < 15 ? 8 * NCT : 15;
+    constexpr int NST = SO ? 0 : W == FORWARD ? 2 * (ES == 4 ? NCT : 1) : 8 * NCT < 15 ? 8 * NCT : 15;
     constexpr int STEP = W == BACK ? -1 : 1, PER = kBlock<IO> / L;  // chunks of a block
     auto body = [&](IO *cur, IO *next, int c, bool first) {
         if (NBUF == 1) {
@@ -515,7 +543,7 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW, W>::PER_CU * NW / 4
                              : v_frag<BV>(cur + L * (C::KOFF + DKP), vc0 + 4 * bt, 8, l16, g4);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            if constexpr (W == FORWARD) q[0][t] = rows.get(Qs, t, 0);
+            if constexpr (OUT) q[0][t] = rows.get(Qs, t, 0);
             k[0][t] = rows.get(Ks, t, 0);
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -523,8 +551,8 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW, W>::PER_CU * NW / 4
         parts(0);
         __builtin_amdgcn_sched_barrier(0);
         // the state is kept: X[dk][dv] of the accumulators, transposed by the unit matrix
-        const bool keep = W == STATES ? c % PER == 0 : W == BACK ? c % PER == PER - 1 || c == nch - 1 : false;
-        char *kept = W == FORWARD ? nullptr
+        const bool keep = SO ? false : W == STATES ? c % PER == 0 : W == BACK ? c % PER == PER - 1 || c == nch - 1 : false;
+        char *kept = W == FORWARD || SO ? nullptr
                                   : to.states + ((((size_t)bh * nblk + c / PER) * ncb + ((col0 + vc0) >> 5)) * NAT) * 2048;
         // K S (lane: column, tokens 16 t + 4 g4 + r) and S^T Q^T (lane: token, columns)
         f32x4 KS[2][NCT], O[2][NCT];
@@ -541,7 +569,7 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW, W>::PER_CU * NW / 4
             if (kk + 1 < NKS) {
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    if constexpr (W == FORWARD) q[u ^ 1][t] = rows.get(Qs, t, kk + 1);
+                    if constexpr (OUT) q[u ^ 1][t] = rows.get(Qs, t, kk + 1);
                     k[u ^ 1][t] = rows.get(Ks, t, kk + 1);
                 }
                 parts(kk + 1);
@@ -567,9 +595,9 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW, W>::PER_CU * NW / 4
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         KS[t][bt] = mfma(k[u][t], xf[u][bt][p], KS[t][bt]);
-                        if (W == FORWARD && p < OP) O[t][bt] = mfma(xf[u][bt][p], q[u][t], O[t][bt]);
+                        if (OUT && p < OP) O[t][bt] = mfma(xf[u][bt][p], q[u][t], O[t][bt]);
                     }
-            if (W != FORWARD && keep && col0 + (vc0 & ~31) < dv)
+            if (W != FORWARD && !SO && keep && col0 + (vc0 & ~31) < dv)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int u2 = kk & 1;
@@ -596,7 +624,7 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW, W>::PER_CU * NW / 4
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            if constexpr (W == FORWARD)
+            if constexpr (OUT)
 #pragma unroll
                 for (int p = 0; p < R::PP; ++p)
                     pf[t][p] = *(const Frag *)(rc + R::P + (t * R::PP + p) * R::FRAG + lane * sizeof(Frag));
@@ -605,7 +633,7 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW, W>::PER_CU * NW / 4
         }
         const auto own_rows = __builtin_amdgcn_make_buffer_rsrc(
             (void *)(to.rows + ((size_t)bh * a.T + (size_t)c * L) * dv), 0,
-            __builtin_amdgcn_readfirstlane(W == FORWARD ? 0 : nc * dv * 4), kBuf);
+            __builtin_amdgcn_readfirstlane(W == FORWARD || SO ? 0 : nc * dv * 4), kBuf);
         Frag uf[NCT][OP], wf[NCT][SP], gf[NCT][SP];
 #pragma unroll
         for (int bt = 0; bt < NCT; ++bt) {
@@ -631,10 +659,10 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW, W>::PER_CU * NW / 4
 #pragma unroll
                 for (int r = 0; r < 4; ++r) x[4 * t + r] = u[r];
             }
-            if constexpr (W == FORWARD) {
-                split8<OP>(x, uf[bt]);
-            } else {
+            if constexpr (OUT) split8<OP>(x, uf[bt]);
+            if constexpr (W != FORWARD) {
                 const bool ok = col0 + vcol + 4 * bt < dv;
+                if constexpr (!SO)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const int i = 16 * (e >> 2) + 4 * g4 + (e & 3);
@@ -659,7 +687,7 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW, W>::PER_CU * NW / 4
             split8<SP>(x, wf[bt]);
         }
         // output
-        if constexpr (W == FORWARD) {
+        if constexpr (OUT) {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const float fade = vec[R::EG * L + 16 * t + l16] * a.scale;
@@ -694,7 +722,7 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW, W>::PER_CU * NW / 4
                         if constexpr (W == BACK) x = mfma(qf[u][t], gf[bt][p], x);
                     }
         }
-        if constexpr (W == FORWARD) {
+        if constexpr (OUT) {
             const auto os = __builtin_amdgcn_make_buffer_rsrc((void *)(og + (size_t)c * L * ldo), 0,
                                                               __builtin_amdgcn_readfirstlane(nc * ldo * ES), kBuf);
 #pragma unroll
@@ -718,44 +746,197 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW, W>::PER_CU * NW / 4
             }
         }
     };
-    const int first = W == BACK ? nch - 1 : 0;
-    if (nch > 0) {
+    const int nloc = c1 - c0, first = W == BACK ? c1 - 1 : c0;
+    if (nloc > 0) {
         if (NBUF == 2) load(tile0, first);
         if constexpr (C::VOWN) load_v(first);
     }
-    for (int i = 0; i < nch; i += 2) {
+    for (int i = 0; i < nloc; i += 2) {
         body(tile0, tile1, first + STEP * i, i == 0);
-        if (i + 1 < nch) body(NBUF == 2 ? tile1 : tile0, tile0, first + STEP * (i + 1), false);
+        if (i + 1 < nloc) body(NBUF == 2 ? tile1 : tile0, tile0, first + STEP * (i + 1), false);
     }
     wait_vm<0>();  // no copy may still be on its way into LDS when the workgroup ends
 
-    if (a.S_T) {
-        const auto xs = __builtin_amdgcn_make_buffer_rsrc((void *)(a.S_T + cell), 0, dk * dv * 4, kBuf);
+    // the state where it ends: the sequence's, or for the scan this segment's b or column of M
+    const int width = SO && W != BACK ? a.dv + dk : dv;
+    const int last = nch > 0 ? (nch - 1) / sg.len : 0;
+    float *end = SO ? sg.local + ((size_t)bh * sg.count + seg) * dk * width + (unit_cols ? a.dv : 0)
+                    : a.S_T && (W == BACK ? seg == 0 : seg == last) ? a.S_T + cell : nullptr;
+    if (end) {
+        const auto xs = __builtin_amdgcn_make_buffer_rsrc((void *)end, 0, (dk - 1) * width * 4 + dv * 4, kBuf);
 #pragma unroll
         for (int at = 0; at < NAT; ++at)
 #pragma unroll
             for (int bt = 0; bt < NCT; ++bt) {
-                const unsigned off = state_at(at, bt);
+                const int col = col0 + vcol + 4 * bt;
+                const unsigned off = krow(at) < dk && col < dv ? (unsigned)((krow(at) * width + col) * 4) : kOut;
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(X[at][bt][r]), xs,
-                                                          off == kOut ? kOut : off + r * dv * 4, 0, 0);
+                                                          off == kOut ? kOut : off + r * width * 4, 0, 0);
             }
     }
-    if constexpr (W != FORWARD) return;
-    // rows behind the sequence's length
-    constexpr int QPR = BV / 4;  // quads of a row
-    const long long quads = (long long)(a.T - n) * QPR;
-    for (long long e = tid; e < quads; e += C::NTH) {
-        const long long t = n + e / QPR;
-        const int cc = (int)(e % QPR) * 4;
-        if (col0 + cc < dv) {
-            if constexpr (ES == 4)
-                *(f32x4 *)(og + t * ldo + cc) = f32x4{0, 0, 0, 0};
-            else
-                *(u32x2 *)(og + t * ldo + cc) = u32x2{0, 0};
+    if constexpr (OUT) {
+        // rows behind the sequence's length, of this segment's tokens
+        const long long z0 = max((long long)n, (long long)c0 * L);
+        const long long z1 = seg == sg.count - 1 ? a.T : min((long long)a.T, (long long)(c0 + sg.len) * L);
+        constexpr int QPR = BV / 4;  // quads of a row
+        const long long quads = max(z1 - z0, 0ll) * QPR;
+        for (long long e = tid; e < quads; e += C::NTH) {
+            const long long t = z0 + e / QPR;
+            const int cc = (int)(e % QPR) * 4;
+            if (col0 + cc < dv) {
+                if constexpr (ES == 4)
+                    *(f32x4 *)(og + t * ldo + cc) = f32x4{0, 0, 0, 0};
+                else
+                    *(u32x2 *)(og + t * ldo + cc) = u32x2{0, 0};
+            }
         }
     }
+}
+
+template <typename IO, int DKP, int NCT, int NW, int SP, bool SO>
+__global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW, FORWARD, SO>::PER_CU * NW / 4)) void forward_kernel(DeltaArgs a, const char *rec,
+                                                                                                            Segs sg) {
+    using C = Cfg<IO, DKP, NCT, NW, FORWARD, SO>;
+    __shared__ __attribute__((aligned(16))) IO tile0[C::ELEMS];
+    __shared__ __attribute__((aligned(16))) IO tile1[C::NBUF == 2 ? C::ELEMS : 16];
+    __shared__ __attribute__((aligned(16))) IO vtiles[NW * C::VELEMS];
+    walk<IO, DKP, NCT, NW, SP, FORWARD, SO>(a, rec, WalkOut{}, sg, blockIdx.x, gridDim.x, tile0, tile1, vtiles);
+}
+
+// Both walks of the backward, which do not need one another: the first `nback` workgroups are
+// BACK's, the longer one.
+struct BackArgs {
+    DeltaArgs a;              // do, dS_T and dS0 in the places of v, S0 and S_T
+    const char *rec, *rec_back;
+    WalkOut to, to_back;
+    Segs sg, sg_back;
+    int nback;
+    const void *v;            // what the first walk has there
+    Strides sv;
+    const float *S0;
+};
+template <typename IO, int DKP, int NCT, int NW, bool SO>
+__global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW, BACK, SO>::PER_CU * NW / 4)) void back_kernel(BackArgs w) {
+    using C = Cfg<IO, DKP, NCT, NW, BACK, SO>;
+    using S = Cfg<IO, DKP, NCT, NW, STATES, SO>;
+    constexpr int N1 = C::NBUF == 2 ? C::ELEMS : 16, N2 = S::NBUF == 2 ? S::ELEMS : 16, SP = sizeof(IO) == 2 ? 3 : 1;
+    __shared__ __attribute__((aligned(16))) IO tile0[C::ELEMS > S::ELEMS ? C::ELEMS : S::ELEMS];
+    __shared__ __attribute__((aligned(16))) IO tile1[N1 > N2 ? N1 : N2];
+    __shared__ __attribute__((aligned(16))) IO vtiles[NW * C::VELEMS];
+    if ((int)blockIdx.x < w.nback) {
+        walk<IO, DKP, NCT, NW, SP, BACK, SO>(w.a, w.rec_back, w.to_back, w.sg_back, blockIdx.x, w.nback, tile0, tile1, vtiles);
+    } else {
+        DeltaArgs a = w.a;
+        a.v = w.v;
+        a.sv = w.sv;
+        a.S0 = w.S0;
+        a.S_T = nullptr;
+        walk<IO, DKP, NCT, NW, SP, STATES, SO>(a, w.rec, w.to, w.sg, blockIdx.x - w.nback, gridDim.x - w.nback, tile0, tile1, vtiles);
+    }
+}
+
+// The states between segments: S_{s+1} = M_s S_s + b_s, or from the last segment back
+// D_{s-1} = M_s^T D_s + c_s, for 16 columns of a head and a wavefront for each 16 rows;
+// float32 MFMA.  A step is bound by latency: a step's M and b are loaded while the one
+// before is computed, ahead of its stores, whose end a later load's wait includes (8 heads of 128 x 128,
+// 32 segments: 160 us with loads where they are used, 81 with them behind the
+// step's products).
+constexpr int kScanLd = 17;
+template <int DKP, bool REV>
+__device__ __forceinline__ void scan(const DeltaArgs &a, const float *start, Segs fwd, Segs sg, int wg, float (*S)[DKP * kScanLd]) {
+    constexpr int NK = DKP / 16, PK = NK < 8 ? NK : 8;  // 16-row tiles; those of a part of M
+    const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g4 = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int ncol = a.dv / 16, col0 = wg % ncol * 16, bh = wg / ncol, b = bh / a.H;
+    const int dk = a.dk, dv = a.dv;  // both multiples of 16
+    const int nch = (tokens(a, b) + L - 1) / L, nseg = (nch + fwd.len - 1) / fwd.len;
+    const int ld = dv + dk, lda = REV ? dv : ld;
+    // Tiles past d_qk read the last one again, against rows of S that stay zero: branches around
+    // the loads would make the compiler wait for them at once.
+    const bool live = 16 * wave < dk;
+    const int row = live ? 16 * wave : dk - 16;
+    for (int i = tid; i < DKP * 16; i += 64 * NK) {
+        const int r = i / 16, c = i % 16;
+        S[0][r * kScanLd + c] = start && r < dk ? start[((size_t)bh * dk + r) * dv + col0 + c] : 0.0f;
+        S[1][r * kScanLd + c] = 0.0f;
+    }
+    // part p of M's columns (all of them up to 128, else 128 each) of a step, and b
+    auto fetch = [&](int step, int p, f32x4 *m, f32x4 &add) {
+        const int s = max(0, min(nseg - 1, REV ? nseg - 1 - step : step));
+        const float *M = fwd.local + ((size_t)bh * fwd.count + s) * dk * ld + dv;
+        const float *A = (REV ? sg.local + ((size_t)bh * sg.count + s) * dk * dv : M - dv) + col0 + l16;
+        if (p == 0)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) add[r] = A[(row + 4 * g4 + r) * lda];
+#pragma unroll
+        for (int k = 0; k < PK; ++k) {
+            const int k0 = min(16 * (p * PK + k), dk - 16) + 4 * g4;
+            if constexpr (REV) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) m[k][e] = M[(k0 + e) * ld + row + l16];
+            } else {
+                m[k] = *(const f32x4 *)(M + (row + l16) * ld + k0);
+            }
+        }
+    };
+    f32x4 acc[2];
+    auto multiply = [&](const float *from, int p, const f32x4 *m) {
+#pragma unroll
+        for (int k = 0; k < PK; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                acc[e & 1] = __builtin_amdgcn_mfma_f32_16x16x4f32(m[k][e], from[(16 * (p * PK + k) + 4 * g4 + e) * kScanLd + l16],
+                                                                 acc[e & 1], 0, 0, 0);
+    };
+    auto finish = [&](int step, float *to) {
+        float *out = sg.state + ((size_t)bh * sg.count + (REV ? nseg - 2 - step : step + 1)) * dk * dv + col0 + l16;
+        acc[0] += acc[1];
+        if (live)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                to[(row + 4 * g4 + r) * kScanLd + l16] = acc[0][r];
+                out[(row + 4 * g4 + r) * dv] = acc[0][r];
+            }
+        __syncthreads();
+    };
+    f32x4 m0[PK], m1[PK], a0, a1;
+    if (nseg > 1) fetch(0, 0, m0, a0);
+    __syncthreads();
+    for (int step = 0; step + 1 < nseg; ++step) {
+        const float *from = S[step & 1];
+        acc[0] = a0;
+        acc[1] = f32x4{0, 0, 0, 0};
+        if constexpr (NK > PK) {
+            fetch(step, 1, m1, a1);
+            multiply(from, 0, m0);
+            fetch(step + 1, 0, m0, a0);
+            multiply(from, 1, m1);
+            finish(step, S[(step & 1) ^ 1]);
+        } else {
+            // two steps a turn, M in turn in m0 and m1
+            fetch(step + 1, 0, m1, a1);
+            multiply(from, 0, m0);
+            finish(step, S[(step & 1) ^ 1]);
+            if (++step + 1 >= nseg) break;
+            acc[0] = a1;
+            acc[1] = f32x4{0, 0, 0, 0};
+            fetch(step + 1, 0, m0, a0);
+            multiply(S[step & 1], 0, m1);
+            finish(step, S[(step & 1) ^ 1]);
+        }
+    }
+}
+// workgroups from `nfwd` on run backwards
+template <int DKP>
+__global__ __launch_bounds__(4 * DKP) void scan_kernel(DeltaArgs a, const float *start, Segs fwd, const float *start_back,
+                                                               Segs back, int nfwd) {
+    __shared__ float S[2][DKP * kScanLd];
+    if ((int)blockIdx.x < nfwd)
+        scan<DKP, false>(a, start, fwd, fwd, blockIdx.x, S);
+    else
+        scan<DKP, true>(a, start_back, fwd, back, blockIdx.x - nfwd, S);
 }
 
 // ---- the gradients of a block, all blocks at once
@@ -1266,42 +1447,90 @@ __global__ __launch_bounds__(64 * NW, SHARED && NW == 4 ? 1 : 2) void grad_kerne
 
 // ---- launches
 
-template <typename IO, int DKP, int NCT, int NW, Walk W>
-hipError_t launch_shape(const DeltaArgs &a, const char *rec, WalkOut to, hipStream_t s) {
-    const dim3 grid((unsigned)(a.B * a.H * ((a.dv + 16 * NCT * NW - 1) / (16 * NCT * NW))));
-    if constexpr (sizeof(IO) == 4)
-        delta_kernel<IO, DKP, NCT, NW, 1, W><<<grid, 64 * NW, 0, s>>>(a, rec, to);
-    else if (W != FORWARD || a.S_T)  // all gradients but those in bfloat16 are float32 sums
-        delta_kernel<IO, DKP, NCT, NW, 3, W><<<grid, 64 * NW, 0, s>>>(a, rec, to);
-    else if constexpr (W == FORWARD)
-        delta_kernel<IO, DKP, NCT, NW, 2, W><<<grid, 64 * NW, 0, s>>>(a, rec, to);
-    return hipGetLastError();
+// Columns of a workgroup, and segments.  128 columns where that gives every compute unit a
+// workgroup, else 64.  Segments where up to a quarter of the units would have one: they
+// cost a second walk, of twice the columns (d_v and d_qk of them) where d_qk is as large as
+// d_v, and the scan's steps, each longer than a chunk; so as many as make a
+// workgroup a unit, and as sqrt(4 chunks), of at least 4 chunks.
+struct Plan {
+    bool wide;
+    int nseg, len;
+};
+Plan make_plan(size_t cells, int T, int dv) {
+    Plan p;
+    p.wide = cells * ((dv + 127) / 128) >= 256;
+    const long long wgs = (long long)cells * ((dv + 63) / 64), nch = chunks(T);
+    long long want = wgs > 64 ? 1 : 256 / wgs;
+    while (want > 1 && (want * want > 4 * nch || want * 4 > nch)) --want;
+    p.len = (int)((nch + want - 1) / want + 1) / 2 * 2;  // whole blocks of the backward
+    p.nseg = (int)((nch + p.len - 1) / p.len);
+    return p;
 }
 
-template <typename IO, Walk W>
-hipError_t launch_walk(const DeltaArgs &a, const char *rec, WalkOut to, hipStream_t s) {
-    constexpr bool BF = sizeof(IO) == 2;
-    const bool wide = (long long)a.B * a.H * ((a.dv + 127) / 128) >= 256;
-    if (a.dk <= 64)
-        return wide ? launch_shape<IO, 64, 2, 4, W>(a, rec, to, s) : launch_shape<IO, 64, 1, 4, W>(a, rec, to, s);
-    if (a.dk <= 128)
-        return wide ? launch_shape<IO, 128, 2, 4, W>(a, rec, to, s) : launch_shape<IO, 128, 1, 4, W>(a, rec, to, s);
-    if constexpr (BF)
-        if (wide) return launch_shape<IO, 256, 2, 4, W>(a, rec, to, s);
-    return launch_shape<IO, 256, 1, 4, W>(a, rec, to, s);
+// the walk's shape: f(DKP, NCT, NW) as constants
+template <typename IO, typename F>
+hipError_t with_shape(int dk, bool wide, F f) {
+    using std::integral_constant;
+    constexpr integral_constant<int, 1> one{};
+    constexpr integral_constant<int, 2> two{};
+    constexpr integral_constant<int, 4> four{};
+    if (dk <= 64) return wide ? f(integral_constant<int, 64>{}, two, four) : f(integral_constant<int, 64>{}, one, four);
+    if (dk <= 128) return wide ? f(integral_constant<int, 128>{}, two, four) : f(integral_constant<int, 128>{}, one, four);
+    if constexpr (sizeof(IO) == 2)
+        if (wide) return f(integral_constant<int, 256>{}, two, four);
+    return f(integral_constant<int, 256>{}, one, four);
+}
+
+// Workspace of the forward, floats from its start.
+struct FwdWs {
+    size_t rec, local, state, total;
+};
+FwdWs fwd_ws(size_t cells, int T, int dk, int dv, int io_bf16) {
+    const Plan p = make_plan(cells, T, dv);
+    FwdWs w;
+    w.rec = 0;
+    w.local = w.rec + cells * (size_t)chunks(T) * (io_bf16 ? Rec<bf16, FORWARD>::BYTES : Rec<float, FORWARD>::BYTES) / 4;
+    w.state = w.local + (p.nseg > 1 ? cells * p.nseg * dk * (dv + dk) : 0);
+    w.total = w.state + (p.nseg > 1 ? cells * p.nseg * dk * dv : 0);
+    return w;
 }
 
 template <typename IO>
 hipError_t launch_fwd_t(const DeltaArgs &a, hipStream_t s) {
-    char *rec = (char *)a.ws;
-    const long long total = (long long)a.B * a.H * chunks(a.T);
+    constexpr bool BF = sizeof(IO) == 2;
+    const size_t cells = (size_t)a.B * a.H;
+    const FwdWs w = fwd_ws(cells, a.T, a.dk, a.dv, BF);
+    const Plan p = make_plan(cells, a.T, a.dv);
+    char *rec = (char *)(a.ws + w.rec);
+    const long long total = (long long)cells * chunks(a.T);
     prep_kernel<IO, false><<<dim3((unsigned)((total + kPrepWaves - 1) / kPrepWaves)), 64 * kPrepWaves, 0, s>>>(a, rec, nullptr, total);
-    return launch_walk<IO, FORWARD>(a, rec, WalkOut{}, s);
+    const Segs sg{p.nseg, p.len, a.ws + w.local, a.ws + w.state};
+    return with_shape<IO>(a.dk, p.wide, [&](auto dkp, auto nct, auto nw) {
+        constexpr int DKP = decltype(dkp)::value, NCT = decltype(nct)::value, NW = decltype(nw)::value, BV = 16 * NCT * NW;
+        const int vt = (a.dv + BV - 1) / BV, kt = (a.dk + BV - 1) / BV;
+        const auto run = [&](auto parts) {
+            constexpr int SP = decltype(parts)::value;
+            if constexpr (NCT == 1)
+                if (p.nseg > 1) {
+                    forward_kernel<IO, DKP, NCT, NW, SP, true><<<dim3((unsigned)(cells * p.nseg * (vt + kt))), 64 * NW, 0, s>>>(a, rec, sg);
+                    const unsigned n = (unsigned)(cells * (a.dv / 16));
+                    scan_kernel<DKP><<<dim3(n), 4 * DKP, 0, s>>>(a, a.S0, sg, nullptr, Segs{}, (int)n);
+                }
+            forward_kernel<IO, DKP, NCT, NW, SP, false><<<dim3((unsigned)(cells * p.nseg * vt)), 64 * NW, 0, s>>>(a, rec, sg);
+        };
+        if constexpr (!BF)
+            run(std::integral_constant<int, 1>{});
+        else if (a.S_T)
+            run(std::integral_constant<int, 3>{});
+        else
+            run(std::integral_constant<int, 2>{});
+        return hipGetLastError();
+    });
 }
 
 // Workspace of the backward, bytes from its start; every part is a multiple of 16.
 struct BwdWs {
-    size_t rec, rec_back, x, du, s, d, total;
+    size_t rec, rec_back, x, du, s, d, local, state, local_back, state_back, total;
 };
 template <typename IO>
 BwdWs bwd_ws(size_t cells, int T, int dk, int dv) {
@@ -1315,7 +1544,13 @@ BwdWs bwd_ws(size_t cells, int T, int dk, int dv) {
     w.du = w.x + cells * T * dv * 4;
     w.s = w.du + cells * T * dv * 4;
     w.d = w.s + states;
-    w.total = w.d + states;
+    const Plan p = make_plan(cells, T, dv);
+    const size_t one = p.nseg > 1 ? cells * p.nseg * dk * 4 : 0;  // bytes of a column of all segments
+    w.local = w.d + states;
+    w.state = w.local + one * (dv + dk);
+    w.local_back = w.state + one * dv;
+    w.state_back = w.local_back + one * dv;
+    w.total = w.state_back + one * dv;
     return w;
 }
 
@@ -1336,15 +1571,36 @@ hipError_t launch_bwd_t(const DeltaArgs &a, hipStream_t s) {
     const size_t cells = (size_t)a.B * a.H;
     const BwdWs w = bwd_ws<IO>(cells, a.T, a.dk, a.dv);
     const long long total = (long long)cells * chunks(a.T);
+    const Plan p = make_plan(cells, a.T, a.dv);
     prep_kernel<IO, true><<<dim3((unsigned)((total + kPrepWaves - 1) / kPrepWaves)), 64 * kPrepWaves, 0, s>>>(a, ws + w.rec, ws + w.rec_back, total);
-    hipError_t e = launch_walk<IO, STATES>(a, ws + w.rec, WalkOut{(float *)(ws + w.x), ws + w.s}, s);
-    if (e != hipSuccess) return e;
-    DeltaArgs back = a;
-    back.v = a.d_o;
-    back.sv = a.sdo;
-    back.S0 = a.dS_T;
-    back.S_T = a.dS0;
-    e = launch_walk<IO, BACK>(back, ws + w.rec_back, WalkOut{(float *)(ws + w.du), ws + w.d}, s);
+    BackArgs k{};
+    k.a = a;
+    k.a.v = a.d_o;
+    k.a.sv = a.sdo;
+    k.a.S0 = a.dS_T;
+    k.a.S_T = a.dS0;
+    k.v = a.v;
+    k.sv = a.sv;
+    k.S0 = a.S0;
+    k.rec = ws + w.rec;
+    k.rec_back = ws + w.rec_back;
+    k.to = WalkOut{(float *)(ws + w.x), ws + w.s};
+    k.to_back = WalkOut{(float *)(ws + w.du), ws + w.d};
+    k.sg = Segs{p.nseg, p.len, (float *)(ws + w.local), (float *)(ws + w.state)};
+    k.sg_back = Segs{p.nseg, p.len, (float *)(ws + w.local_back), (float *)(ws + w.state_back)};
+    const hipError_t e = with_shape<IO>(a.dk, p.wide, [&](auto dkp, auto nct, auto nw) {
+        constexpr int DKP = decltype(dkp)::value, NCT = decltype(nct)::value, NW = decltype(nw)::value, BV = 16 * NCT * NW;
+        const int vt = (a.dv + BV - 1) / BV, kt = (a.dk + BV - 1) / BV;
+        k.nback = (int)(cells * p.nseg * vt);
+        if constexpr (NCT == 1)
+            if (p.nseg > 1) {
+                back_kernel<IO, DKP, NCT, NW, true><<<dim3((unsigned)(cells * p.nseg * (2 * vt + kt))), 64 * NW, 0, s>>>(k);
+                const unsigned n = (unsigned)(cells * (a.dv / 16));
+                scan_kernel<DKP><<<dim3(2 * n), 4 * DKP, 0, s>>>(a, a.S0, k.sg, a.dS_T, k.sg_back, (int)n);
+            }
+        back_kernel<IO, DKP, NCT, NW, false><<<dim3((unsigned)(2 * cells * p.nseg * vt)), 64 * NW, 0, s>>>(k);
+        return hipGetLastError();
+    });
     if (e != hipSuccess) return e;
     const GradIn in{(const float *)(ws + w.x), (const float *)(ws + w.du), ws + w.s, ws + w.d};
     const long long nblk = (chunks(a.T) * L + kBlock<IO> - 1) / kBlock<IO>;
@@ -1357,7 +1613,7 @@ hipError_t launch_bwd_t(const DeltaArgs &a, hipStream_t s) {
 size_t deltarule_workspace_floats(int B, int Hk, int H, int T, int dk, int dv, int io_bf16, int backward) {
     (void)Hk;
     const size_t n = (size_t)B * H;
-    if (!backward) return n * chunks(T) * (io_bf16 ? Rec<bf16, FORWARD>::BYTES : Rec<float, FORWARD>::BYTES) / 4;
+    if (!backward) return fwd_ws(n, T, dk, dv, io_bf16).total;
     return (io_bf16 ? bwd_ws<bf16>(n, T, dk, dv).total : bwd_ws<float>(n, T, dk, dv).total) / 4;
 }
 
