@@ -243,6 +243,23 @@ def test_long_sequence_of_few_heads(io):
     check(make(io, 1, 1, 2, 1500, 64, 64, seed=11, decay=0.02), io, scale=0.125, what=f"{io} long")
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 1, 1, 700, 240, 32), (1, 1, 3, 600, 96, 176), (2, 1, 2, 530, 16, 64)], ids=str)
+def test_segments(io, shape):
+    """Few heads and many chunks in segments: sizes that fill no tile, lengths that end in
+    every segment, strong and weak decays."""
+    d = make(io, *shape, seed=13, decay=0.01)
+    d["g"][:, -1] *= 30.0
+    T = shape[3]
+    lengths = None if shape[0] == 1 else [T, 97]
+    if lengths is not None:
+        for n in ("q", "k", "v", "do", "g", "beta"):
+            d[n][1, :, 97:] = 0
+    check(d, io, lengths, scale=0.2, what=f"{io} segments {shape}")
+    if shape[0] == 1:
+        check({**d, "S0": None, "dS": None}, io, [T - 290], scale=0.2, what=f"{io} segments {shape} short", backward=False)
+
+
 def test_gradients_are_the_differences():
     """float32 gradients against differences of the forward's own results: a change of
     2^-7 in a random direction, twice, leaves third-order terms, 2^-14 of the loss's

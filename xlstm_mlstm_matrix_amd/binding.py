@@ -440,7 +440,8 @@ def _guard(device):
     """The device as the current one (torch's guard only where it is not: a few
     microseconds, as much as a small kernel runs)."""
     import torch
-    if device.index == torch.cuda.current_device():
+    current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    if device.index == current():
         return _NO_GUARD
     return torch.cuda.device(device)
 
@@ -525,9 +526,21 @@ def _hip_device(t, name):
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("tensors must be on a HIP device")
     return t.device
+
+
+def _good(dtype, index, *pairs):
+    """Whether all (tensor, shape) pass _view's and _strided's checks; the fast way
+    through them, which says nothing about what is wrong."""
+    try:
+        for t, shape in pairs:
+            if t.shape != shape or t.dtype is not dtype or t.get_device() != index or t.stride(-1) != 1:
+                return False
+    except AttributeError:
+        return False
+    return True
 
 
 def _workspace(workspace, nbytes, device):
@@ -695,20 +708,25 @@ def deltarule_fwd(q, k, v, log_decay, beta, S0=None, *, lengths=None, scale: flo
         raise ValueError("q, k, v must be [B, H, T, d]")
     B, Hk, T, dk = q.shape
     H, dv = v.shape[1], v.shape[-1]
-    _view(q, "q", (B, Hk, T, dk), q.dtype, dev)
-    _view(k, "k", (B, Hk, T, dk), q.dtype, dev)
-    _view(v, "v", (B, H, T, dv), q.dtype, dev)
-    _strided(log_decay, "log_decay", (B, H, T), torch.float32, dev)
-    _strided(beta, "beta", (B, H, T), torch.float32, dev)
-    _dense(S0, "S0", (B, H, dk, dv), torch.float32, dev)
+    dt, nk, nv, ng, ns = q.dtype, (B, Hk, T, dk), (B, H, T, dv), (B, H, T), (B, H, dk, dv)
+    if not _good(dt, dev.index, (q, nk), (k, nk), (v, nv)):
+        _view(q, "q", nk, dt, dev)
+        _view(k, "k", nk, dt, dev)
+        _view(v, "v", nv, dt, dev)
+    if not _good(torch.float32, dev.index, (log_decay, ng), (beta, ng)):
+        _strided(log_decay, "log_decay", ng, torch.float32, dev)
+        _strided(beta, "beta", ng, torch.float32, dev)
+    _dense(S0, "S0", ns, torch.float32, dev)
     _dense(lengths, "lengths", (B,), torch.int32, dev)
     with _guard(dev):
         if o is None:
-            o = torch.empty((B, H, T, dv), dtype=q.dtype, device=dev)
-        if return_state and S_T is None:
-            S_T = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
-        _view(o, "o", (B, H, T, dv), q.dtype, dev)
-        _dense(S_T, "S_T", (B, H, dk, dv), torch.float32, dev)
+            o = torch.empty(nv, dtype=dt, device=dev)
+        else:
+            _view(o, "o", nv, dt, dev)
+        if S_T is not None:
+            _dense(S_T, "S_T", ns, torch.float32, dev)
+        elif return_state:
+            S_T = torch.empty(ns, dtype=torch.float32, device=dev)
         wp, wn, _keep = _workspace(workspace, deltarule_workspace_size(B, Hk, H, T, dk, dv, io), dev)
         _check(lib().mlstm_deltarule_fwd(
             _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(beta), _ptr(S0), _ptr(lengths), _ptr(o),
@@ -732,20 +750,26 @@ def deltarule_step(q, k, v, log_decay, beta, S=None, *, scale: float = 1.0, o=No
         raise ValueError("q, k, v must be [B, H, d]")
     B, Hk, dk = q.shape
     H, dv = v.shape[1], v.shape[-1]
-    _view(q, "q", (B, Hk, dk), q.dtype, dev)
-    _view(k, "k", (B, Hk, dk), q.dtype, dev)
-    _view(v, "v", (B, H, dv), q.dtype, dev)
-    _strided(log_decay, "log_decay", (B, H), torch.float32, dev)
-    _strided(beta, "beta", (B, H), torch.float32, dev)
-    _dense(S, "S", (B, H, dk, dv), torch.float32, dev)
+    dt, nk, nv, ng, ns = q.dtype, (B, Hk, dk), (B, H, dv), (B, H), (B, H, dk, dv)
+    if not _good(dt, dev.index, (q, nk), (k, nk), (v, nv)):
+        _view(q, "q", nk, dt, dev)
+        _view(k, "k", nk, dt, dev)
+        _view(v, "v", nv, dt, dev)
+    if not _good(torch.float32, dev.index, (log_decay, ng), (beta, ng)):
+        _strided(log_decay, "log_decay", ng, torch.float32, dev)
+        _strided(beta, "beta", ng, torch.float32, dev)
+    _dense(S, "S", ns, torch.float32, dev)
     with _guard(dev):
         if o is None:
-            o = torch.empty((B, H, dv), dtype=q.dtype, device=dev)
-        if S_out is None:
-            S_out = S if inplace and S is not None else \
-                torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
-        _view(o, "o", (B, H, dv), q.dtype, dev)
-        _dense(S_out, "S_out", (B, H, dk, dv), torch.float32, dev)
+            o = torch.empty(nv, dtype=dt, device=dev)
+        else:
+            _view(o, "o", nv, dt, dev)
+        if S_out is not None:
+            _dense(S_out, "S_out", ns, torch.float32, dev)
+        elif inplace and S is not None:
+            S_out = S
+        else:
+            S_out = torch.empty(ns, dtype=torch.float32, device=dev)
         _check(lib().mlstm_deltarule_step(
             _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(beta), _ptr(S), _ptr(o), _ptr(S_out),
             _gate_strides((3, 4), q, k, v, log_decay, beta, o), scale, B, Hk, H, dk, dv, io, _raw_stream(dev)))
@@ -908,20 +932,24 @@ def _qk_checks(q, k, others, inv_freq, positions, weights, dev):
     import torch
     B, H, T, d = q.shape
     Hk = 0 if k is None else k.shape[1]
-    for name, t, h in (("q", q, H), ("k", k, Hk)) + others:
-        if k is not None or h != Hk:
-            _view(t, name, (B, h, T, d), q.dtype, dev)
-        elif t is not None:
-            raise ValueError(f"{name} without k")
+    nq, nk = (B, H, T, d), (B, Hk, T, d)
+    if k is None or not _good(q.dtype, dev.index, (q, nq), (k, nk), *((t, nq if h == H else nk) for _, t, h in others)):
+        for name, t, h in (("q", q, H), ("k", k, Hk)) + others:
+            if k is not None or h != Hk:
+                _view(t, name, (B, h, T, d), q.dtype, dev)
+            elif t is not None:
+                raise ValueError(f"{name} without k")
     for name, w in weights:
-        _dense(w, name, (d,), torch.float32, dev)
+        if w is not None:
+            _dense(w, name, (d,), torch.float32, dev)
     n = 0
     if inv_freq is not None:
         if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
             raise TypeError("inv_freq must be a torch tensor of one dimension")
         n = inv_freq.shape[0]
         _dense(inv_freq, "inv_freq", (n,), torch.float32, dev)
-    _dense(positions, "positions", (B, T), torch.int32, dev)
+    if positions is not None:
+        _dense(positions, "positions", (B, T), torch.int32, dev)
     return B, H, Hk, T, d, n
 
 

@@ -130,7 +130,7 @@ constexpr int kPrepWaves = 4, kLd = 36;  // wavefronts of a workgroup, row of a 
 // One wavefront a chunk.  The inverse goes by blocks of 16 x 16: those on the diagonal
 // row by row (a lane a column), which no cancellation hurts where keys are alike,
 // then T'_21 = -T'_22 (N beta)_21 T'_11 on the float32 MFMA.
-template <typename IO, bool BWD>
+template <typename IO, int DKP, bool BWD>
 __global__ __launch_bounds__(64 * kPrepWaves) void prep_kernel(DeltaArgs a, char *rec, char *rec_back, long long total) {
     using R = Rec<IO, BWD ? STATES : FORWARD>;
     using RB = Rec<IO, BACK>;
@@ -182,21 +182,29 @@ __global__ __launch_bounds__(64 * kPrepWaves) void prep_kernel(DeltaArgs a, char
     f32x4 kk[3] = {}, qk[3] = {};  // tiles (0, 0), (1, 0), (1, 1)
     const IO *kp = (const IO *)a.k + b * a.sk.s0 + hk * a.sk.s1 + s * a.sk.s2;
     const IO *qp = (const IO *)a.q + b * a.sq.s0 + hk * a.sq.s1 + s * a.sq.s2;
-    for (int col = 8 * g4; col < (a.dk + 31) / 32 * 32; col += 32) {
-        Frag k[2], q[2];
+    // loads of AHEAD steps in flight: one at a time the wavefront waits for each
+    constexpr int NKS = DKP / 32, AHEAD = sizeof(IO) == 2 ? (NKS < 4 ? NKS : 4) : 2;
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const int r = 16 * t + l16;
-            const bool ok = r < nc && col < a.dk;
-            k[t] = row8(kp + r * a.sk.s2 + col, ok);
-            q[t] = row8(qp + r * a.sq.s2 + col, ok);
+    for (int k0 = 0; k0 < NKS; k0 += AHEAD) {
+        Frag k[AHEAD][2], q[AHEAD][2];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int r = 16 * t + l16, col = 32 * (k0 + i) + 8 * g4;
+                const bool ok = r < nc && col < a.dk;
+                k[i][t] = row8(kp + r * a.sk.s2 + col, ok);
+                q[i][t] = row8(qp + r * a.sq.s2 + col, ok);
+            }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            kk[0] = mfma(k[i][0], k[i][0], kk[0]);
+            kk[1] = mfma(k[i][1], k[i][0], kk[1]);
+            kk[2] = mfma(k[i][1], k[i][1], kk[2]);
+            qk[0] = mfma(q[i][0], k[i][0], qk[0]);
+            qk[1] = mfma(q[i][1], k[i][0], qk[1]);
+            qk[2] = mfma(q[i][1], k[i][1], qk[2]);
         }
-        kk[0] = mfma(k[0], k[0], kk[0]);
-        kk[1] = mfma(k[1], k[0], kk[1]);
-        kk[2] = mfma(k[1], k[1], kk[2]);
-        qk[0] = mfma(q[0], k[0], qk[0]);
-        qk[1] = mfma(q[1], k[0], qk[1]);
-        qk[2] = mfma(q[1], k[1], qk[2]);
     }
     __syncthreads();
 #pragma unroll
@@ -258,7 +266,12 @@ __global__ __launch_bounds__(64 * kPrepWaves) void prep_kernel(DeltaArgs a, char
             const float bi = be[o + i];
             float sum = 0.0f;
 #pragma unroll
-            for (int m = 0; m < i; ++m) sum += A[(o + i) * kLd + o + m] * y[m];
+            for (int m = 0; m < i; m += 4) {
+                const f32x4 n4 = *(const f32x4 *)(A + (o + i) * kLd + o + m);  // zeros from column i on
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (m + e < i) sum += n4[e] * y[m + e];
+            }
             x[i] = (i == l16 ? 1.0f : 0.0f) - (second ? sum * bi : sum);
             y[i] = second ? x[i] : x[i] * bi;
             to[(o + i) * kLd + o + l16] = x[i];
@@ -344,7 +357,7 @@ struct Cfg {
     static constexpr int ELEMS = L * TROW + REC, VELEMS = VOWN ? L * 16 * NCT : 8;
     static constexpr size_t TILE = (size_t)ELEMS * sizeof(IO), VTILE = VOWN ? (size_t)L * BV * sizeof(IO) : 0;
     static constexpr int NBUF = 2 * TILE + VTILE <= kLds ? 2 : 1;
-    static constexpr int PER_CU = 2 * (NBUF * TILE + VTILE) <= kLds && NW == 4 && DKP * NCT < 512 ? 2 : 1;  // workgroups of a compute unit
+    static constexpr int PER_CU = 2 * (NBUF * TILE + VTILE) <= kLds && NW == 4 ? 2 : 1;  // workgroups of a compute unit
     static_assert(QG >= 8, "swizzle");
     static_assert(TILE + VTILE <= kLds, "LDS");
 };
@@ -1476,9 +1489,22 @@ hipError_t with_shape(int dk, bool wide, F f) {
     constexpr integral_constant<int, 4> four{};
     if (dk <= 64) return wide ? f(integral_constant<int, 64>{}, two, four) : f(integral_constant<int, 64>{}, one, four);
     if (dk <= 128) return wide ? f(integral_constant<int, 128>{}, two, four) : f(integral_constant<int, 128>{}, one, four);
+    // two wavefronts a SIMD: one of 32 columns each does its vector and matrix instructions by
+    // turns (64 heads of 256 x 512, 4096 tokens: 713 us, with four wavefronts of 32 columns 802)
     if constexpr (sizeof(IO) == 2)
-        if (wide) return f(integral_constant<int, 256>{}, two, four);
+        if (wide) return f(integral_constant<int, 256>{}, one, integral_constant<int, 8>{});
     return f(integral_constant<int, 256>{}, one, four);
+}
+
+template <typename IO, bool BWD>
+void launch_prep(const DeltaArgs &a, char *rec, char *back, long long total, hipStream_t s) {
+    const dim3 grid((unsigned)((total + kPrepWaves - 1) / kPrepWaves));
+    if (a.dk <= 64)
+        prep_kernel<IO, 64, BWD><<<grid, 64 * kPrepWaves, 0, s>>>(a, rec, back, total);
+    else if (a.dk <= 128)
+        prep_kernel<IO, 128, BWD><<<grid, 64 * kPrepWaves, 0, s>>>(a, rec, back, total);
+    else
+        prep_kernel<IO, 256, BWD><<<grid, 64 * kPrepWaves, 0, s>>>(a, rec, back, total);
 }
 
 // Workspace of the forward, floats from its start.
@@ -1503,7 +1529,7 @@ hipError_t launch_fwd_t(const DeltaArgs &a, hipStream_t s) {
     const Plan p = make_plan(cells, a.T, a.dv);
     char *rec = (char *)(a.ws + w.rec);
     const long long total = (long long)cells * chunks(a.T);
-    prep_kernel<IO, false><<<dim3((unsigned)((total + kPrepWaves - 1) / kPrepWaves)), 64 * kPrepWaves, 0, s>>>(a, rec, nullptr, total);
+    launch_prep<IO, false>(a, rec, nullptr, total, s);
     const Segs sg{p.nseg, p.len, a.ws + w.local, a.ws + w.state};
     return with_shape<IO>(a.dk, p.wide, [&](auto dkp, auto nct, auto nw) {
         constexpr int DKP = decltype(dkp)::value, NCT = decltype(nct)::value, NW = decltype(nw)::value, BV = 16 * NCT * NW;
@@ -1572,7 +1598,7 @@ hipError_t launch_bwd_t(const DeltaArgs &a, hipStream_t s) {
     const BwdWs w = bwd_ws<IO>(cells, a.T, a.dk, a.dv);
     const long long total = (long long)cells * chunks(a.T);
     const Plan p = make_plan(cells, a.T, a.dv);
-    prep_kernel<IO, true><<<dim3((unsigned)((total + kPrepWaves - 1) / kPrepWaves)), 64 * kPrepWaves, 0, s>>>(a, ws + w.rec, ws + w.rec_back, total);
+    launch_prep<IO, true>(a, ws + w.rec, ws + w.rec_back, total, s);
     BackArgs k{};
     k.a = a;
     k.a.v = a.d_o;

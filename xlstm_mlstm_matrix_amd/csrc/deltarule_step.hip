@@ -12,14 +12,30 @@ namespace mlstm {
 
 namespace {
 
-// Workgroup: 256 threads = 16 column threads (4 columns, 16 bytes each) x 16 row
-// groups; thread (rg, ct) holds rows rg, rg + 16, ... (NR of them).
-template <typename IO, int NR>
-__global__ __launch_bounds__(256) void deltarule_step_kernel(DeltaStepArgs a, int ntile) {
-    constexpr int CT = 16, RG = 16;
+constexpr long long kStreamBytes = 320ll << 20;  // a quarter more than the Infinity Cache
+
+// 16 bytes of state, past the caches' replacement order when STREAM
+template <bool STREAM>
+__device__ __forceinline__ f32x4 load(const float *p) {
+    if constexpr (STREAM) return __builtin_nontemporal_load((const f32x4 *)p);
+    return *(const f32x4 *)p;
+}
+template <bool STREAM>
+__device__ __forceinline__ void store(float *p, f32x4 x) {
+    if constexpr (STREAM)
+        __builtin_nontemporal_store(x, (f32x4 *)p);
+    else
+        *(f32x4 *)p = x;
+}
+
+// Workgroup: CT column threads (4 columns, 16 bytes each) x 16 row groups; thread
+// (rg, ct) holds rows rg, rg + 16, ... (NR of them).
+template <typename IO, int NR, int CT, bool STREAM>
+__global__ __launch_bounds__(16 * CT) void deltarule_step_kernel(DeltaStepArgs a, int ntile) {
+    constexpr int RG = 16, NW = CT / 4;
     __shared__ float qs[256], ks[256];
-    __shared__ f32x4 red[4][2][CT];
-    __shared__ float dot[4];
+    __shared__ f32x4 red[NW][2][CT];
+    __shared__ float dot[NW];
     const int tile = blockIdx.x % ntile, bh = blockIdx.x / ntile;
     const int b = bh / a.H, h = bh % a.H, hk = h / (a.H / a.Hk);
     const int tid = threadIdx.x, ct = tid % CT, rg = tid / CT, wave = tid >> 6;
@@ -30,32 +46,37 @@ __global__ __launch_bounds__(256) void deltarule_step_kernel(DeltaStepArgs a, in
     const IO *v = (const IO *)a.v + b * a.sv.s0 + h * a.sv.s1;
     const float gam = __builtin_amdgcn_exp2f(decay_log2(a.g[b * a.sg.s0 + h * a.sg.s1]));
     const float beta = a.beta[b * a.sb.s0 + h * a.sb.s1];
-    if (tid < a.dk) {
-        qs[tid] = to_f(q[tid]);
-        ks[tid] = to_f(k[tid]);
+    // d_qk is a multiple of 16: a thread's rows past it are the same for all threads.  They
+    // load the last row again and count as zeros, without a branch.
+    const int nr = a.dk / RG;
+    for (int i = tid; i < RG * NR; i += RG * CT) {
+        const int r = min(i, a.dk - 1);
+        qs[i] = i < a.dk ? to_f(q[r]) : 0.0f;
+        ks[i] = i < a.dk ? to_f(k[r]) : 0.0f;
     }
-    const size_t base = (size_t)bh * a.dk * a.dv + col;
+    const int c = ok ? col : 0;
+    const size_t base = (size_t)bh * a.dk * a.dv + c;
     f32x4 S[NR];
+    if (a.S_in) {
 #pragma unroll
-    for (int i = 0; i < NR; ++i) {
-        const int r = rg + RG * i;
-        S[i] = f32x4{0, 0, 0, 0};
-        if (ok && a.S_in && r < a.dk) S[i] = gam * *(const f32x4 *)(a.S_in + base + (size_t)r * a.dv);
+        for (int i = 0; i < NR; ++i) S[i] = load<STREAM>(a.S_in + base + (size_t)(rg + RG * min(i, nr - 1)) * a.dv);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NR; ++i) S[i] = f32x4{0, 0, 0, 0};
     }
     __syncthreads();
     f32x4 kS = {0, 0, 0, 0}, qS = kS;
     float qk = 0.0f;
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
-        const int r = rg + RG * i;
-        if (r < a.dk) {
-            kS += ks[r] * S[i];
-            qS += qs[r] * S[i];
-            qk += qs[r] * ks[r];
-        }
+        const float kr = ks[rg + RG * i], qr = qs[rg + RG * i];
+        S[i] *= i < nr ? gam : 0.0f;
+        kS += kr * S[i];
+        qS += qr * S[i];
+        qk += qr * kr;
     }
 #pragma unroll
-    for (int m = 16; m < 64; m <<= 1) {
+    for (int m = CT; m < 64; m <<= 1) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             kS[e] += __shfl_xor(kS[e], m);
@@ -69,36 +90,59 @@ __global__ __launch_bounds__(256) void deltarule_step_kernel(DeltaStepArgs a, in
         if (ct == 0) dot[wave] = qk;
     }
     __syncthreads();
-    kS = (red[0][0][ct] + red[1][0][ct]) + (red[2][0][ct] + red[3][0][ct]);
+    kS = red[0][0][ct];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) kS += red[w][0][ct];
     if (!ok) return;
     const f32x4 vv = {to_f(v[col]), to_f(v[col + 1]), to_f(v[col + 2]), to_f(v[col + 3])};
     const f32x4 u = (vv - kS) * beta;
     float *So = a.S_out + base;
 #pragma unroll
-    for (int i = 0; i < NR; ++i) {
-        const int r = rg + RG * i;
-        if (r < a.dk) *(f32x4 *)(So + (size_t)r * a.dv) = S[i] + ks[r] * u;
-    }
+    for (int i = 0; i < NR; ++i)
+        if (i < nr) store<STREAM>(So + (size_t)(rg + RG * i) * a.dv, S[i] + ks[rg + RG * i] * u);
     if (rg == 0) {
         IO *o = (IO *)a.o + b * a.so.s0 + h * a.so.s1 + col;
-        qS = (red[0][1][ct] + red[1][1][ct]) + (red[2][1][ct] + red[3][1][ct]);
-        const f32x4 y = (qS + ((dot[0] + dot[1]) + (dot[2] + dot[3])) * u) * a.scale;
+        qS = red[0][1][ct];
+        qk = dot[0];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) {
+            qS += red[w][1][ct];
+            qk += dot[w];
+        }
+        const f32x4 y = (qS + qk * u) * a.scale;
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[e] = from_f<IO>(y[e]);
     }
 }
 
-template <typename IO>
-hipError_t launch_t(const DeltaStepArgs &a, hipStream_t s) {
-    const int ntile = (a.dv + 63) / 64;
+template <typename IO, int CT, bool STREAM>
+hipError_t launch_ct(const DeltaStepArgs &a, hipStream_t s) {
+    const int ntile = (a.dv + 4 * CT - 1) / (4 * CT);
     const dim3 grid((unsigned)(a.B * a.H * ntile));
     if (a.dk <= 64)
-        deltarule_step_kernel<IO, 4><<<grid, 256, 0, s>>>(a, ntile);
+        deltarule_step_kernel<IO, 4, CT, STREAM><<<grid, 16 * CT, 0, s>>>(a, ntile);
     else if (a.dk <= 128)
-        deltarule_step_kernel<IO, 8><<<grid, 256, 0, s>>>(a, ntile);
+        deltarule_step_kernel<IO, 8, CT, STREAM><<<grid, 16 * CT, 0, s>>>(a, ntile);
     else
-        deltarule_step_kernel<IO, 16><<<grid, 256, 0, s>>>(a, ntile);
+        deltarule_step_kernel<IO, 16, CT, STREAM><<<grid, 16 * CT, 0, s>>>(a, ntile);
     return hipGetLastError();
+}
+
+template <typename IO>
+hipError_t launch_t(const DeltaStepArgs &a, hipStream_t s) {
+    const long long cells = (long long)a.B * a.H;
+    const int quads = a.dv / 4;
+    // States that the cache cannot hold from one step to the next are streamed past it, by
+    // the bytes touched: once in place, twice from one tensor into another.  128 columns a
+    // workgroup, 256 x 512: 1 GB in place 384 us, streamed 372; 128 MB 80 us, streamed 103.  With
+    // 64 columns they take 439 and 83.
+    const bool once = !a.S_in || a.S_in == a.S_out;
+    if (cells * a.dk * a.dv * (once ? 4 : 8) > kStreamBytes && quads >= 32) return launch_ct<IO, 32, true>(a, s);
+    // narrower ones for two workgroups a compute unit
+    auto wgs = [&](int ct) { return cells * ((quads + ct - 1) / ct); };
+    if (quads >= 32 && wgs(32) >= 512) return launch_ct<IO, 32, false>(a, s);
+    if (quads >= 16 && wgs(16) >= 512) return launch_ct<IO, 16, false>(a, s);
+    return launch_ct<IO, 8, false>(a, s);
 }
 
 }  // namespace

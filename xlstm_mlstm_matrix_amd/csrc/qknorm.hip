@@ -30,13 +30,24 @@ struct QkPlan {
 };
 
 template <typename IO, int V>
-__device__ __forceinline__ void load_row(const IO *p, bool ok, float *x) {
+struct Raw {
+    typedef IO type __attribute__((ext_vector_type(V)));
+};
+template <typename IO>
+struct Raw<IO, 1> {
+    typedef IO type;
+};
+template <typename IO, int V>
+__device__ __forceinline__ typename Raw<IO, V>::type load_row(const IO *p, bool ok) {
+    typename Raw<IO, V>::type v = {};
+    if (ok) v = *(const typename Raw<IO, V>::type *)p;
+    return v;
+}
+template <typename IO, int V>
+__device__ __forceinline__ void unpack(const typename Raw<IO, V>::type &v, float *x) {
     if constexpr (V == 1) {
-        x[0] = ok ? to_f(*p) : 0.0f;
+        x[0] = to_f(v);
     } else {
-        typedef IO vec __attribute__((ext_vector_type(V)));
-        vec v = {};
-        if (ok) v = *(const vec *)p;
 #pragma unroll
         for (int j = 0; j < V; ++j) x[j] = to_f((IO)v[j]);
     }
@@ -135,6 +146,18 @@ __global__ __launch_bounds__(kThreads) void qk_kernel(QkArgs a, QkPlan p) {
             const IO *xr = (const IO *)a.x[ti] + b * a.sx[ti].s0 + t * a.sx[ti].s2;
             const IO *gr = BWD ? (const IO *)a.dy[ti] + b * a.sdy[ti].s0 + t * a.sdy[ti].s2 : nullptr;
             IO *yr = (IO *)a.y[ti] + b * a.sy[ti].s0 + t * a.sy[ti].s2;
+            // a head's row is on its way while the one before is computed
+            typename Raw<IO, V>::type xn[UPL][2], gn[UPL][2];
+            const auto fetch = [&](int h) {
+#pragma unroll
+                for (int i = 0; i < UPL; ++i)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        xn[i][k] = load_row<IO, V>(xr + h * a.sx[ti].s1 + off[i][k], ok[i][k]);
+                        if constexpr (BWD) gn[i][k] = load_row<IO, V>(gr + h * a.sdy[ti].s1 + off[i][k], ok[i][k]);
+                    }
+            };
+            fetch(first);
             for (int h = first; h < last; ++h) {
                 float x[UPL][W], g[UPL][W];
                 float ss = 0.0f, dot = 0.0f;
@@ -142,9 +165,10 @@ __global__ __launch_bounds__(kThreads) void qk_kernel(QkArgs a, QkPlan p) {
                 for (int i = 0; i < UPL; ++i)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        load_row<IO, V>(xr + h * a.sx[ti].s1 + off[i][k], ok[i][k], x[i] + k * V);
-                        if constexpr (BWD) load_row<IO, V>(gr + h * a.sdy[ti].s1 + off[i][k], ok[i][k], g[i] + k * V);
+                        unpack<IO, V>(xn[i][k], x[i] + k * V);
+                        if constexpr (BWD) unpack<IO, V>(gn[i][k], g[i] + k * V);
                     }
+                if (h + 1 < last) fetch(h + 1);
                 if constexpr (BWD) {
 #pragma unroll
                     for (int i = 0; i < UPL; ++i)
