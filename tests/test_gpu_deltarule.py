@@ -260,6 +260,23 @@ def test_segments(io, shape):
         check({**d, "S0": None, "dS": None}, io, [T - 290], scale=0.2, what=f"{io} segments {shape} short", backward=False)
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_state_in_place_over_segments(io):
+    """S_T over S0 where the sequence runs in segments, against separate tensors; an empty
+    sequence among them keeps its state."""
+    d = make(io, 3, 1, 1, 900, 64, 128, seed=14, decay=0.01)
+    g = cu(d)
+    a = [g[n] for n in ("q", "k", "v", "g", "beta")]
+    n = ints([900, 0, 333])
+    o, S = B.deltarule_fwd(*a, g["S0"], lengths=n, scale=0.2)
+    for _ in range(5):
+        state = g["S0"].clone()
+        o2, S2 = B.deltarule_fwd(*a, state, lengths=n, scale=0.2, S_T=state)
+        torch.cuda.synchronize()
+        assert S2 is state and torch.equal(o, o2) and torch.equal(S, S2)
+    assert torch.equal(S[1], g["S0"][1])
+
+
 def test_gradients_are_the_differences():
     """float32 gradients against differences of the forward's own results: a change of
     2^-7 in a random direction, twice, leaves third-order terms, 2^-14 of the loss's

@@ -421,11 +421,12 @@ __device__ __forceinline__ void walk(const DeltaArgs &a, const char *rec, WalkOu
 #pragma unroll
         for (int bt = 0; bt < NCT; ++bt) X[at][bt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     const int nch = (n + L - 1) / L, c0 = seg * sg.len, c1 = min(c0 + sg.len, nch);  // this segment's chunks
-    const float *start = W == BACK ? (c1 == nch ? a.S0 : nullptr) : (seg == 0 ? a.S0 : nullptr);
-    if (SO)
-        start = nullptr;
-    else if (sg.count > 1 && c0 < nch)
-        start = (W == BACK ? c1 < nch : seg > 0) ? sg.state + (size_t)seg * dk * dv + (size_t)bh * (sg.count - 1) * dk * dv : start;
+    // The state before the first token of this walk.  With segments all but an empty sequence's
+    // come from the scan's buffer, the first one too: S_T may be S0, which the last segment's
+    // workgroups write while the first one's may not have read it.
+    const float *start = SO ? nullptr : W == BACK ? (c1 == nch ? a.S0 : nullptr) : (seg == 0 ? a.S0 : nullptr);
+    if (!SO && sg.count > 1 && c0 < nch && (W == BACK ? c1 < nch : seg > 0 || a.S0))
+        start = sg.state + ((size_t)bh * (sg.count - 1) + seg) * dk * dv;  // + cell below
     if (start) {
         const auto xs = __builtin_amdgcn_make_buffer_rsrc((void *)(start + cell), 0, dk * dv * 4, kBuf);
 #pragma unroll
@@ -872,8 +873,10 @@ __device__ __forceinline__ void scan(const DeltaArgs &a, const float *start, Seg
     const int row = live ? 16 * wave : dk - 16;
     for (int i = tid; i < DKP * 16; i += 64 * NK) {
         const int r = i / 16, c = i % 16;
-        S[0][r * kScanLd + c] = start && r < dk ? start[((size_t)bh * dk + r) * dv + col0 + c] : 0.0f;
+        const float x = start && r < dk ? start[((size_t)bh * dk + r) * dv + col0 + c] : 0.0f;
+        S[0][r * kScanLd + c] = x;
         S[1][r * kScanLd + c] = 0.0f;
+        if (!REV && r < dk) sg.state[((size_t)bh * sg.count * dk + r) * dv + col0 + c] = x;
     }
     // part p of M's columns (all of them up to 128, else 128 each) of a step, and b
     auto fetch = [&](int step, int p, f32x4 *m, f32x4 &add) {
