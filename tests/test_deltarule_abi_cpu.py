@@ -148,6 +148,10 @@ def test_qknorm_refusals(back):
     for off in (3 * 32 * 2, 4 * 32 * 2 - 2, 5 * 32 * 2):
         at["yk"] = 9 * M + off
         assert qk(back, strides=strides(*six[:-2], row, row), **at) == ALIAS, off
+    # rows at 0, 100, 132 and 232 and those 50 behind them: 132 ... 163 meets 150 ... 181
+    odd = dict(T=1, H=2, Hk=2, yq=9 * M, yk=9 * M + 50 * 2)
+    dense = [(64, 32, 32)] * (len(six) - 2)
+    assert qk(back, strides=strides(*dense, (132, 100, 0), (132, 100, 0)), **odd) == ALIAS
     wider = (10 * 6 * 32, 32, 7 * 32)
     assert qk(back, strides=strides(*six[:-2], row, wider), yq=9 * M, yk=9 * M + 256) == ALIAS
     if back:

@@ -277,6 +277,18 @@ def test_state_in_place_over_segments(io):
     assert torch.equal(S[1], g["S0"][1])
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_gradients_over_segments_of_a_padded_batch(io):
+    """Sequences that end in the last segment, the first, a middle one and before any
+    token, of heads that share queries and keys."""
+    lengths = [700, 20, 333, 0]
+    d = make(io, 4, 1, 2, 700, 48, 32, seed=15, decay=0.01)
+    for i, n in enumerate(lengths):
+        for name in ("q", "k", "v", "do", "g", "beta"):
+            d[name][i, :, n:] = 0
+    check(d, io, lengths, scale=0.2, what=f"{io} padded segments")
+
+
 def test_gradients_are_the_differences():
     """float32 gradients against differences of the forward's own results: a change of
     2^-7 in a random direction, twice, leaves third-order terms, 2^-14 of the loss's

@@ -7,6 +7,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "hostcheck.hpp"
 #include "ops.hpp"
 
@@ -482,7 +484,15 @@ bool interleaved(const View &x, const View &y, size_t es) {
     // inner dimensions 0 .. m - 1 of both, side by side within one step of dimension m
     long long span_a = a.d, span_b = b.d;
     for (int m = 0;; ++m) {
-        if (delta >= span_a && (m == n || delta + span_b <= st[dim[m]])) return true;
+        if (delta >= span_a && (m == n || delta + span_b <= st[dim[m]])) {
+            // ... and the steps of the outer ones are apart from one another
+            long long reach = m == n ? 0 : st[dim[m]];
+            for (int j = m; j < n; ++j) {
+                if (st[dim[j]] < reach) return false;
+                reach += st[dim[j]] * (std::max(na[dim[j]], nb[dim[j]]) - 1);
+            }
+            return true;
+        }
         if (m == n) return false;
         span_a += st[dim[m]] * (na[dim[m]] - 1);
         span_b += st[dim[m]] * (nb[dim[m]] - 1);
