@@ -1539,7 +1539,7 @@ hipError_t launch_fwd_t(const DeltaArgs &a, hipStream_t s) {
         const int vt = (a.dv + BV - 1) / BV, kt = (a.dk + BV - 1) / BV;
         const auto run = [&](auto parts) {
             constexpr int SP = decltype(parts)::value;
-            if constexpr (NCT == 1)
+            if constexpr (NCT == 1 && NW == 4)
                 if (p.nseg > 1) {
                     forward_kernel<IO, DKP, NCT, NW, SP, true><<<dim3((unsigned)(cells * p.nseg * (vt + kt))), 64 * NW, 0, s>>>(a, rec, sg);
                     const unsigned n = (unsigned)(cells * (a.dv / 16));
@@ -1621,7 +1621,7 @@ hipError_t launch_bwd_t(const DeltaArgs &a, hipStream_t s) {
         constexpr int DKP = decltype(dkp)::value, NCT = decltype(nct)::value, NW = decltype(nw)::value, BV = 16 * NCT * NW;
         const int vt = (a.dv + BV - 1) / BV, kt = (a.dk + BV - 1) / BV;
         k.nback = (int)(cells * p.nseg * vt);
-        if constexpr (NCT == 1)
+        if constexpr (NCT == 1 && NW == 4)
             if (p.nseg > 1) {
                 back_kernel<IO, DKP, NCT, NW, true><<<dim3((unsigned)(cells * p.nseg * (2 * vt + kt))), 64 * NW, 0, s>>>(k);
                 const unsigned n = (unsigned)(cells * (a.dv / 16));
