@@ -130,6 +130,9 @@ constexpr int kPrepWaves = 4, kLd = 36;  // wavefronts of a workgroup, row of a 
 // One wavefront a chunk.  The inverse goes by blocks of 16 x 16: those on the diagonal
 // row by row (a lane a column), which no cancellation hurts where keys are alike,
 // then T'_21 = -T'_22 (N beta)_21 T'_11 on the float32 MFMA.
+// Bound by HBM where there are many chunks: 64 heads of 256 x 512, 4096 tokens, bfloat16 71 us for
+// 394 MB (5.5 TB/s; 137 MB read and 157 written for the backward at d_qk = 128: 63 us); a
+// call of two chunks takes 8 us, the inverse's rows one after another.
 template <typename IO, int DKP, bool BWD>
 __global__ __launch_bounds__(64 * kPrepWaves) void prep_kernel(DeltaArgs a, char *rec, char *rec_back, long long total) {
     using R = Rec<IO, BWD ? STATES : FORWARD>;
@@ -378,6 +381,12 @@ __device__ __forceinline__ f32x4 mfma_parts(const Frag *x, const Frag *y, f32x4 
 //   D <- e^{G_L} D + Q^T (scale e^G o do) - K^T (e^G o dV).
 // Workgroup `wg` of `nwg`.  The tiles are two arrays of the kernel, and a loop goes over pairs of
 // chunks: the compiler waits for a copy in flight before any LDS read that may alias it.
+//
+// Bound by vector and matrix instructions that one or two wavefronts a SIMD overlap little (d_qk = 128,
+// three parts: 82 MFMA and some 380 vector instructions a chunk and wavefront, half of these the
+// split of S): 64 heads of 256 x 512, 4096 tokens, bfloat16 640 us (5 us a chunk), 128 x 128
+// 1.75 us a chunk.  Half of the rows for each of two wavefronts, their sums joined in LDS, was
+// slower (1.75 -> 2.05 us): the small products are then done twice.
 template <typename IO, int DKP, int NCT, int NW, int SP, Walk W, bool SO>
 __device__ __forceinline__ void walk(const DeltaArgs &a, const char *rec, WalkOut to, Segs sg, int wg, int nwg, IO *tile0,
                                      IO *tile1, IO *vtiles) {
@@ -820,7 +829,8 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW, FORWARD, SO>::PER_C
 }
 
 // Both walks of the backward, which do not need one another: the first `nback` workgroups are
-// BACK's, the longer one.
+// BACK's, the longer one (64 heads of 128 x 128, 4096 tokens, bfloat16: 365 us, 2.9 us a chunk, with
+// 0.8 GB of X, dU and kept states written).
 struct BackArgs {
     DeltaArgs a;              // do, dS_T and dS0 in the places of v, S0 and S_T
     const char *rec, *rec_back;
@@ -978,7 +988,8 @@ __global__ __launch_bounds__(4 * DKP) void scan_kernel(DeltaArgs a, const float 
 // d_qk for all tokens: S and D come to it in operand order straight from memory; do, X
 // and dU are split once, by the wavefront of their 16 tokens, and shared through LDS.
 // Everything is computed transposed (lane: token, rows: d_qk), so that rows leave in
-// whole vectors.
+// whole vectors.  Bound by HBM and what it feeds: 64 heads of 128 x 128, 4096 tokens, bfloat16
+// 315 us for 1.17 GB read and 0.22 written (4.4 TB/s); float32, 16 heads of 64 x 64, 1024 tokens 19 us.
 struct GradIn {
     const float *x, *du;
     const char *s, *d;
@@ -1464,19 +1475,25 @@ __global__ __launch_bounds__(64 * NW, SHARED && NW == 4 ? 1 : 2) void grad_kerne
 // ---- launches
 
 // Columns of a workgroup, and segments.  128 columns where that gives every compute unit a
-// workgroup, else 64.  Segments where up to a quarter of the units would have one: they
-// cost a second walk, of twice the columns (d_v and d_qk of them) where d_qk is as large as
-// d_v, and the scan's steps, each longer than a chunk; so as many as make a
-// workgroup a unit, and as sqrt(4 chunks), of at least 4 chunks.
+// workgroup, else 64 (4096 tokens, bfloat16, 64 / 128: 64 heads of 128 x 128 245 / 376 us, 192 heads
+// 460 / 464, 64 heads of 256 x 512 803 / 653; 256 heads of 128 x 128, 2048 tokens 284 / 273).
+//
+// Segments where up to a quarter of the units would have a workgroup: they cost a second
+// walk, of twice the columns (d_v and d_qk of them) where d_qk is as large as d_v, and the scan's
+// steps, each longer than a chunk; so as many as make a workgroup a unit, and as
+// sqrt(4 chunks), of at least 4 chunks.  Without / with, 4096 tokens of 128 x 128: 32 heads (64
+// workgroups) 221 / 166 us, 48 heads 233 / 270; 8 heads of 256 x 512 (64) 354 / 248, 16 heads 363 / 425.
+// The backward's two walks run side by side and count both: 16 heads of 8192 tokens (2 x 32) 743 / 500 us,
+// 32 heads of 4096 (2 x 64) 494 / 504, 8 heads of 256 x 512 (2 x 64) 719 / 840.
 struct Plan {
     bool wide;
     int nseg, len;
 };
-Plan make_plan(size_t cells, int T, int dv) {
+Plan make_plan(size_t cells, int T, int dv, int walks) {
     Plan p;
     p.wide = cells * ((dv + 127) / 128) >= 256;
     const long long wgs = (long long)cells * ((dv + 63) / 64), nch = chunks(T);
-    long long want = wgs > 64 ? 1 : 256 / wgs;
+    long long want = wgs * walks > 64 ? 1 : 256 / wgs;
     while (want > 1 && (want * want > 4 * nch || want * 4 > nch)) --want;
     p.len = (int)((nch + want - 1) / want + 1) / 2 * 2;  // whole blocks of the backward
     p.nseg = (int)((nch + p.len - 1) / p.len);
@@ -1515,7 +1532,7 @@ struct FwdWs {
     size_t rec, local, state, total;
 };
 FwdWs fwd_ws(size_t cells, int T, int dk, int dv, int io_bf16) {
-    const Plan p = make_plan(cells, T, dv);
+    const Plan p = make_plan(cells, T, dv, 1);
     FwdWs w;
     w.rec = 0;
     w.local = w.rec + cells * (size_t)chunks(T) * (io_bf16 ? Rec<bf16, FORWARD>::BYTES : Rec<float, FORWARD>::BYTES) / 4;
@@ -1529,7 +1546,7 @@ hipError_t launch_fwd_t(const DeltaArgs &a, hipStream_t s) {
     constexpr bool BF = sizeof(IO) == 2;
     const size_t cells = (size_t)a.B * a.H;
     const FwdWs w = fwd_ws(cells, a.T, a.dk, a.dv, BF);
-    const Plan p = make_plan(cells, a.T, a.dv);
+    const Plan p = make_plan(cells, a.T, a.dv, 1);
     char *rec = (char *)(a.ws + w.rec);
     const long long total = (long long)cells * chunks(a.T);
     launch_prep<IO, false>(a, rec, nullptr, total, s);
@@ -1573,7 +1590,7 @@ BwdWs bwd_ws(size_t cells, int T, int dk, int dv) {
     w.du = w.x + cells * T * dv * 4;
     w.s = w.du + cells * T * dv * 4;
     w.d = w.s + states;
-    const Plan p = make_plan(cells, T, dv);
+    const Plan p = make_plan(cells, T, dv, 2);
     const size_t one = p.nseg > 1 ? cells * p.nseg * dk * 4 : 0;  // bytes of a column of all segments
     w.local = w.d + states;
     w.state = w.local + one * (dv + dk);
@@ -1600,7 +1617,7 @@ hipError_t launch_bwd_t(const DeltaArgs &a, hipStream_t s) {
     const size_t cells = (size_t)a.B * a.H;
     const BwdWs w = bwd_ws<IO>(cells, a.T, a.dk, a.dv);
     const long long total = (long long)cells * chunks(a.T);
-    const Plan p = make_plan(cells, a.T, a.dv);
+    const Plan p = make_plan(cells, a.T, a.dv, 2);
     launch_prep<IO, true>(a, ws + w.rec, ws + w.rec_back, total, s);
     BackArgs k{};
     k.a = a;

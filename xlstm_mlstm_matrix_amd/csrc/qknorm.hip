@@ -7,9 +7,9 @@
 // dw = sum over rows of u x r, dx = r (u w) - x r^3 (sum u w x) / n.
 //
 // Each row is read once and written once, nothing else is large: the pass is
-// bound by HBM (2 x 134 MB of 128 bfloat16 channels: 44 us, 6.1 TB/s with the inputs
-// partly in the cache; gradients of 168 MB of rows with rotation 65 us, 3.9 TB/s).  A row belongs to a few lanes of a wavefront; a lane holds both
-// channels of its pairs, so that rotating costs no exchange, and the row's sums are
+// bound by HBM (2 x 134 MB of 128 bfloat16 channels: 45 us, 6 TB/s with the inputs
+// partly in the cache, 58 us cold; gradients with rotation, 252 MB: 62 us, 4.1 TB/s).  A
+// row belongs to a few lanes of a wavefront; a lane holds both channels of its pairs, so that rotating costs no exchange, and the row's sums are
 // the only thing that crosses lanes.  The heads of a token are walked by the
 // same lanes, which keep the token's sines and cosines in registers.
 #include "ops.hpp"
