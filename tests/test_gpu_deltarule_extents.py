@@ -233,3 +233,14 @@ def test_qknorm_past_32_bit_offsets():
     torch.cuda.synchronize()
     assert bool(torch.isfinite(dw).all()) and bool((dk[0, 0, -64:].float().abs().amax(1) >= 0).all())
     assert bool(torch.isfinite(dq[0, :, -64:]).all())
+
+
+def test_qknorm_most_rows():
+    """2^31 - 1 rows, in place: two lanes a row are 2^32 threads, more than a launch takes."""
+    T, d = (1 << 31) - 1, 9
+    x = torch.full((1, 1, T, d), 2.0, dtype=torch.bfloat16, device="cuda")
+    assert B.qknorm_fwd(x, norm="rms", yq=x) is x
+    torch.cuda.synchronize()
+    flat = x.view(-1)
+    for i in range(0, flat.numel(), 1 << 32):
+        assert bool((flat[i:i + (1 << 32)] == 1.0).all()), i

@@ -20,6 +20,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxBlocks = 1024;  // of a backward: rows of partial weight gradients
+constexpr int kMaxGrid = 1 << 22;  // of any call: HIP takes fewer than 2^32 threads a launch
 
 struct QkPlan {
     int lpr;            // lanes of a row, a power of two
@@ -287,7 +288,8 @@ hipError_t launch_v(const QkArgs &a, hipStream_t s) {
         most = p.items[i] > most ? p.items[i] : most;
     }
     const long long blocks = (most * p.lpr + kThreads - 1) / kThreads;
-    p.blocks = (int)(BWD && blocks > kMaxBlocks ? kMaxBlocks : blocks);
+    const int limit = BWD ? kMaxBlocks : kMaxGrid;
+    p.blocks = (int)(blocks > limit ? limit : blocks);
     const dim3 grid((unsigned)p.blocks, a.H[1] > 0 ? 2 : 1);
     if (a.pairs)
         qk_kernel<IO, V, UPL, true, BWD><<<grid, kThreads, 0, s>>>(a, p);
