@@ -7,8 +7,8 @@
 // dw = sum over rows of u x r, dx = r (u w) - x r^3 (sum u w x) / n.
 //
 // Each row is read once and written once, nothing else is large: the pass is
-// bound by HBM (2 x 134 MB of 128 bfloat16 channels: 45 us, 6 TB/s with the inputs
-// partly in the cache, 58 us cold; gradients with rotation, 252 MB: 62 us, 4.1 TB/s).  A
+// bound by HBM (2 x 134 MB of 128 bfloat16 channels: 43 us, 6.2 TB/s with the inputs
+// partly in the cache, 58 us cold; gradients with rotation, 252 MB: 47 us, 5.4 TB/s).  A
 // row belongs to a few lanes of a wavefront; a lane holds both channels of its pairs, so that rotating costs no exchange, and the row's sums are
 // the only thing that crosses lanes.  The heads of a token are walked by the
 // same lanes, which keep the token's sines and cosines in registers.
@@ -275,9 +275,16 @@ hipError_t launch_v(const QkArgs &a, hipStream_t s) {
     p.units = p.rot_units + (a.d - 2 * a.nf + 2 * V - 1) / (2 * V);
     p.lpr = pow2_at_least((p.units + UPL - 1) / UPL);
     const long long tokens = (long long)a.B * a.T;
-    // all heads of a token to one group of lanes where the tokens fill the card
-    // (8 wavefronts a SIMD), else as many groups as that takes
-    const long long groups = 8ll * 1024 * 64 / p.lpr;
+    // Heads of a token for one group of lanes: all of them where the tokens make enough
+    // wavefronts, else fewer.  One wavefront a SIMD is enough for up to 48 MB: a token's turns are made
+    // once and the next head's row hides the loads (cold inputs, 8 wavefronts / 1: 4096 tokens of 16 + 4
+    // heads of 128, bfloat16 22 / 15 us, backward 38 / 25; 1024 tokens 9.2 / 7.7 and 20 / 15).  More are in
+    // flight from HBM with 8 (16384 tokens of 16 + 16 heads, no rotation: 58 / 76, backward 98 / 112;
+    // 2 x 8192 tokens of 32 + 8 heads of 64, float32, rotated 72 / 82, backward 105 / 128), with 2
+    // where bfloat16 rows are rotated (the same in bfloat16, 8 / 2 / 1: 42 / 39 / 48, backward 73 / 64 / 72).
+    const long long bytes = tokens * (a.H[0] + a.H[1]) * a.d * (long long)sizeof(IO);
+    const int waves = bytes <= 48ll << 20 ? 1 : a.nf > 0 && sizeof(IO) == 2 ? 2 : 8;
+    const long long groups = waves * 1024ll * 64 / p.lpr;
     const long long split = tokens >= groups ? 1 : (groups + tokens - 1) / tokens;
     long long most = 0;
     for (int i = 0; i < 2; ++i) {
