@@ -289,6 +289,33 @@ def test_gradients_over_segments_of_a_padded_batch(io):
     check(d, io, lengths, scale=0.2, what=f"{io} padded segments")
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_segments_without_a_state(io):
+    """Segments where no state is given or asked for: fewer parts of the states between
+    them in bfloat16."""
+    d = make(io, 1, 1, 2, 640, 64, 96, seed=16, state=False, decay=0.01)
+    g = cu(d)
+    a = [g[x] for x in ("q", "k", "v", "g", "beta")]
+    o = B.deltarule_fwd(*a, scale=0.2, return_state=False)
+    got = B.deltarule_bwd(*a, g["do"], scale=0.2)
+    torch.cuda.synchronize()
+    D.check(D.sweep(d, None, 0.2), {"o": o, **dict(zip(GRADS, got))}, io, f"{io} segments, no state")
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_extreme_gates_over_segments(io):
+    """Decays of 0 and 1 and reflections (strength 2 and a unit key) in sequences of segments,
+    one that forgets everything in each segment and one that forgets nothing."""
+    d = make(io, 1, 4, 4, 600, 32, 64, seed=17, decay=0.02)
+    d["g"][0, 0] = 0.0
+    d["beta"][0, 0] = 2.0
+    d["g"][0, 1, ::60] = -INF
+    d["g"][0, 2, 300:] = -1e30
+    d["beta"][0, 3] = 0.0
+    got = check(d, io, scale=0.3, what=f"{io} extreme gates, segments")
+    assert bool((got[5][(d["g"] == -INF).cuda()] == 0).all())
+
+
 def test_gradients_are_the_differences():
     """float32 gradients against differences of the forward's own results: a change of
     2^-7 in a random direction, twice, leaves third-order terms, 2^-14 of the loss's
