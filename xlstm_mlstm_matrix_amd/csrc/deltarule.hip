@@ -888,24 +888,33 @@ __device__ __forceinline__ void scan(const DeltaArgs &a, const float *start, Seg
         S[1][r * kScanLd + c] = 0.0f;
         if (!REV && r < dk) sg.state[((size_t)bh * sg.count * dk + r) * dv + col0 + c] = x;
     }
-    // part p of M's columns (all of them up to 128, else 128 each) of a step, and b
+    // part p of M's columns (all of them up to 128, else 128 each) of a step, and b; one lane
+    // address each, the rest of it the same for the wavefront (addresses in pairs of registers
+    // for every load spill: one head of 256 x 512, 32 segments, backwards 511 us, so 236)
+    const unsigned vm = (unsigned)((REV ? 4 * g4 * ld + row + l16 : (row + l16) * ld + 4 * g4) * 4);
+    const unsigned va = (unsigned)(((row + 4 * g4) * lda + l16) * 4);
     auto fetch = [&](int step, int p, f32x4 *m, f32x4 &add) {
         const int s = max(0, min(nseg - 1, REV ? nseg - 1 - step : step));
-        const float *M = fwd.local + ((size_t)bh * fwd.count + s) * dk * ld + dv;
-        const float *A = (REV ? sg.local + ((size_t)bh * sg.count + s) * dk * dv : M - dv) + col0 + l16;
+        const float *M = fwd.local + ((size_t)bh * fwd.count + s) * dk * ld;  // b's columns first
+        const float *A = REV ? sg.local + ((size_t)bh * sg.count + s) * dk * dv : M;
+        const auto ms = __builtin_amdgcn_make_buffer_rsrc((void *)M, 0, dk * ld * 4, kBuf);
+        const auto as = __builtin_amdgcn_make_buffer_rsrc((void *)A, 0, dk * lda * 4, kBuf);
         if (p == 0)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) add[r] = A[(row + 4 * g4 + r) * lda];
+            for (int r = 0; r < 4; ++r)
+                add[r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(as, va, (r * lda + col0) * 4, 0));
 #pragma unroll
         for (int k = 0; k < PK; ++k) {
-            const int k0 = min(16 * (p * PK + k), dk - 16) + 4 * g4;
+            const int k0 = min(16 * (p * PK + k), dk - 16);
             if constexpr (REV) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) m[k][e] = M[(k0 + e) * ld + row + l16];
+                for (int e = 0; e < 4; ++e)
+                    m[k][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ms, vm, ((k0 + e) * ld + dv) * 4, 0));
             } else {
-                m[k] = *(const f32x4 *)(M + (row + l16) * ld + k0);
+                m[k] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(ms, vm, (k0 + dv) * 4, 0));
             }
         }
+        __builtin_amdgcn_sched_barrier(0);  // the loads stay in front of the products
     };
     f32x4 acc[2];
     auto multiply = [&](const float *from, int p, const f32x4 *m) {
