@@ -1127,7 +1127,11 @@ __global__ __launch_bounds__(64 * NW, SHARED && NW == 4 ? 1 : 2) void grad_kerne
     auto put_rows = [&](int t, int x, f32x4 q, f32x4 k) {
         const int id = wave * RTW + x, c = 32 * (id >> 1) + 8 * (lane0 >> 4) + 4 * (id & 1), i = 16 * t + (lane0 & 15);
         if (i < rows && c < dk) {
-            const float u[4] = {q[0], q[1], q[2], q[3]}, v[4] = {k[0], k[1], k[2], k[3]};
+            // rows behind the sequence's length are zeros, also where their zeros met a NaN of its own
+            const bool own = i < n;
+            float u[4], v[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) u[r] = own ? q[r] : 0.0f, v[r] = own ? k[r] : 0.0f;
             store4(dqg + i * a.sdq.s2 + c, u);
             store4(dkg + i * a.sdk.s2 + c, v);
         }
