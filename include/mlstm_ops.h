@@ -305,7 +305,8 @@ typedef enum {
  * 1 <= d <= 512 (MLSTM_ERR_UNSUPPORTED above); B * T * (H + Hk) below 2^31
  * (MLSTM_ERR_SHAPE).  yq may be exactly q (the same pointer and strides) and yk
  * exactly k.  Every row is computed, whatever the lengths of the sequences; a row
- * reaches no other's result.  The sum of a row's squares is finite in float32.
+ * reaches no other's result.  With a norm the sum of a row's squares is finite in
+ * float32, and at least 2^-100 if eps is 0; so are the sums of x times its gradient.
  *
  * Precision.  float32, the angle in 64 bits and reduced to a turn before its sine
  * is taken; results rounded once.
