@@ -287,7 +287,8 @@ typedef enum {
  *   z = weight x / norm(x),   (y_a, y_b) = A (z_a cos w - z_b sin w, z_b cos w + z_a sin w)
  *
  * with w = positions[b, t] inv_freq[i] for pair i (a, b) of the first 2 n_freq
- * channels; the other channels are z.
+ * channels; the other channels are z (without a norm and weights the input's own
+ * bits, a NaN's aside, and so are their gradients).
  *
  *  q, yq        [B, H, T, d] io dtype;  k, yk  [B, Hk, T, d] io dtype, both NULL for
  *               queries alone (Hk is ignored then)

@@ -1,5 +1,6 @@
 """Rows of queries and keys at the ends of what qknorm_fwd and qknorm_bwd take: magnitudes far
-from one.  References and bounds as in test_gpu_qknorm.py."""
+from one, infinities and NaN where the definition copies a channel.  References and bounds
+as in test_gpu_qknorm.py."""
 import pytest
 import torch
 
@@ -30,3 +31,35 @@ def test_rows_of_any_magnitude(io, norm, shift, eps, shape, n):
     torch.cuda.synchronize()
     for name, x, (ref, tol) in zip(("yq", "yk", "dq", "dk", "dwq", "dwk"), got, y + dx + dw):
         close(x, ref, tol, "f32" if name[:2] == "dw" else io, f"{io} {norm} 2^{shift} {name}")
+
+
+def bits(t):
+    return t.contiguous().view(torch.int32 if t.dtype == torch.float32 else torch.int16)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("layout", ["half", "pairs"])
+@pytest.mark.parametrize("d,n", [(64, 16), (64, 0), (40, 3), (33, 8), (512, 8)])
+def test_channels_that_are_not_rotated_are_copied(io, layout, d, n):
+    """Without a norm and weights a channel behind the rotated ones is the input's, bit for
+    bit, whatever its neighbours hold, and so is its gradient."""
+    c = make(io, 2, 11, 3, 2, d, n, "none", 50, seed=d + n, weight=False)
+    odd = (float("inf"), -float("inf"), float("nan"), -0.0, 3e38)
+    g = cu(c)
+    plain = {}
+    for name in ("q", "k", "dyq", "dyk"):
+        x = g[name].clone()
+        plain[name] = x.clone()
+        for i, value in enumerate(odd * 3):
+            x[i % 2, i % x.shape[1], i % 11, 2 * n + (5 * i) % (d - 2 * n)] = value
+        g[name] = x
+    kw = dict(norm="none", inv_freq=g["f"], positions=g["pos"], layout=layout)
+    got = B.qknorm_fwd(g["q"], g["k"], **kw) + B.qknorm_bwd(g["q"], g["k"], g["dyq"], g["dyk"], weight_grad=False, **kw)[:2]
+    ref = B.qknorm_fwd(plain["q"], plain["k"], **kw) \
+        + B.qknorm_bwd(plain["q"], plain["k"], plain["dyq"], plain["dyk"], weight_grad=False, **kw)[:2]
+    torch.cuda.synchronize()
+    for name, x, r in zip(("q", "k", "dyq", "dyk"), got, ref):
+        a, b = x[..., 2 * n:], g[name][..., 2 * n:]
+        same = (bits(a) == bits(b)) | (a.isnan() & b.isnan()).contiguous()
+        assert bool(same.all()), (name, int((~same).sum()))
+        assert torch.equal(x[..., :2 * n], r[..., :2 * n]), name

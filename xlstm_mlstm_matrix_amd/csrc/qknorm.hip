@@ -103,7 +103,8 @@ __global__ __launch_bounds__(kThreads) void qk_kernel(QkArgs a, QkPlan p) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) ok[i][k] = u < p.units && off[i][k] < d;
     }
-    // the pair (ia(j), ib(j)) of a unit's W channels
+    // the pair (ia(j), ib(j)) of a unit's W channels.  Channels that are not rotated are left alone, not
+    // turned by 0: 0 times an infinite neighbour is a NaN.
     const auto ia = [](int j) { return PAIRS ? 2 * j : j; };
     const auto ib = [](int j) { return PAIRS ? 2 * j + 1 : V + j; };
     const int ti = blockIdx.y;
@@ -169,8 +170,8 @@ __global__ __launch_bounds__(kThreads) void qk_kernel(QkArgs a, QkPlan p) {
 #pragma unroll
                         for (int j = 0; j < V; ++j) {
                             const float ya = g[i][ia(j)], yb = g[i][ib(j)];
-                            g[i][ia(j)] = c[i][j] * ya + s[i][j] * yb;
-                            g[i][ib(j)] = c[i][j] * yb - s[i][j] * ya;
+                            g[i][ia(j)] = rot[i] ? c[i][j] * ya + s[i][j] * yb : ya;
+                            g[i][ib(j)] = rot[i] ? c[i][j] * yb - s[i][j] * ya : yb;
                         }
                 }
 #pragma unroll
@@ -190,7 +191,7 @@ __global__ __launch_bounds__(kThreads) void qk_kernel(QkArgs a, QkPlan p) {
                 }
                 // factors r one by one beside their x or u: r^3 alone leaves float32's range for rows
                 // of 10^13 or of 10^-13
-                const float back = BWD && a.norm != 0 ? dot * r / count : 0.0f;
+                const float back = dot * r / count;
 #pragma unroll
                 for (int i = 0; i < UPL; ++i) {
                     if constexpr (BWD) {
@@ -198,7 +199,8 @@ __global__ __launch_bounds__(kThreads) void qk_kernel(QkArgs a, QkPlan p) {
                         for (int j = 0; j < W; ++j) {
                             const float z = x[i][j] * r;
                             dw[i][j] += g[i][j] * z;
-                            x[i][j] = r * (g[i][j] * w[i][j] - z * back);
+                            const float u = g[i][j] * w[i][j];
+                            x[i][j] = a.norm != 0 ? r * (u - z * back) : u;
                         }
                     } else {
 #pragma unroll
@@ -206,8 +208,8 @@ __global__ __launch_bounds__(kThreads) void qk_kernel(QkArgs a, QkPlan p) {
 #pragma unroll
                         for (int j = 0; j < V; ++j) {
                             const float za = x[i][ia(j)], zb = x[i][ib(j)];
-                            x[i][ia(j)] = za * c[i][j] - zb * s[i][j];
-                            x[i][ib(j)] = zb * c[i][j] + za * s[i][j];
+                            x[i][ia(j)] = rot[i] ? za * c[i][j] - zb * s[i][j] : za;
+                            x[i][ib(j)] = rot[i] ? zb * c[i][j] + za * s[i][j] : zb;
                         }
                     }
 #pragma unroll
