@@ -359,10 +359,9 @@ struct Cfg {
     static constexpr int REC = Rec<IO, W>::BYTES / (int)sizeof(IO);  // elements of a record
     static constexpr int ELEMS = L * TROW + REC, VELEMS = VOWN ? L * 16 * NCT : 8;
     static constexpr size_t TILE = (size_t)ELEMS * sizeof(IO), VTILE = VOWN ? (size_t)L * BV * sizeof(IO) : 0;
-    static constexpr int NBUF = 2 * TILE + VTILE <= kLds ? 2 : 1;
-    static constexpr int PER_CU = 2 * (NBUF * TILE + VTILE) <= kLds && NW == 4 ? 2 : 1;  // workgroups of a compute unit
+    static constexpr int PER_CU = 2 * (2 * TILE + VTILE) <= kLds && NW == 4 ? 2 : 1;  // workgroups of a compute unit
     static_assert(QG >= 8, "swizzle");
-    static_assert(TILE + VTILE <= kLds, "LDS");
+    static_assert(2 * TILE + VTILE <= kLds, "two chunks' tiles in LDS");
 };
 
 // acc + the products of two operands' parts whose joint order stays below ORD
@@ -393,7 +392,7 @@ __device__ __forceinline__ void walk(const DeltaArgs &a, const char *rec, WalkOu
     using C = Cfg<IO, DKP, NCT, NW, W, SO>;
     using R = Rec<IO, W>;
     using Frag = typename Types<IO>::Frag;
-    constexpr int NAT = C::NAT, NKS = C::NKS, QG = C::QG, VG = C::VG, BV = C::BV, NBUF = C::NBUF;
+    constexpr int NAT = C::NAT, NKS = C::NKS, QG = C::QG, VG = C::VG, BV = C::BV;
     constexpr int OP = Types<IO>::XPARTS;  // parts of what leads to the output
     constexpr int ES = (int)sizeof(IO);
     constexpr bool OUT = W == FORWARD && !SO;  // makes o
@@ -533,11 +532,7 @@ __device__ __forceinline__ void walk(const DeltaArgs &a, const char *rec, WalkOu
     constexpr int NST = SO ? 0 : W == FORWARD ? 2 * (ES == 4 ? NCT : 1) : 8 * NCT < 15 ? 8 * NCT : 15;
     constexpr int STEP = W == BACK ? -1 : 1, PER = kBlock<IO> / L;  // chunks of a block
     auto body = [&](IO *cur, IO *next, int c, bool first) {
-        if (NBUF == 1) {
-            __syncthreads();
-            load(cur, c);
-            wait_vm<0>();
-        } else if (first) {
+        if (first) {
             wait_vm<0>();
         } else {
             wait_vm<NST>();  // this wavefront's copies have landed
@@ -570,7 +565,7 @@ __device__ __forceinline__ void walk(const DeltaArgs &a, const char *rec, WalkOu
             k[0][t] = rows.get(Ks, t, 0);
         }
         __builtin_amdgcn_sched_barrier(0);
-        if (NBUF == 2) load(next, c + STEP);
+        load(next, c + STEP);
         parts(0);
         __builtin_amdgcn_sched_barrier(0);
         // the state is kept: X[dk][dv] of the accumulators, transposed by the unit matrix
@@ -771,12 +766,12 @@ __device__ __forceinline__ void walk(const DeltaArgs &a, const char *rec, WalkOu
     };
     const int nloc = c1 - c0, first = W == BACK ? c1 - 1 : c0;
     if (nloc > 0) {
-        if (NBUF == 2) load(tile0, first);
+        load(tile0, first);
         if constexpr (C::VOWN) load_v(first);
     }
     for (int i = 0; i < nloc; i += 2) {
         body(tile0, tile1, first + STEP * i, i == 0);
-        if (i + 1 < nloc) body(NBUF == 2 ? tile1 : tile0, tile0, first + STEP * (i + 1), false);
+        if (i + 1 < nloc) body(tile1, tile0, first + STEP * (i + 1), false);
     }
     wait_vm<0>();  // no copy may still be on its way into LDS when the workgroup ends
 
@@ -823,7 +818,7 @@ __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW, FORWARD, SO>::PER_C
                                                                                                             Segs sg) {
     using C = Cfg<IO, DKP, NCT, NW, FORWARD, SO>;
     __shared__ __attribute__((aligned(16))) IO tile0[C::ELEMS];
-    __shared__ __attribute__((aligned(16))) IO tile1[C::NBUF == 2 ? C::ELEMS : 16];
+    __shared__ __attribute__((aligned(16))) IO tile1[C::ELEMS];
     __shared__ __attribute__((aligned(16))) IO vtiles[NW * C::VELEMS];
     walk<IO, DKP, NCT, NW, SP, FORWARD, SO>(a, rec, WalkOut{}, sg, blockIdx.x, gridDim.x, tile0, tile1, vtiles);
 }
@@ -845,9 +840,9 @@ template <typename IO, int DKP, int NCT, int NW, bool SO>
 __global__ __launch_bounds__(64 * NW, (Cfg<IO, DKP, NCT, NW, BACK, SO>::PER_CU * NW / 4)) void back_kernel(BackArgs w) {
     using C = Cfg<IO, DKP, NCT, NW, BACK, SO>;
     using S = Cfg<IO, DKP, NCT, NW, STATES, SO>;
-    constexpr int N1 = C::NBUF == 2 ? C::ELEMS : 16, N2 = S::NBUF == 2 ? S::ELEMS : 16, SP = sizeof(IO) == 2 ? 3 : 1;
-    __shared__ __attribute__((aligned(16))) IO tile0[C::ELEMS > S::ELEMS ? C::ELEMS : S::ELEMS];
-    __shared__ __attribute__((aligned(16))) IO tile1[N1 > N2 ? N1 : N2];
+    constexpr int SP = sizeof(IO) == 2 ? 3 : 1, ELEMS = C::ELEMS > S::ELEMS ? C::ELEMS : S::ELEMS;
+    __shared__ __attribute__((aligned(16))) IO tile0[ELEMS];
+    __shared__ __attribute__((aligned(16))) IO tile1[ELEMS];
     __shared__ __attribute__((aligned(16))) IO vtiles[NW * C::VELEMS];
     if ((int)blockIdx.x < w.nback) {
         walk<IO, DKP, NCT, NW, SP, BACK, SO>(w.a, w.rec_back, w.to_back, w.sg_back, blockIdx.x, w.nback, tile0, tile1, vtiles);
@@ -1669,8 +1664,7 @@ hipError_t launch_bwd_t(const DeltaArgs &a, hipStream_t s) {
 
 }  // namespace
 
-size_t deltarule_workspace_floats(int B, int Hk, int H, int T, int dk, int dv, int io_bf16, int backward) {
-    (void)Hk;
+size_t deltarule_workspace_floats(int B, int H, int T, int dk, int dv, int io_bf16, int backward) {
     const size_t n = (size_t)B * H;
     if (!backward) return fwd_ws(n, T, dk, dv, io_bf16).total;
     return (io_bf16 ? bwd_ws<bf16>(n, T, dk, dv).total : bwd_ws<float>(n, T, dk, dv).total) / 4;

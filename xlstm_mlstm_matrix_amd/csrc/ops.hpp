@@ -71,8 +71,8 @@ struct DeltaArgs {
     float *dg, *db, *dS0;
     Strides sdo, sdq, sdk, sdv, sdg, sdb;
 };
-// 0 when the workspace would not fit the limit
-size_t deltarule_workspace_floats(int B, int Hk, int H, int T, int dk, int dv, int io_bf16, int backward);
+// the caller refuses sizes past its limit
+size_t deltarule_workspace_floats(int B, int H, int T, int dk, int dv, int io_bf16, int backward);
 hipError_t launch_deltarule_fwd(const DeltaArgs &a, int io_bf16, hipStream_t s);
 hipError_t launch_deltarule_bwd(const DeltaArgs &a, int io_bf16, hipStream_t s);
 

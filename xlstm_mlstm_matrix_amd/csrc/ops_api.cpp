@@ -285,7 +285,7 @@ mlstm_status_t delta_dims(int B, int Hk, int H, int T, int dk, int dv, mlstm_dty
         // 2^40 bytes.  A 32-token chunk of a head has at least one KB and below 2^24 bytes of it, so
         // the sizes of what passes here do not overflow.
         if (*cells * (((size_t)T + 31) / 32) > (size_t)1 << 30) return MLSTM_ERR_SHAPE;
-        const size_t f = deltarule_workspace_floats(B, Hk, H, T, dk, dv, io == MLSTM_BF16, backward);
+        const size_t f = deltarule_workspace_floats(B, H, T, dk, dv, io == MLSTM_BF16, backward);
         if (f > ((size_t)1 << 38)) return MLSTM_ERR_SHAPE;
         *need = 4 * f;
     }
