@@ -159,8 +159,8 @@ mlstm_status_t mlstm_linattn_bwd(const void *q, const void *k, const void *v,
  * outputs of its own 32-token chunk and everything after it.
  *
  * Precision.  As for mlstm_linattn_fwd: float32 products and sums for float32;
- * for bfloat16 o is rounded once, and a state that is handed out is exact to
- * float32 sums.
+ * for bfloat16 o is rounded once, the scores, what is written and the read-out's copy of
+ * the state keep 16 bits each, and a state that is handed out is exact to float32 sums.
  */
 mlstm_status_t mlstm_deltarule_fwd_workspace_size(int B, int Hk, int H, int T, int d_qk, int d_v,
                                                   mlstm_dtype_t io, size_t *bytes);
@@ -199,7 +199,8 @@ mlstm_status_t mlstm_deltarule_step(const void *q, const void *k, const void *v,
  *              NULL S0 too)
  *  strides     11: of q, k, v, log_decay, beta, d_o, dq, dk, dv, dlog_decay, dbeta
  *              over (b, h, t), or NULL
- * Everything else as for mlstm_deltarule_fwd.
+ * Everything else as for mlstm_deltarule_fwd, the precision too; dlog_decay, dbeta and dS0
+ * are exact to float32 sums in bfloat16 calls as well.
  */
 mlstm_status_t mlstm_deltarule_bwd_workspace_size(int B, int Hk, int H, int T, int d_qk, int d_v,
                                                   mlstm_dtype_t io, size_t *bytes);
@@ -324,7 +325,7 @@ mlstm_status_t mlstm_qknorm_fwd(const void *q, const void *k, const float *q_wei
  *
  *  dq, dk               as q and k, io dtype; dq may be exactly dyq and dk exactly dyk
  *  dq_weight, dk_weight [d] float32, written, each NULL when not wanted; summed in
- *                       an order that the sizes fix
+ *                       an order that the sizes, strides and alignment fix
  *  strides              6: of q, k, dyq, dyk, dq, dk, or NULL
  *  workspace            at least mlstm_qknorm_bwd_workspace_size bytes, not needed if
  *                       both weight gradients are NULL

@@ -23,9 +23,11 @@
 //
 // Roundings (bfloat16 I/O), as in linattn.hip: the copy of S that meets Q has two
 // parts (8 + 8 bits), and so have P and the U that meets it: each is off by 2^-16
-// where the output's own rounding is off by 2^-8.  Where the state is handed out,
-// all that leads to it has three parts (24 bits): the copy of S that meets K, T', its
-// right side, the update's e^{G_L - G} U; else two.  S itself, decays and sums
+// at most where the output's own rounding is off by 2^-8.  Of two split operands the
+// product of the last parts is left out: of P U 2^-14 at most, 2^-17 on average.  Where the
+// state is handed out, all that leads to it has three parts (24 bits, products of 2^-21 at
+// most left out): the copy of S that meets K, T', its right side, the update's
+// e^{G_L - G} U; else two.  S itself, decays and sums
 // are float32.  float32 I/O runs on the float32 MFMA without further rounding.
 #include <type_traits>
 
@@ -76,7 +78,7 @@ __device__ __forceinline__ float gate_log2(float g) {
 // 8 floats as a sum of PARTS bfloat16 operands.  All but the last part are cut, not
 // rounded: the upper halves of two floats by one byte permutation, the rest by a mask
 // and a subtraction.  Three parts hold a float's 24 bits, so the third is cut too and the
-// sum is exact; of two the second is rounded, 2^-17.  (A conversion is half as fast as those, and
+// sum is exact; of two the second is rounded, 2^-16 at most.  (A conversion is half as fast as those, and
 // v_dot2c_f32_bf16 in place of the subtraction does not run beside the MFMA.)
 template <int PARTS>
 __device__ __forceinline__ void split8(const float *x, bf16x8 *f) {
@@ -383,7 +385,8 @@ __device__ __forceinline__ f32x4 mfma_parts(const Frag *x, const Frag *y, f32x4 
 //
 // Bound by vector and matrix instructions that one or two wavefronts a SIMD overlap little (d_qk = 128,
 // three parts: 82 MFMA and some 380 vector instructions a chunk and wavefront, half of these the
-// split of S): 64 heads of 256 x 512, 4096 tokens, bfloat16 640 us (5 us a chunk), 128 x 128
+// split of S): 64 heads of 256 x 512, 4096 tokens, bfloat16 626 us (5 us a chunk; from one call to the
+// next 572 to 783, as the clock moves under load), 128 x 128
 // 1.75 us a chunk.  Half of the rows for each of two wavefronts, their sums joined in LDS, was
 // slower (1.75 -> 2.05 us): the small products are then done twice.
 template <typename IO, int DKP, int NCT, int NW, int SP, Walk W, bool SO>
@@ -984,7 +987,8 @@ __global__ __launch_bounds__(4 * DKP) void scan_kernel(DeltaArgs a, const float 
 // starts anew at each block, so that its roundings do not add up over a sequence.
 //
 // Roundings (bfloat16 I/O): dq and dk are rounded once at the end, and what makes them
-// has two parts, as in the forward; dbeta and dlog_decay are float32, and so what makes
+// has two parts, as in the forward (of dV S^T and E2 the first two of three cut parts' products
+// leave out 2^-13 at most of their terms); dbeta and dlog_decay are float32, and so what makes
 // them (X and dU themselves, three parts of S, D and X) has 24 bits.
 //
 // A workgroup has a block of kBlock tokens of one head of q and k and walks the
@@ -1483,14 +1487,21 @@ __global__ __launch_bounds__(64 * NW, SHARED && NW == 4 ? 1 : 2) void grad_kerne
 // ---- launches
 
 // Columns of a workgroup, and segments.  128 columns where that gives every compute unit a
-// workgroup, else 64 (4096 tokens, bfloat16, 64 / 128: 64 heads of 128 x 128 245 / 376 us, 192 heads
-// 460 / 464, 64 heads of 256 x 512 803 / 653; 256 heads of 128 x 128, 2048 tokens 284 / 273).
+// workgroup, else 64 (64 / 128 columns, bfloat16: 4096 tokens, 64 heads of 128 x 128 245 / 376 us, 192 heads
+// 460 / 464, 64 heads of 256 x 512 867 / 638, backward 3663 / 3187; 256 heads of 128 x 128, 2048 tokens
+// 283 / 292, 512 heads, 1024 tokens 290 / 269; 128 heads of 256 x 256, 1024 tokens 246 / 188, backward 1039 / 891;
+// float32, 256 heads of 128 x 128, 1024 tokens 361 / 330, backward 1255 / 1212).  It counts blocks and not how
+// full the last one is, and the backward's two walks as one, so it misses some calls: 256 heads of
+// 64 x 64, 2048 tokens 165 / 221 (float32, 1024 tokens 147 / 200, backward 447 / 544), 256 heads of 128 x 192, 1024
+// tokens 194 / 210; 32 heads of 256 x 512 backward, which stay with 64, 1868 / 1682.
 //
 // Segments where up to a quarter of the units would have a workgroup: they cost a second
 // walk, of twice the columns (d_v and d_qk of them) where d_qk is as large as d_v, and the scan's
 // steps, each longer than a chunk; so as many as make a workgroup a unit, and as
 // sqrt(4 chunks), of at least 4 chunks.  Without / with, 4096 tokens of 128 x 128: 32 heads (64
-// workgroups) 221 / 166 us, 48 heads 233 / 270; 8 heads of 256 x 512 (64) 354 / 248, 16 heads 363 / 425.
+// workgroups) 221 / 166 us, 48 heads 233 / 270; 8 heads of 256 x 512 (64) 354 / 248, 16 heads 363 / 425.  Where
+// d_qk is the larger the first walk has more columns than d_v counts: 32 heads of 256 x 64 381 / 313, but 64
+// heads (64 workgroups) 447 / 520.
 // The backward's two walks run side by side and count both: 16 heads of 8192 tokens (2 x 32) 743 / 500 us,
 // 32 heads of 4096 (2 x 64) 494 / 504, 8 heads of 256 x 512 (2 x 64) 719 / 840.
 struct Plan {

@@ -69,7 +69,9 @@ __device__ __forceinline__ void store_row(IO *p, bool ok, const float *x) {
 }
 
 // Cosine and sine of position * freq.  The angle is a double product, good to
-// 2^-52 of itself, and only its distance from a whole turn goes on in float32.
+// 2^-52 of itself, and only its distance from a whole turn goes on in float32: half a turn
+// to 2^-25, 1e-7 radians, as much as the sine's own rounding (sines of the double
+// angle would leave outputs at 6.4e-8 of a float32 row where these are 7.4e-8).
 __device__ __forceinline__ void turn(int pos, float freq, float amp, float &c, float &s) {
     const double t = (double)pos * (double)freq * 0.15915494309189533577;  // 1 / (2 pi)
     const float half = (float)(2.0 * (t - rint(t)));
@@ -283,10 +285,11 @@ hipError_t launch_v(const QkArgs &a, hipStream_t s) {
     // Heads of a token for one group of lanes: all of them where the tokens make enough
     // wavefronts, else fewer.  One wavefront a SIMD is enough for up to 48 MB: a token's turns are made
     // once and the next head's row hides the loads (cold inputs, 8 wavefronts / 1: 4096 tokens of 16 + 4
-    // heads of 128, bfloat16 22 / 15 us, backward 38 / 25; 1024 tokens 9.2 / 7.7 and 20 / 15).  More are in
-    // flight from HBM with 8 (16384 tokens of 16 + 16 heads, no rotation: 58 / 76, backward 98 / 112;
-    // 2 x 8192 tokens of 32 + 8 heads of 64, float32, rotated 72 / 82, backward 105 / 128), with 2
-    // where bfloat16 rows are rotated (the same in bfloat16, 8 / 2 / 1: 42 / 39 / 48, backward 73 / 64 / 72).
+    // heads of 128, bfloat16, 21 MB, 22 / 15 us, backward 38 / 25; 1024 tokens 9.2 / 7.7 and 20 / 15).  More are in
+    // flight from HBM with 8 (16384 tokens of 16 + 16 heads, 134 MB, no rotation: 58 / 76, backward 98 / 112;
+    // 2 x 8192 tokens of 32 + 8 heads of 64, float32, 168 MB, rotated 72 / 82, backward 105 / 128), with 2
+    // where bfloat16 rows are rotated (the same in bfloat16, 84 MB, 8 / 2 / 1: 42 / 39 / 48, backward
+    // 73 / 64 / 72).  48 MB lies between what was measured.
     const long long bytes = tokens * (a.H[0] + a.H[1]) * a.d * (long long)sizeof(IO);
     const int waves = bytes <= 48ll << 20 ? 1 : a.nf > 0 && sizeof(IO) == 2 ? 2 : 8;
     const long long groups = waves * 1024ll * 64 / p.lpr;
@@ -315,7 +318,9 @@ hipError_t launch_v(const QkArgs &a, hipStream_t s) {
 template <typename IO, bool BWD>
 hipError_t launch_io(const QkArgs &a, hipStream_t s) {
     constexpr int V = 16 / (int)sizeof(IO);
-    // whole vectors: pairs and the rest begin and end on 16 bytes, and so do all rows
+    // whole vectors: pairs and the rest begin and end on 16 bytes, and so do all rows; else single
+    // channels (bfloat16, 4 x 4096 tokens of 16 + 4 heads: 96 channels with 36 pairs 49 us, 2.6 TB/s, backward
+    // 76; 128 with 64 pairs by vectors 35, 4.8 TB/s, backward 56)
     bool vec = a.d % V == 0 && a.nf % V == 0;
     for (int i = 0; i < 2; ++i) {
         if (a.H[i] == 0) continue;
