@@ -769,8 +769,10 @@ __global__ __launch_bounds__(NTS) void bwd_b_kernel(BwdArgs a) {
                     const f32x4 gv{gacc[x][q][0][v], gacc[x][q][1][v], gacc[x][q][2][v], gacc[x][q][3][v]};
                     buf_st4(gv, g0r, off);
                     const f32x4 cv = buf_ld4(c0r, off);
+                    // lanes past the block's columns have taken theirs from LDS that nothing has
+                    // written: they are left out (0 times a NaN there would be one)
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) part = fmaf(gv[y], cv[y], part);
+                    for (int y = 0; y < 4; ++y) part = soff[x][q] != kFar ? fmaf(gv[y], cv[y], part) : part;
                 }
     }
     if (blk == 0 && a.gn0)
