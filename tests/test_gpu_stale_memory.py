@@ -85,6 +85,28 @@ def test_cell(io, dk, dv, state):
     check(lambda: B.step(*first, *st, inplace=False), f"{io} {dk} x {dv} step state {state}")
 
 
+@pytest.mark.parametrize("dk,dv", [(16, 48), (64, 64), (80, 112), (128, 128), (240, 400), (256, 512)], ids=str)
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("variant", ["fused", "segscan"])
+def test_cell_schedules(io, dk, dv, variant):
+    """Both schedules of the forward, every chunk length that a size takes."""
+    r = rnd(dk + dv + 1)
+    H, T = 3, 600
+    q, k = (r(1, H, T, dk, dt=io, std=dk ** -0.5) for _ in range(2))
+    v, o = (r(1, H, T, dv, dt=io) for _ in range(2))
+    i, f = r(1, H, T), -r(1, H, T).abs()
+    st, ran = (r(1, H, dk, dv), r(1, H, dk), r(1, H)), 0
+    for chunk in (16, 32, 64, 128, 256):
+        try:
+            B.workspace_size(1, H, T, dk, dv, chunk, int(io == "bf16"), variant)
+        except B.MlstmError:
+            continue
+        check(lambda: B.fwd_chunkwise(q, k, v, i, f, o, *st, chunk=chunk, variant=variant),
+              f"{io} {dk} x {dv} {variant} {chunk}")
+        ran += 1
+    assert ran
+
+
 @pytest.mark.parametrize("pairs", [1, 2, 7])
 @pytest.mark.parametrize("dk,dv", [(16, 16), (16, 80), (64, 48), (48, 144), (256, 208)], ids=str)
 @pytest.mark.parametrize("io", ["f32", "bf16"])
@@ -146,13 +168,18 @@ def test_norms(io, d, n):
                   f"{io} {d} groupnorm_bwd of {T} {over}")
 
 
-@pytest.mark.parametrize("name", ["layer_small"])
-def test_layer(name):
-    d = {k: v.cuda() if v is not None else None for k, v in I.gen_layer(I.layer_workload(name)).items()}
+@pytest.mark.parametrize("override", [dict(name="layer_small"), dict(name="layer_small", d_qk=48, d_v=80, d_model=96),
+                                      dict(name="layer_7b_bf16", B=1, T=150, d_model=512, H=2),
+                                      dict(name="layer_7b_bf16", B=2, T=70, d_model=192, H=3, d_qk=48, d_v=112)], ids=str)
+def test_layer(override):
+    d = {k: v.cuda() if v is not None else None for k, v in I.gen_layer(I.layer_workload(**override)).items()}
     names = ("x", "W_q", "W_k", "W_v", "W_o", "W_i", "W_f", "b_q", "b_k", "b_v", "b_o", "b_i", "b_f", "C0", "n0", "m0")
-    check(lambda: B.layer_fwd(*(d[n] for n in names), chunk=32), name)
+    for chunk in (32, 64):
+        check(lambda: B.layer_fwd(*(d[n] for n in names), chunk=chunk), f"{override} {chunk}")
 
 
-def test_slstm():
-    d = {k: v.cuda() if v is not None else None for k, v in I.gen_slstm(I.slstm_workload("slstm_small", T=40)).items()}
-    check(lambda: B.slstm_fwd(d["gx"], d["R"], d["c0"], d["n0"], d["m0"], d["h0"]), "slstm")
+@pytest.mark.parametrize("override", [dict(name="slstm_small", T=40), dict(name="slstm_bf16", T=40, B=3, H=2),
+                                      dict(name="slstm_bf16", T=9, B=1, H=1, d=48)], ids=str)
+def test_slstm(override):
+    d = {k: v.cuda() if v is not None else None for k, v in I.gen_slstm(I.slstm_workload(**override)).items()}
+    check(lambda: B.slstm_fwd(d["gx"], d["R"], d["c0"], d["n0"], d["m0"], d["h0"]), str(override))
