@@ -308,7 +308,7 @@ typedef enum {
  * (MLSTM_ERR_SHAPE).  yq may be exactly q (the same pointer and strides) and yk
  * exactly k.  Every row is computed, whatever the lengths of the sequences; a row
  * reaches no other's result.  With a norm the sum of a row's squares is finite in
- * float32, and at least 2^-100 if eps is 0; so are the sums of x times its gradient.
+ * float32, and at least 2^-100 if eps is 0; the sum of x times its gradient is finite too.
  *
  * Precision.  float32, the angle in 64 bits and reduced to a turn before its sine
  * is taken; results rounded once.
